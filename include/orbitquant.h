@@ -87,6 +87,16 @@ extern "C" {
                                            H are applied.  Same outputs as the unpermuted rows
                                            without this flag */
 
+/* microscaled element formats (the value is the element's bits) */
+#define OQ_MX_FP4 4 /* e2m1: +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} */
+#define OQ_MX_FP8 8 /* e4m3: largest 448, one NaN pattern per sign, no infinity */
+
+/* rotary embedding flags */
+#define OQ_ROPE_HALF (1u << 0)    /* pair j is elements (j, j + R/2) of the R turned ones instead
+                                     of (2j, 2j + 1) */
+#define OQ_ROPE_INVERSE (1u << 1) /* turn by the opposite angle: undoes the embedding, and is the
+                                     gradient of it (the turn is orthogonal) */
+
 /* Text for a status code.  Never NULL; the string is static. */
 const char *oq_strerror(int status);
 
@@ -257,6 +267,104 @@ int oq_permute_rows(const void *src, void *dst, int64_t rows, int64_t row_bytes,
  * made by oq_plan_create), OQ_EUNSUPPORTED, OQ_ENOMEM, OQ_EDEVICE. */
 int oq_plan_create(int d, uint64_t seed, uint32_t flags, void **plan);
 int oq_plan_destroy(void *plan);
+
+/* ---- the microscaled path: norm -> codes -> projection -> embedding ----
+ *
+ * What a diffusion transformer's block needs around a projection in
+ * microscaled (MX) floating point (the OCP Microscaling formats, e2m1 and
+ * e4m3 elements in blocks of 32 with an e8m0 scale): the calls below take and
+ * give the same rows as the rest of the library and follow its conventions.
+ * None of them keeps anything between calls or needs a workspace; each is one
+ * or two kernels on `stream` and can be captured into a graph.
+ *
+ * MX rows: a row of d elements is d * format / 8 code bytes (e2m1: two codes a
+ * byte, the even element in the low half; sign, two exponent bits, one mantissa
+ * bit from the top; e4m3: one byte) and d / 32 scale bytes, both in coordinate
+ * order.  Scale byte s of a block stands for 2^(s - 127); with m = max |x|
+ * over the block, s = max(127 + floor(log2 m) - e_max, 0), e_max = 2 (e2m1)
+ * or 8 (e4m3); an element is x / 2^(s - 127) rounded to the nearest value of
+ * its type, ties to even, at most the largest.  A block of zeros has s = 0.
+ * A block with a NaN or an infinity gets s = 255 and codes 0 and reads back
+ * as NaN; in a product it makes the row's outputs NaN.
+ * d (K): a multiple of 32, 32 <= d <= 16384; rows up to 2^30. */
+
+/* Quantize rows to MX codes.
+ *   x: device fp32 or bf16 [rows][d], 16-byte aligned
+ *   codes: device [rows][d * format / 8], 16-byte aligned; scales: device
+ *   [rows][d / 32].  No two of the arrays may share a byte.
+ * rows = 0 is a no-op that succeeds.
+ * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
+int oq_mx_quantize(const void *x, int dtype, int64_t rows, int d, int format, uint8_t *codes,
+                   uint8_t *scales, void *stream);
+
+/* Read MX codes back: out[i] = element * 2^(s - 127), in dtype (exact, but for
+ * values of 2^128 and more, which are infinite, and in bf16 for e4m3 values
+ * below 2^-126, which round).
+ *   out: device fp32 or bf16 [rows][d], 16-byte aligned, apart from the inputs
+ * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
+int oq_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int format, int64_t rows, int d,
+                     int dtype, void *out, void *stream);
+
+/* Linear on MX codes:
+ *   y[m][n] = bf16( sum_b 2^(sa_mb + sw_nb - 254) sum_{k in block b} a_mk w_nk )
+ * fp32 accumulation on the matrix cores, one bf16 rounding, no bias; any
+ * pair of formats.
+ *   a_codes [M][K * a_format / 8], a_scales [M][K / 32], w_codes
+ *   [N][K * w_format / 8], w_scales [N][K / 32]: device, codes 16-byte aligned
+ *   y: device bf16 [M][N], apart from every input
+ * M = 0 or N = 0 is a no-op that succeeds.
+ * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
+int oq_mx_linear(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
+                 const uint8_t *w_codes, const uint8_t *w_scales, int w_format, int64_t M,
+                 int64_t N, int K, uint16_t *y, void *stream);
+
+/* Gated residual sum and modulated RMS norm of every row:
+ *   h = residual + gate_g * x
+ *   y = h / sqrt(mean(h^2) + eps) * weight * (1 + scale_g) + shift_g
+ * with g = row / rows_per_mod; residual, gate, weight, scale and shift may
+ * each be NULL (then 0, 1, 1, 0, 0).  fp32 arithmetic; the norm runs over h
+ * before it is rounded to the stream's type.
+ *   x, residual: device, dtype [rows][d]
+ *   weight: device, param_dtype [d]; gate, scale, shift: device, param_dtype,
+ *     row g at g * mod_stride elements (mod_stride >= d, a multiple of 16
+ *     bytes, where there is more than one group: the slices of one modulation
+ *     projection [groups][6 d] are passed as they lie)
+ *   eps > 0
+ *   sum: device, dtype [rows][d], receives h; may be NULL
+ *   y_format 0: y is dtype [rows][d] and y_scales is NULL; OQ_MX_FP4 or
+ *     OQ_MX_FP8: y are MX codes and y_scales their scale bytes, as
+ *     oq_mx_quantize makes them of the fp32 values
+ * Every pointer but y_scales 16-byte aligned.  sum, and a y in dtype, may be x
+ * or the residual themselves (in place); otherwise an output may not share a
+ * byte with an input or with another output.
+ * d a multiple of 32, 32 <= d <= 16384; rows up to 2^30; rows = 0 no-op.
+ * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
+int oq_add_rms_norm(const void *x, const void *residual, int dtype, int64_t rows, int d, float eps,
+                    const void *weight, const void *gate, const void *scale, const void *shift,
+                    int param_dtype, int64_t rows_per_mod, int64_t mod_stride, void *sum,
+                    int y_format, void *y, uint8_t *y_scales, void *stream);
+
+/* Rotary embedding with several axes (time, height, width of a latent video).
+ * The first R = sum(axis_dims) elements of each head are R/2 pairs, numbered
+ * axis after axis; pair i of axis a turns by pos_a * theta^(-2 i / axis_dims[a]):
+ *   (u, v) -> (u cos - v sin, u sin + v cos)
+ * and the other head_dim - R elements are copied.  Angles are exact to 2^-32
+ * of a turn at every int32 position.
+ *   x, y: device, dtype; element e of head h of token t at t * token stride +
+ *     h * head stride + e (strides in elements, multiples of 16 bytes, >= 0), so
+ *     the queries and keys inside a fused projection's output are read in
+ *     place; 16-byte aligned.  y is x with the same strides (in place), or
+ *     its span may not meet x's; y's elements have addresses of their own
+ *     (each head whole, heads inside tokens or tokens inside heads)
+ *   pos: device int32 [tokens][axes]
+ *   axes 1..4; axis_dims: host, even, >= 0, sum R <= head_dim
+ *   head_dim % 8 == 0, <= 512; with OQ_ROPE_HALF R % 16 == 0; theta >= 1
+ *   flags: OQ_ROPE_HALF, OQ_ROPE_INVERSE
+ * tokens = 0 or heads = 0 is a no-op that succeeds; tokens up to 2^30.
+ * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
+int oq_rope(const void *x, int dtype, int64_t tokens, int heads, int head_dim, int64_t x_token,
+            int64_t x_head, const int32_t *pos, int axes, const int *axis_dims, double theta,
+            uint32_t flags, void *y, int64_t y_token, int64_t y_head, void *stream);
 
 #ifdef __cplusplus
 }

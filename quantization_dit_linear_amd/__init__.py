@@ -14,6 +14,10 @@ Functions mirror the C entry points:
 * :func:`fake_quantize`   -> ``oq_rotate_quantize`` with ``OQ_OUT_BF16_DEQUANT``
 * :func:`prepare_weights` -> ``oq_prepare_weights``
 * :func:`linear`          -> ``oq_linear``
+* :func:`mx_quantize`, :func:`mx_dequantize` -> ``oq_mx_quantize``, ``oq_mx_dequantize``
+* :func:`mx_linear`       -> ``oq_mx_linear``
+* :func:`add_rms_norm`    -> ``oq_add_rms_norm``
+* :func:`rope`            -> ``oq_rope``
 """
 import ctypes
 import os
@@ -27,6 +31,8 @@ OQ_OK, OQ_EINVAL, OQ_EUNSUPPORTED, OQ_ENOMEM, OQ_EDEVICE = 0, -1, -2, -3, -4
 OQ_F32, OQ_BF16 = 0, 1
 OQ_ROT_NO_SIGNS, OQ_OUT_F32_ROTATED, OQ_OUT_BF16_DEQUANT, OQ_ROT_INPUT_PERMUTED = 1, 2, 4, 8
 OQ_CODEBOOK_SPHERE = 16
+OQ_MX_FP4, OQ_MX_FP8 = 4, 8
+OQ_ROPE_HALF, OQ_ROPE_INVERSE = 1, 2
 
 # every symbol the header declares, with (restype, argtypes)
 _P = ctypes.c_void_p
@@ -56,6 +62,20 @@ _SIGS = {
                                                _P, _P, _P]),
     "oq_rtn4_linear": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, _P, _P, ctypes.c_int64,
                                       ctypes.c_int, _P, _P]),
+    "oq_mx_quantize": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                      _P, _P, _P]),
+    "oq_mx_dequantize": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int,
+                                        ctypes.c_int, _P, _P]),
+    "oq_mx_linear": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, _P, ctypes.c_int, ctypes.c_int64,
+                                    ctypes.c_int64, ctypes.c_int, _P, _P]),
+    "oq_add_rms_norm": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int,
+                                       ctypes.c_float, _P, _P, _P, _P, ctypes.c_int,
+                                       ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int, _P, _P,
+                                       _P]),
+    "oq_rope": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                               ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int, _P,
+                               ctypes.c_double, ctypes.c_uint32, _P, ctypes.c_int64,
+                               ctypes.c_int64, _P]),
     "oq_diag_mfma_f16": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, _P]),
 }
 
@@ -100,7 +120,7 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _dev_ptr(t, name):
+def _on_device(t, name):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -109,6 +129,10 @@ def _dev_ptr(t, name):
     if t.device.index is not None and t.device.index != torch.cuda.current_device():
         raise ValueError(f"{name} lives on {t.device}, not on the current device "
                          f"cuda:{torch.cuda.current_device()}")
+
+
+def _dev_ptr(t, name):
+    _on_device(t, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
@@ -301,6 +325,199 @@ def rtn4_linear(x, q4, scales, *, out=None, stream=None):
                               _dev_ptr(scales, "scales"), N, K, _dev_ptr(out, "y"),
                               _stream(stream))
     _check(rc, "oq_rtn4_linear")
+    return out
+
+
+# ------------------------------------------------- the microscaled path --
+
+_MX = {"fp4": OQ_MX_FP4, "fp8": OQ_MX_FP8}
+
+
+def _mx(fmt, name="fmt"):
+    if fmt not in _MX:
+        raise ValueError(f"{name} must be 'fp4' or 'fp8' (got {fmt!r})")
+    return _MX[fmt]
+
+
+def _empty(shape, dtype, device, stream):
+    """A fresh output, owned by the stream that the call runs on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _mx_outputs(codes, scales, rows, d, bits, device, stream):
+    import torch
+    if codes is None:
+        codes = _empty((rows, d * bits // 8), torch.uint8, device, stream)
+    if scales is None:
+        scales = _empty((rows, d // 32), torch.uint8, device, stream)
+    _expect(codes, (rows, d * bits // 8), torch.uint8, "codes")
+    _expect(scales, (rows, d // 32), torch.uint8, "scales")
+    return codes, scales
+
+
+def _mx_pair(codes, scales, bits, names):
+    """(rows, d) of a pair of MX arrays, whose shapes must agree."""
+    import torch
+    for t, n in zip((codes, scales), names):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+        if t.dim() != 2:
+            raise ValueError(f"{n} must be two-dimensional")
+    rows, d = scales.shape[0], 32 * scales.shape[1]
+    _expect(codes, (rows, d * bits // 8), torch.uint8, names[0])
+    _expect(scales, (rows, d // 32), torch.uint8, names[1])
+    return rows, d
+
+
+def mx_quantize(x, fmt, *, codes=None, scales=None, stream=None):
+    """MX codes (uint8 [rows, d/2] for 'fp4', [rows, d] for 'fp8') and e8m0
+    scale bytes (uint8 [rows, d/32]) of x [rows, d] (bfloat16 or float32):
+    activations and weights alike."""
+    bits = _mx(fmt)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, d]")
+    rows, d = x.shape
+    codes, scales = _mx_outputs(codes, scales, rows, d, bits, x.device, stream)
+    rc = lib().oq_mx_quantize(_dev_ptr(x, "x"), _dtype_code(x), rows, d, bits,
+                              _dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"),
+                              _stream(stream))
+    _check(rc, "oq_mx_quantize")
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, fmt, *, dtype=None, out=None, stream=None):
+    """The values [rows, d] that MX codes stand for (bfloat16 unless dtype or
+    out says float32)."""
+    import torch
+    bits = _mx(fmt)
+    rows, d = _mx_pair(codes, scales, bits, ("codes", "scales"))
+    if out is None:
+        out = _empty((rows, d), dtype or torch.bfloat16, codes.device, stream)
+    _expect(out, (rows, d), dtype or out.dtype, "out")
+    rc = lib().oq_mx_dequantize(_dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"), bits, rows,
+                                d, _dtype_code(out), _dev_ptr(out, "out"), _stream(stream))
+    _check(rc, "oq_mx_dequantize")
+    return out
+
+
+def mx_linear(a_codes, a_scales, a_fmt, w_codes, w_scales, w_fmt, *, out=None, stream=None):
+    """bf16 y [M, N] = A W^T of MX activations [M, K] and weights [N, K]."""
+    import torch
+    a_bits, w_bits = _mx(a_fmt, "a_fmt"), _mx(w_fmt, "w_fmt")
+    M, K = _mx_pair(a_codes, a_scales, a_bits, ("a_codes", "a_scales"))
+    N, Kw = _mx_pair(w_codes, w_scales, w_bits, ("w_codes", "w_scales"))
+    if K != Kw:
+        raise ValueError(f"activations have {K} columns, weights {Kw}")
+    if out is None:
+        out = _empty((M, N), torch.bfloat16, a_codes.device, stream)
+    _expect(out, (M, N), torch.bfloat16, "out")
+    rc = lib().oq_mx_linear(_dev_ptr(a_codes, "a_codes"), _dev_ptr(a_scales, "a_scales"), a_bits,
+                            _dev_ptr(w_codes, "w_codes"), _dev_ptr(w_scales, "w_scales"), w_bits,
+                            M, N, K, _dev_ptr(out, "y"), _stream(stream))
+    _check(rc, "oq_mx_linear")
+    return out
+
+
+def _strided_ptr(t, name):
+    """Device pointer of a tensor whose last dimension is dense (the other
+    strides are the call's arguments)."""
+    _on_device(t, name)
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def add_rms_norm(x, residual=None, *, weight=None, gate=None, scale=None, shift=None,
+                 rows_per_mod=None, eps=1e-6, fmt=None, sum_out=None, out=None, scales_out=None,
+                 stream=None):
+    """h = residual + gate * x and y = h / rms(h) * weight * (1 + scale) + shift.
+
+    x, residual: [rows, d], bfloat16 or float32.  weight [d]; gate, scale and
+    shift [groups, d] (or [d]) with one common row stride, row r taking group
+    r // rows_per_mod (by default the rows split evenly); all parameters of one
+    type, bfloat16 or float32.  Returns (h, y), or with fmt 'fp4' / 'fp8'
+    (h, codes, scales): y in MX codes.  sum_out (for h) and out may be x or
+    residual themselves; sum_out=False computes no h and returns None for it.
+    """
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, d]")
+    rows, d = x.shape
+    if residual is not None:
+        _expect(residual, (rows, d), x.dtype, "residual")
+    params = [p for p in (weight, gate, scale, shift) if p is not None]
+    for p, n in ((weight, "weight"), (gate, "gate"), (scale, "scale"), (shift, "shift")):
+        if p is not None and (p.shape[-1:] != (d,) or p.dtype != params[0].dtype):
+            raise ValueError(f"{n} must have {d} columns and the other parameters' dtype")
+    if weight is not None and weight.dim() != 1:
+        raise ValueError("weight must be [d]")
+    groups, stride = 1, d
+    mods = {n: p for n, p in (("gate", gate), ("scale", scale), ("shift", shift)) if p is not None}
+    for i, (n, p) in enumerate(mods.items()):
+        if p.dim() not in (1, 2):
+            raise ValueError(f"{n} must be [groups, d] or [d]")
+        g = 1 if p.dim() == 1 else p.shape[0]
+        s = d if g == 1 else p.stride(0)
+        if i and (g, s) != (groups, stride):
+            raise ValueError("gate, scale and shift must have the same groups and row stride")
+        groups, stride = g, s
+    if rows_per_mod is None:
+        rows_per_mod = max(1, -(-rows // max(1, groups)))
+    if mods and (rows_per_mod < 1 or -(-rows // rows_per_mod) > groups):
+        raise ValueError(f"{rows} rows at {rows_per_mod} per group need more than {groups} groups")
+    if sum_out is None:
+        sum_out = _empty((rows, d), x.dtype, x.device, stream)
+    elif sum_out is False:
+        sum_out = None
+    if sum_out is not None:
+        _expect(sum_out, (rows, d), x.dtype, "sum_out")
+    if fmt is None:
+        if scales_out is not None:
+            raise ValueError("scales_out needs a fmt")
+        if out is None:
+            out = _empty((rows, d), x.dtype, x.device, stream)
+        _expect(out, (rows, d), x.dtype, "out")
+        bits, scales = 0, None
+    else:
+        bits = _mx(fmt)
+        out, scales = _mx_outputs(out, scales_out, rows, d, bits, x.device, stream)
+    opt = lambda t, n: None if t is None else _dev_ptr(t, n)  # noqa: E731
+    mod = lambda t, n: None if t is None else _strided_ptr(t, n)  # noqa: E731
+    rc = lib().oq_add_rms_norm(
+        _dev_ptr(x, "x"), opt(residual, "residual"), _dtype_code(x), rows, d, eps,
+        opt(weight, "weight"), mod(gate, "gate"), mod(scale, "scale"), mod(shift, "shift"),
+        _dtype_code(params[0]) if params else OQ_F32, rows_per_mod, stride,
+        opt(sum_out, "sum_out"), bits, _dev_ptr(out, "out"), opt(scales, "scales_out"),
+        _stream(stream))
+    _check(rc, "oq_add_rms_norm")
+    return (sum_out, out) if fmt is None else (sum_out, out, scales)
+
+
+def rope(x, pos, axis_dims, *, theta=10000.0, half=False, inverse=False, out=None, stream=None):
+    """Rotary embedding of x [tokens, heads, head_dim] (bfloat16 or float32, any
+    16-byte strides, dense heads: a slice of a fused projection's output is
+    taken as it lies) at pos int32 [tokens, axes]; axis_dims: elements of a
+    head that turn with each axis.  half: pairs (j, j + R/2) instead of
+    (2j, 2j+1); inverse: the opposite turn, which is the gradient.  out may be x."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be [tokens, heads, head_dim]")
+    tokens, heads, hd = x.shape
+    dims = [int(v) for v in axis_dims]
+    _expect(pos, (tokens, len(dims)), torch.int32, "pos")
+    if out is None:
+        out = _empty((tokens, heads, hd), x.dtype, x.device, stream)
+    _expect(out, (tokens, heads, hd), x.dtype, "out")
+    flags = (OQ_ROPE_HALF if half else 0) | (OQ_ROPE_INVERSE if inverse else 0)
+    rc = lib().oq_rope(_strided_ptr(x, "x"), _dtype_code(x), tokens, heads, hd, x.stride(0),
+                       x.stride(1), _dev_ptr(pos, "pos"), len(dims),
+                       (ctypes.c_int * len(dims))(*dims), theta, flags, _strided_ptr(out, "out"),
+                       out.stride(0), out.stride(1), _stream(stream))
+    _check(rc, "oq_rope")
     return out
 
 

@@ -13,7 +13,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "liborbitquant.so")
 SOURCES = ["oq_host.cpp", "rotate_quantize.hip", "rotate_quantize_fast.hip", "linear.hip",
-           "adaln_rtn4.hip", "diag.hip"]
+           "adaln_rtn4.hip", "mx.hip", "mx_linear.hip", "rms_norm.hip", "rope.hip", "diag.hip"]
 # per-source extra flags: the rotate kernel keeps its MFMA results in
 # ordinary VGPRs (no accumulation-register round trip per value)
 PER_SOURCE = {"rotate_quantize_fast.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}

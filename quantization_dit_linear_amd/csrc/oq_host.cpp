@@ -796,4 +796,215 @@ int oq_release_plans(void) {
   return rc;
 }
 
+// ------------------------------------------- microscaled path and its kin --
+
+namespace {
+
+// internal element format of an OQ_MX_* value: 0 = e2m1, 1 = e4m3, -1 = neither
+int mx_format(int format) { return format == OQ_MX_FP4 ? 0 : format == OQ_MX_FP8 ? 1 : -1; }
+
+int check_mx_shape(int64_t rows, int d) {
+  if (rows < 0 || d <= 0) return OQ_EINVAL;
+  if (d % oq::kMxBlock != 0 || d > oq::kMaxD || rows > kMaxRows) return OQ_EUNSUPPORTED;
+  return OQ_OK;
+}
+
+int elem_bytes(int dtype) { return dtype == OQ_F32 ? 4 : 2; }
+
+// bytes from the first to the last element of a strided [n0][n1][n2] array (-1: too large)
+int64_t span_bytes(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int size) {
+  const __int128 e = (__int128)(n0 - 1) * s0 + (__int128)(n1 - 1) * s1 + n2;
+  return e > ((int64_t)1 << 58) ? -1 : (int64_t)e * size;
+}
+
+}  // namespace
+
+int oq_mx_quantize(const void *x, int dtype, int64_t rows, int d, int format, uint8_t *codes,
+                   uint8_t *scales, void *stream) {
+  const int f = mx_format(format);
+  if (f < 0 || (dtype != OQ_F32 && dtype != OQ_BF16)) return OQ_EINVAL;
+  const int rc = check_mx_shape(rows, d);
+  if (rc != OQ_OK) return rc;
+  if (rows == 0) return OQ_OK;
+  if (!x || !codes || !scales) return OQ_EINVAL;
+  if (!aligned(x, 16) || !aligned(codes, 16)) return OQ_EINVAL;
+  const int64_t n = rows * d, xb = n * elem_bytes(dtype), cb = n * format / 8, sb = n / oq::kMxBlock;
+  if (overlaps(x, xb, codes, cb) || overlaps(x, xb, scales, sb) || overlaps(codes, cb, scales, sb))
+    return OQ_EINVAL;
+  hipError_t e = oq::launch_mx_quantize(x, dtype, rows, d, f, codes, scales, (hipStream_t)stream);
+  return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
+}
+
+int oq_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int format, int64_t rows, int d,
+                     int dtype, void *out, void *stream) {
+  const int f = mx_format(format);
+  if (f < 0 || (dtype != OQ_F32 && dtype != OQ_BF16)) return OQ_EINVAL;
+  const int rc = check_mx_shape(rows, d);
+  if (rc != OQ_OK) return rc;
+  if (rows == 0) return OQ_OK;
+  if (!codes || !scales || !out) return OQ_EINVAL;
+  if (!aligned(codes, 16) || !aligned(out, 16)) return OQ_EINVAL;
+  const int64_t n = rows * d, ob = n * elem_bytes(dtype);
+  if (overlaps(out, ob, codes, n * format / 8) || overlaps(out, ob, scales, n / oq::kMxBlock))
+    return OQ_EINVAL;
+  hipError_t e =
+      oq::launch_mx_dequantize(codes, scales, f, rows, d, dtype, out, (hipStream_t)stream);
+  return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
+}
+
+int oq_mx_linear(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
+                 const uint8_t *w_codes, const uint8_t *w_scales, int w_format, int64_t M,
+                 int64_t N, int K, uint16_t *y, void *stream) {
+  const int fa = mx_format(a_format), fw = mx_format(w_format);
+  if (fa < 0 || fw < 0) return OQ_EINVAL;
+  int rc = check_mx_shape(M, K);
+  if (rc != OQ_OK) return rc;
+  rc = check_mx_shape(N, K);
+  if (rc != OQ_OK) return rc;
+  if (M == 0 || N == 0) return OQ_OK;
+  if (!a_codes || !a_scales || !w_codes || !w_scales || !y) return OQ_EINVAL;
+  if (!aligned(a_codes, 16) || !aligned(w_codes, 16) || !aligned(y, 2)) return OQ_EINVAL;
+  const int64_t yb = M * N * 2;
+  if (overlaps(y, yb, a_codes, M * K * a_format / 8) || overlaps(y, yb, w_codes, N * K * w_format / 8) ||
+      overlaps(y, yb, a_scales, M * K / oq::kMxBlock) || overlaps(y, yb, w_scales, N * K / oq::kMxBlock))
+    return OQ_EINVAL;
+  const oq::MxLinearArgs a{a_codes, a_scales, fa, w_codes, w_scales, fw, M, N, K, y,
+                           (hipStream_t)stream};
+  hipError_t e = oq::launch_mx_linear(a);
+  return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
+}
+
+int oq_add_rms_norm(const void *x, const void *residual, int dtype, int64_t rows, int d, float eps,
+                    const void *weight, const void *gate, const void *scale, const void *shift,
+                    int param_dtype, int64_t rows_per_mod, int64_t mod_stride, void *sum,
+                    int y_format, void *y, uint8_t *y_scales, void *stream) {
+  if (dtype != OQ_F32 && dtype != OQ_BF16) return OQ_EINVAL;
+  if (param_dtype != OQ_F32 && param_dtype != OQ_BF16) return OQ_EINVAL;
+  const int f = y_format == 0 ? 0 : mx_format(y_format);
+  if (f < 0 || !(eps > 0.f) || !std::isfinite(eps)) return OQ_EINVAL;
+  const int rc = check_mx_shape(rows, d);
+  if (rc != OQ_OK) return rc;
+  const bool mod = gate || scale || shift;
+  if (mod && (rows_per_mod < 1 || mod_stride < 0)) return OQ_EINVAL;
+  if (rows == 0) return OQ_OK;
+  if (!x || !y || (y_format != 0) != (y_scales != nullptr)) return OQ_EINVAL;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(gate, 16) ||
+      !aligned(scale, 16) || !aligned(shift, 16) || !aligned(sum, 16) || !aligned(y, 16))
+    return OQ_EINVAL;
+  const int64_t groups = mod ? (rows - 1) / rows_per_mod + 1 : 1;
+  const int pb = elem_bytes(param_dtype);
+  if (mod && groups > 1 && (mod_stride < d || mod_stride * pb % 16 != 0)) return OQ_EINVAL;
+  // outputs: the sum and a plain y may take the place of x or of the
+  // residual (every thread reads its elements before it writes them); no
+  // other two arrays may share a byte
+  const int64_t n = rows * d, b = n * elem_bytes(dtype), sb = n / oq::kMxBlock;
+  const int64_t yb = y_format == 0 ? b : n * y_format / 8;
+  const int64_t mb = mod ? span_bytes(groups, mod_stride, 1, 0, d, pb) : 0;
+  if (mb < 0) return OQ_EINVAL;
+  struct Range {
+    const void *p;
+    int64_t bytes;
+    bool in_place;  // a stream input
+  } ins[] = {{x, b, true},       {residual, b, true}, {weight, (int64_t)d * pb, false},
+             {gate, mb, false},  {scale, mb, false},  {shift, mb, false}},
+    outs[] = {{sum, b, true}, {y, yb, y_format == 0}, {y_scales, sb, false}};
+  for (const Range &o : outs)
+    for (const Range &i : ins)
+      if (o.p && i.p && overlaps(o.p, o.bytes, i.p, i.bytes) &&
+          !(o.p == i.p && o.in_place && i.in_place))
+        return OQ_EINVAL;
+  for (int i = 0; i < 3; i++)
+    for (int j = i + 1; j < 3; j++)
+      if (outs[i].p && outs[j].p && overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+        return OQ_EINVAL;
+  oq::RmsNormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.dtype = dtype;
+  a.rows = rows;
+  a.d = d;
+  a.eps = eps;
+  a.weight = weight;
+  a.gate = gate;
+  a.scale = scale;
+  a.shift = shift;
+  a.param_dtype = param_dtype;
+  a.rows_per_mod = mod ? rows_per_mod : rows;
+  a.mod_stride = mod_stride;
+  a.sum = sum;
+  a.out = y_format == 0 ? 0 : f == 1 ? 1 : 2;
+  a.y = y;
+  a.y_scales = y_scales;
+  a.stream = (hipStream_t)stream;
+  hipError_t e = oq::launch_rms_norm(a);
+  return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
+}
+
+int oq_rope(const void *x, int dtype, int64_t tokens, int heads, int head_dim, int64_t x_token,
+            int64_t x_head, const int32_t *pos, int axes, const int *axis_dims, double theta,
+            uint32_t flags, void *y, int64_t y_token, int64_t y_head, void *stream) {
+  if (dtype != OQ_F32 && dtype != OQ_BF16) return OQ_EINVAL;
+  if (flags & ~(OQ_ROPE_HALF | OQ_ROPE_INVERSE)) return OQ_EINVAL;
+  if (tokens < 0 || heads < 0 || head_dim <= 0 || axes < 1 || !axis_dims) return OQ_EINVAL;
+  if (!(theta >= 1.0) || !std::isfinite(theta)) return OQ_EINVAL;
+  if (head_dim % 8 != 0 || head_dim > oq::kRopeMaxHeadDim || axes > oq::kRopeMaxAxes)
+    return OQ_EUNSUPPORTED;
+  int64_t turned = 0;
+  for (int i = 0; i < axes; i++) {
+    if (axis_dims[i] < 0 || axis_dims[i] % 2 != 0) return OQ_EINVAL;
+    turned += axis_dims[i];
+  }
+  if (turned > head_dim) return OQ_EINVAL;
+  const bool half = (flags & OQ_ROPE_HALF) != 0;
+  if (half && turned % 16 != 0) return OQ_EUNSUPPORTED;
+  if (x_token < 0 || x_head < 0 || y_token < 0 || y_head < 0) return OQ_EINVAL;
+  if (tokens > kMaxRows) return OQ_EUNSUPPORTED;
+  if (tokens == 0 || heads == 0) return OQ_OK;
+  if (!x || !y || !pos) return OQ_EINVAL;
+  const int size = elem_bytes(dtype), unit = 16 / size;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(pos, 4)) return OQ_EINVAL;
+  if (x_token % unit || x_head % unit || y_token % unit || y_head % unit) return OQ_EINVAL;
+  const int64_t xb = span_bytes(tokens, x_token, heads, x_head, head_dim, size);
+  const int64_t yb = span_bytes(tokens, y_token, heads, y_head, head_dim, size);
+  if (xb < 0 || yb < 0) return OQ_EINVAL;
+  // no two elements of y at one address: heads inside tokens, or tokens inside heads
+  const bool by_token = (heads == 1 || y_head >= head_dim) &&
+                        (tokens == 1 || (__int128)(heads - 1) * y_head + head_dim <= y_token);
+  const bool by_head = (tokens == 1 || y_token >= head_dim) &&
+                       (heads == 1 || (__int128)(tokens - 1) * y_token + head_dim <= y_head);
+  if (!by_token && !by_head) return OQ_EINVAL;
+  const bool in_place = x == y && (tokens == 1 || x_token == y_token) &&
+                        (heads == 1 || x_head == y_head);
+  if (!in_place && overlaps(x, xb, y, yb)) return OQ_EINVAL;
+  if (overlaps(y, yb, pos, tokens * axes * 4)) return OQ_EINVAL;
+  oq::RopeArgs a{};
+  a.x = x;
+  a.dtype = dtype;
+  a.tokens = tokens;
+  a.heads = heads;
+  a.head_dim = head_dim;
+  a.turned = (int)turned;
+  a.x_token = x_token;
+  a.x_head = x_head;
+  a.y_token = y_token;
+  a.y_head = y_head;
+  a.pos = pos;
+  a.axes = axes;
+  a.half = half;
+  a.inverse = (flags & OQ_ROPE_INVERSE) != 0;
+  a.y = y;
+  a.stream = (hipStream_t)stream;
+  int j = 0;
+  for (int i = 0; i < axes; i++)
+    for (int k = 0; k < axis_dims[i]; k += 2, j++) {
+      // turns per position, at most 1 / 2 pi (theta >= 1), in units of 2^-64
+      const long double f =
+          expl(-(long double)k / axis_dims[i] * logl((long double)theta)) / (2 * acosl(-1.0L));
+      a.freq[j] = (uint64_t)rintl(ldexpl(f, 64));
+      a.axis[j] = (uint8_t)i;
+    }
+  hipError_t e = oq::launch_rope(a);
+  return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
+}
+
 }  // extern "C"

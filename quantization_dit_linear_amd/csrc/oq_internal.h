@@ -148,4 +148,58 @@ hipError_t launch_rtn4_linear(const void *x, int dtype, int64_t M, const uint8_t
 hipError_t launch_permute_rows(const void *src, void *dst, int64_t rows, int64_t row_bytes,
                                const int32_t *perm_inv, hipStream_t stream);
 
+// Microscaled (MX) codes: format 0 = e2m1 (4 bits), 1 = e4m3 (8 bits), blocks
+// of kMxBlock elements with a power-of-two scale byte.
+constexpr int kMxBlock = 32;
+hipError_t launch_mx_quantize(const void *x, int dtype, int64_t rows, int d, int format,
+                              uint8_t *codes, uint8_t *scales, hipStream_t stream);
+hipError_t launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int format,
+                                int64_t rows, int d, int dtype, void *out, hipStream_t stream);
+
+struct MxLinearArgs {
+  const uint8_t *a_codes, *a_scales;
+  int a_format;
+  const uint8_t *w_codes, *w_scales;
+  int w_format;
+  int64_t M, N;
+  int K;
+  uint16_t *y;
+  hipStream_t stream;
+};
+hipError_t launch_mx_linear(const MxLinearArgs &a);
+
+struct RmsNormArgs {
+  const void *x, *residual;
+  int dtype;
+  int64_t rows;
+  int d;
+  float eps;
+  const void *weight, *gate, *scale, *shift;  // any may be null
+  int param_dtype;
+  int64_t rows_per_mod, mod_stride;
+  void *sum;  // may be null
+  int out;    // 0: y in dtype, 1: MX e4m3, 2: MX e2m1
+  void *y;
+  uint8_t *y_scales;
+  hipStream_t stream;
+};
+hipError_t launch_rms_norm(const RmsNormArgs &a);
+
+constexpr int kRopeMaxHeadDim = 512, kRopeMaxAxes = 4;
+struct RopeArgs {
+  const void *x;
+  int dtype;
+  int64_t tokens;
+  int heads, head_dim, turned;  // turned: leading elements of a head that are paired
+  int64_t x_token, x_head, y_token, y_head;  // strides in elements
+  const int32_t *pos;                        // [tokens][axes]
+  int axes;
+  bool half, inverse;
+  void *y;
+  hipStream_t stream;
+  uint64_t freq[kRopeMaxHeadDim / 2];  // turns per position of each pair, units of 2^-64
+  uint8_t axis[kRopeMaxHeadDim / 2];   // the axis of each pair
+};
+hipError_t launch_rope(const RopeArgs &a);
+
 }  // namespace oq
