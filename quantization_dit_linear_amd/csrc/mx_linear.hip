@@ -2,12 +2,20 @@
 //
 //   y[m][n] = bf16( sum_b 2^(sa_mb + sw_nb - 254) sum_{k in block b} a_mk w_nk )
 //
-// v_mfma_scale_f32_16x16x128_f8f6f4 multiplies elements of either type and
-// applies the two blocks' powers of two itself.  Lane (r = lane % 16, g =
-// lane / 16) supplies row r.  4-bit elements: k = 32 g + [0, 32), one
-// 16-byte word.  8-bit elements: k = 16 g + [0, 16) and 64 + 16 g + [0, 16).
-// In both cases the lane's scale byte is that of k block g (k = 32 g ..).
+// The scaled matrix instructions multiply elements of either type and apply
+// the two blocks' powers of two themselves, so codes and scale bytes go from
+// memory to the matrix cores as they are: no decoding, no separate scaling.
+//
+// Operand layout of v_mfma_scale_f32_32x32x64_f8f6f4: lane (r = lane % 32,
+// g = lane / 32) supplies row r.  4-bit elements: 16 bytes, block g of the
+// two.  8-bit elements: bytes 16 g .. 16 g + 15 of block 0, then of block 1.
+// Either way the lane's scale byte is that of block g.  Any assignment of
+// the row's blocks to (instruction, g) will do that both operands share.
+// (16x16x128: r = lane % 16, four groups g; 4-bit block g; 8-bit bytes 16 g of
+// each 64-element half; scale of block g.)
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "mx_codec.h"
 #include "oq_internal.h"
@@ -15,71 +23,351 @@
 namespace oq {
 namespace {
 
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// One row's operand for k0 .. k0 + 127: zero codes and scales past K or the last row.
-template <int FMT>
-__device__ __forceinline__ void load_operand(const uint8_t *codes, const uint8_t *scales,
-                                             int64_t row, bool in, int k0, int K, int g, i32x8 &v,
-                                             int &s) {
-  u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-  s = 0;
-  if (in) {
-    if constexpr (FMT == 0) {
-      if (k0 + 32 * g < K) lo = *(const u32x4 *)(codes + row * (K / 2) + k0 / 2 + 16 * g);
-    } else {
-      const uint8_t *p = codes + row * K + k0 + 16 * g;
-      if (k0 + 16 * g < K) lo = *(const u32x4 *)p;
-      if (k0 + 64 + 16 * g < K) hi = *(const u32x4 *)(p + 64);
-    }
-    if (k0 + 32 * g < K) s = scales[row * (K / 32) + k0 / 32 + g];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; i++) v[i] = (int)lo[i], v[4 + i] = (int)hi[i];
+constexpr int kGroupM = 8;  // tile rows per group of the tile order
+
+// A workgroup of 2 x 2 waves computes a (64 IB) x (64 JB) tile; each wave a
+// (32 IB) x (32 JB) block of it.
+template <int FA, int FW, int IB_, int JB_, int WGS_>
+struct MxTile {
+  static constexpr int IB = IB_, JB = JB_, WGS = WGS_;
+  static constexpr int TM = 64 * IB, TN = 64 * JB;
+  // elements of K a stage: the same matrix-core time with 4-bit elements on
+  // both sides as with 8-bit ones, which run at half the rate
+  static constexpr int KS = (FA || FW) ? 64 : 128;
+  static constexpr int STEPS = KS / 64;
+  static constexpr int RA = KS / (FA ? 1 : 2), RW = KS / (FW ? 1 : 2);  // row bytes a stage
+  static constexpr int AB = TM * RA, STAGE = AB + TN * RW;
+  static constexpr int SROWS = TM + TN;
+  static constexpr int SBUF = 4 * SROWS * 4;     // scales of 16 blocks: 4 planes of one word a row
+  static constexpr int SPG = 512 / KS;           // stages that one such group lasts
+  static constexpr int EPI = 32 * 64 * JB;       // a wave's staging of 32 output rows
+  static constexpr int SC0 = 2 * STAGE, EP0 = SC0 + 2 * SBUF;
+  static constexpr int LDS = EP0 + 4 * EPI;
+  static_assert(LDS * WGS <= 160 * 1024, "LDS of one CU");
+};
+
+// XOR swizzle of a row's 16-byte pieces in LDS: rows lie one after another,
+// so the stores are consecutive, and 8 or 16 rows' equal pieces fall into
+// different banks.
+template <int RB>
+__device__ __forceinline__ int swizzle(int row) {
+  return RB == 64 ? ((row >> 1) ^ (row >> 3)) & 3 : ((row >> 2) ^ (row >> 3)) & 1;
 }
 
-// A wave computes 16 x 16 outputs, weights as the first operand so that a
-// lane ends up with 4 consecutive columns of one output row.
-template <int FA, int FW>
-__global__ __launch_bounds__(256) void mx_linear_kernel(
+__device__ __forceinline__ u32x4 buf_load(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t base) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, base, 0));
+}
+
+// Group-major tile order: index g -> tile (tm, tn), kGroupM tile rows per
+// group, column-major inside a group.
+__device__ __forceinline__ void tile_of(int g, int nbm, int nbn, int &tm, int &tn) {
+  const int gsz = kGroupM * nbn, grp = g / gsz, first = grp * kGroupM;
+  const int gm = (nbm - first) < kGroupM ? (nbm - first) : kGroupM;
+  tm = first + (g % gsz) % gm;
+  tn = (g % gsz) / gm;
+}
+
+template <int FMT>
+struct Frag {
+  u32x4 v[FMT ? 2 : 1];
+  __device__ __forceinline__ i32x8 op() const {
+    const u32x4 h = v[FMT ? 1 : 0];
+    return i32x8{(int)v[0][0], (int)v[0][1], (int)v[0][2], (int)v[0][3],
+                 (int)h[0],    (int)h[1],    (int)h[2],    (int)h[3]};
+  }
+};
+
+template <int FA, int FW, class TL>
+__global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
     const uint8_t *__restrict__ A, const uint8_t *__restrict__ As, const uint8_t *__restrict__ W,
-    const uint8_t *__restrict__ Ws, int M, int N, int K, uint16_t *__restrict__ Y) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = lane & 15, g = lane >> 4;
-  const int nbn = (N + 15) / 16;
-  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-  const int m0 = (int)(t / nbn) * 16, n0 = (int)(t % nbn) * 16;
-  if (m0 >= M) return;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 0; k0 < K; k0 += 128) {
-    i32x8 a, w;
-    int sa, sw;
-    load_operand<FA>(A, As, m0 + r, m0 + r < M, k0, K, g, a, sa);
-    load_operand<FW>(W, Ws, n0 + r, n0 + r < N, k0, K, g, w, sw);
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, acc, FW ? 0 : 4, FA ? 0 : 4, 0, sw,
-                                                           0, sa);
-  }
-  const int m = m0 + r;
-  if (m >= M) return;
+    const uint8_t *__restrict__ Ws, int M, int N, int K, uint16_t *__restrict__ Y, int vec) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  constexpr int IB = TL::IB, JB = TL::JB, RA = TL::RA, RW = TL::RW;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1, r = lane & 31, g = lane >> 5;
+  const int rowA = K / (FA ? 1 : 2), rowW = K / (FW ? 1 : 2), nb = K / 32;
+  const int T = (K + TL::KS - 1) / TL::KS;
+  const int nbm = (M + TL::TM - 1) / TL::TM, nbn = (N + TL::TN - 1) / TL::TN;
+  const int count = nbm * nbn;
+
+  // loads of a stage: piece idx = tid + 256 i of an operand, CA / CW pieces a row
+  constexpr int CA = RA / 16, CW = RW / 16;
+  constexpr int LA = (TL::TM * CA + 255) / 256, LW = (TL::TN * CW + 255) / 256;
+  // (fewer pieces than threads: the upper half repeats the lower half's work)
+  const int ta = tid % (TL::TM * CA < 256 ? TL::TM * CA : 256);
+  const int tw = tid % (TL::TN * CW < 256 ? TL::TN * CW : 256);
+  const int ra0 = ta / CA, ca0 = ta % CA, rw0 = tw / CW, cw0 = tw % CW;
+  const int dstA = ra0 * RA + ((ca0 ^ swizzle<RA>(ra0)) << 4);
+  const int dstW = TL::AB + rw0 * RW + ((cw0 ^ swizzle<RW>(rw0)) << 4);
+  // fragments: the pieces of lane (r, g); step 1 of a 128-element stage and the
+  // second half of an 8-bit fragment are one flipped bit away
+  const int arow = wm * 32 * IB + r, wrow = wn * 32 * JB + r;
+  const int fa0 = arow * RA + (((FA ? g : TL::STEPS * g) ^ swizzle<RA>(r)) << 4);
+  const int fw0 = TL::AB + wrow * RW + (((FW ? g : TL::STEPS * g) ^ swizzle<RW>(r)) << 4);
+  const int sa0 = TL::SC0 + 4 * arow + TL::STEPS * g, sw0 = TL::SC0 + 4 * (TL::TM + wrow) + TL::STEPS * g;
+
+  for (int v = blockIdx.x; v < count; v += gridDim.x) {
+    // each XCD takes a contiguous run of the tile order
+    const int xcd = v & 7, per = count >> 3, rem = count & 7;
+    int tm, tn;
+    tile_of(xcd * per + (xcd < rem ? xcd : rem) + (v >> 3), nbm, nbn, tm, tn);
+    const int m0 = tm * TL::TM, n0 = tn * TL::TN;
+    const int mr = M - m0 < TL::TM ? M - m0 : TL::TM, nr = N - n0 < TL::TN ? N - n0 : TL::TN;
+    // rows past the last give zeros (outside the buffer)
+    const __amdgpu_buffer_rsrc_t bufA = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(A + (int64_t)m0 * rowA), 0, mr * rowA, 0x00027000);
+    const __amdgpu_buffer_rsrc_t bufW = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(W + (int64_t)n0 * rowW), 0, nr * rowW, 0x00027000);
+
+    // piece k of a stage: activations first.  Pieces past K and whole stages
+    // past the last are sent outside the buffer as well: zeros.
+    u32x4 st[LA + LW];
+    auto load_piece = [&](int t, int k) {
+      if (k < LA) {
+        const bool in = ca0 * 16 < rowA - t * RA;
+        st[k] = buf_load(bufA, in ? (ra0 + k * (256 / CA)) * rowA + ca0 * 16 : 0x7ffffff0u, t * RA);
+      } else {
+        const bool in = cw0 * 16 < rowW - t * RW;
+        st[k] = buf_load(bufW, in ? (rw0 + (k - LA) * (256 / CW)) * rowW + cw0 * 16 : 0x7ffffff0u, t * RW);
+      }
+    };
+    auto store_piece = [&](int buf, int k) {
+      *(u32x4 *)(lds + buf * TL::STAGE + (k < LA ? dstA + k * 4096 : dstW + (k - LA) * 4096)) = st[k];
+    };
+
+    // Scales: 16 blocks of every row at a time, one 16-byte load a row (its
+    // address has no alignment).  A last, partial group goes byte by byte
+    // straight to LDS, zero past K.
+    constexpr int LS = (TL::SROWS + 255) / 256;
+    u32x4 sts[LS];
+    auto group_rows = [&](auto f) {
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int n = n0 + 4 * g + i;
-    if (n < N) Y[(int64_t)m * N + n] = __builtin_bit_cast(uint16_t, (__bf16)acc[i]);
+      for (int i = 0; i < LS; i++) {
+        const int row = tid + 256 * i;
+        if (row < TL::SROWS) {
+          const bool isw = row >= TL::TM;
+          const int lr = isw ? row - TL::TM : row, n = (isw ? nr : mr) - 1;
+          f(i, row, (isw ? Ws : As) + (int64_t)((isw ? n0 : m0) + (lr < n ? lr : n)) * nb);
+        }
+      }
+    };
+    auto load_group = [&](int grp) {
+      if (16 * grp + 16 <= nb) {
+        group_rows([&](int i, int, const uint8_t *p) { __builtin_memcpy(&sts[i], p + 16 * grp, 16); });
+      } else {
+        uint8_t *b = lds + TL::SC0 + (grp & 1) * TL::SBUF;
+        group_rows([&](int, int row, const uint8_t *p) {
+#pragma unroll 1
+          for (int k = 0; k < 16; k++)
+            b[((k >> 2) * TL::SROWS + row) * 4 + (k & 3)] = 16 * grp + k < nb ? p[16 * grp + k] : 0;
+        });
+      }
+    };
+    auto store_group = [&](int grp) {
+      if (16 * grp + 16 > nb) return;
+      uint8_t *b = lds + TL::SC0 + (grp & 1) * TL::SBUF;
+      group_rows([&](int i, int row, const uint8_t *) {
+#pragma unroll
+        for (int p = 0; p < 4; p++) *(uint32_t *)(b + (p * TL::SROWS + row) * 4) = sts[i][p];
+      });
+    };
+
+    f32x16 acc[JB][IB];
+#pragma unroll
+    for (int j = 0; j < JB; j++)
+#pragma unroll
+      for (int i = 0; i < IB; i++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) acc[j][i][e] = 0.f;
+
+    Frag<FA> a[2][IB];
+    Frag<FW> w[2][JB];
+    int sa[2][IB], sw[2][JB];
+    // LDS read k of a step's fragments, in the order its products need them
+    constexpr int NRA = FA ? 2 : 1, NRW = FW ? 2 : 1, NR = JB * NRW + IB * NRA;
+    auto read_frag = [&](int buf, int step, Frag<FA> *fa, Frag<FW> *fw, int k) {
+      const uint8_t *b = lds + buf * TL::STAGE;
+      const bool isa = k >= NRW && k < NRW + IB * NRA;  // w[0], every a, the other w
+      if (isa) {
+        const int i = (k - NRW) / NRA, h = (k - NRW) % NRA;
+        fa[i].v[h] = *(const u32x4 *)(b + (fa0 ^ (FA ? h << 5 : step << 4)) + i * 32 * RA);
+      } else {
+        const int q = k < NRW ? k : k - IB * NRA, j = q / NRW, h = q % NRW;
+        fw[j].v[h] = *(const u32x4 *)(b + (fw0 ^ (FW ? h << 5 : step << 4)) + j * 32 * RW);
+      }
+    };
+    // scale bytes of stage t, read k: blocks STEPS g + step of it in byte `step`
+    auto read_scale = [&](int t, int *xa, int *xw, int k) {
+      const int blk = t * (TL::KS / 32);
+      const uint8_t *b = lds + ((blk >> 4) & 1) * TL::SBUF + ((blk >> 2) & 3) * (TL::SROWS * 4) + (blk & 3);
+      const bool isa = k >= 1 && k < 1 + IB;
+      const int x = isa ? k - 1 : k < 1 ? 0 : k - IB;
+      const uint8_t *p = b + (isa ? sa0 : sw0) + 128 * x;
+      (isa ? xa : xw)[x] = TL::STEPS == 2 ? *(const uint16_t *)p : *p;
+    };
+    // product x of a step, column blocks first
+    auto multiply = [&](auto step, const Frag<FA> *fa, const Frag<FW> *fw, const int *xa, const int *xw,
+                        int x) {
+      constexpr int S = decltype(step)::value;
+      const int j = x / IB, i = x % IB;
+      acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          fw[j].op(), fa[i].op(), acc[j][i], FW ? 0 : 4, FA ? 0 : 4, S, xw[j], S, xa[i]);
+    };
+
+    __syncthreads();  // the previous tile's buffers are free
+    load_group(0);
+#pragma unroll
+    for (int k = 0; k < LA + LW; k++) load_piece(0, k);
+    store_group(0);
+#pragma unroll
+    for (int k = 0; k < LA + LW; k++) {
+      store_piece(0, k);
+      load_piece(1, k);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NR; k++) read_frag(0, 0, a[0], w[0], k);
+#pragma unroll
+    for (int k = 0; k < IB + JB; k++) read_scale(0, sa[0], sw[0], k);
+
+    // One stage t, in two parts with a barrier between.  Part one: stage t + 1
+    // goes from registers to the other LDS buffer and stage t + 2 is requested
+    // (and the stage's second step is read).  Part two: the first fragments
+    // and the scales of stage t + 1 are read.  Each memory operation is pinned
+    // behind a product, so that the matrix cores always have the next one.
+    using C0 = std::integral_constant<int, 0>;
+    using C1 = std::integral_constant<int, 1>;
+    auto stage = [&](int t, auto par) {
+      constexpr int P = decltype(par)::value;         // t & 1: LDS buffer and scale registers
+      constexpr bool TWO = TL::STEPS == 2;
+      constexpr int F0 = TWO ? 0 : P, F1 = TWO ? 0 : 1 - P;  // fragments of this and the next stage
+      constexpr int NM = IB * JB, NL = LA + LW;
+      constexpr int M1 = TWO ? NM : NM / 2, O1 = (TWO ? NR : 0) + 2 * NL;
+      constexpr int M2 = TWO ? NM : NM - NM / 2, O2 = NR + IB + JB;
+      auto first = [&](int k) {
+        if (TWO && k < NR) {
+          read_frag(P, 1, a[1], w[1], k);
+        } else {
+          const int q = k - (TWO ? NR : 0);
+          if (q % 2 == 0) store_piece(1 - P, q / 2);
+          else load_piece(t + 2, q / 2);
+        }
+      };
+      auto second = [&](int k) {
+        if (k < NR) read_frag(1 - P, 0, a[F1], w[F1], k);
+        else read_scale(t + 1, sa[1 - P], sw[1 - P], k - NR);
+      };
+      if constexpr (M1 == 0) {
+#pragma unroll
+        for (int k = 0; k < O1; k++) first(k);
+      }
+#pragma unroll
+      for (int x = 0; x < M1; x++) {
+        multiply(C0{}, a[F0], w[F0], sa[P], sw[P], x);
+#pragma unroll
+        for (int k = x * O1 / (M1 ? M1 : 1); k < (x + 1) * O1 / (M1 ? M1 : 1); k++) first(k);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const int ph = t & (TL::SPG - 1), grp = t / TL::SPG;
+      if ((grp + 1) * 16 < nb) {
+        if (ph == 0) load_group(grp + 1);
+        if (ph == TL::SPG / 2) store_group(grp + 1);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int x = 0; x < M2; x++) {
+        if constexpr (TWO) multiply(C1{}, a[1], w[1], sa[P], sw[P], x);
+        else multiply(C0{}, a[F0], w[F0], sa[P], sw[P], M1 + x);
+#pragma unroll
+        for (int k = x * O2 / M2; k < (x + 1) * O2 / M2; k++) second(k);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int t = 0;
+    for (; t + 1 < T; t += 2) {
+      stage(t, C0{});
+      stage(t + 1, C1{});
+    }
+    if (t < T) stage(t, C0{});
+
+    // Epilogue: 32 output rows of the wave's block at a time through the
+    // wave's own LDS region (16-byte pieces XOR-swizzled by the row), out as
+    // whole rows in 16-byte pieces.  Lane (r, g) holds row r, columns
+    // 32 j + 8 q + 4 g + (0..3).
+    uint8_t *reg = lds + TL::EP0 + wave * TL::EPI;
+    constexpr int PPR = 4 * JB;  // pieces per row
+    int lane_ = lane;            // opaque: keeps the addresses below out of the K loop's registers
+    asm volatile("" : "+v"(lane_));
+    const int er = lane_ & 31, eg = lane_ >> 5;
+#pragma unroll
+    for (int i = 0; i < IB; i++) {
+#pragma unroll
+      for (int j = 0; j < JB; j++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const bf16x2 p0 = {(__bf16)acc[j][i][4 * q], (__bf16)acc[j][i][4 * q + 1]};
+          const bf16x2 p1 = {(__bf16)acc[j][i][4 * q + 2], (__bf16)acc[j][i][4 * q + 3]};
+          *(u32x2 *)(reg + er * (64 * JB) + (((4 * j + q) ^ (er & (PPR - 1))) << 4) + 8 * eg) =
+              u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
+        }
+      __builtin_amdgcn_wave_barrier();  // LDS works in order within a wave
+      const int c = lane_ % PPR;
+#pragma unroll 4
+      for (int rr = lane_ / PPR; rr < 32; rr += 64 / PPR) {
+        const u32x4 o = *(const u32x4 *)(reg + rr * (64 * JB) + ((c ^ (rr & (PPR - 1))) << 4));
+        const int m = m0 + wm * 32 * IB + 32 * i + rr, n = n0 + wn * 32 * JB + 8 * c;
+        if (m >= M || n >= N) continue;
+        uint16_t *yp = Y + (int64_t)m * N + n;
+        if (vec && n + 7 < N) {
+          __builtin_nontemporal_store(o, (u32x4 *)yp);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; e++)
+            if (n + e < N) yp[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
   }
+}
+
+template <int FA, int FW, class TL>
+hipError_t launch_tiles(const MxLinearArgs &a, int cus) {
+  static std::atomic<uint64_t> lds_set{0};  // per instantiation and device
+  hipError_t e = ensure_lds_limit((const void *)mx_tile_kernel<FA, FW, TL>, TL::LDS, lds_set);
+  if (e != hipSuccess) return e;
+  const int64_t tiles = ((a.M + TL::TM - 1) / TL::TM) * ((a.N + TL::TN - 1) / TL::TN);
+  if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
+  const int64_t slots = (int64_t)cus * TL::WGS;
+  const int vec = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
+  hipLaunchKernelGGL((mx_tile_kernel<FA, FW, TL>), dim3((unsigned)(tiles < slots ? tiles : slots)),
+                     dim3(256), TL::LDS, a.stream, a.a_codes, a.a_scales, a.w_codes, a.w_scales,
+                     (int)a.M, (int)a.N, a.K, a.y, vec);
+  return hipGetLastError();
+}
+
+template <int FA, int FW>
+hipError_t launch_pair(const MxLinearArgs &a, int cus) {
+  const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+  const int64_t mid = ((a.M + 127) / 128) * ((a.N + 127) / 128);
+  if (big >= cus) return launch_tiles<FA, FW, MxTile<FA, FW, 4, 4, 1>>(a, cus);
+  if (mid >= cus) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 2, 2>>(a, cus);
+  return launch_tiles<FA, FW, MxTile<FA, FW, 1, 1, 4>>(a, cus);
 }
 
 }  // namespace
 
 hipError_t launch_mx_linear(const MxLinearArgs &a) {
-  const int64_t waves = ((a.M + 15) / 16) * ((a.N + 15) / 16), grid = (waves + 3) / 4;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-#define OQ_CASE(FA, FW)                                                                        \
-  if (a.a_format == FA && a.w_format == FW)                                                    \
-    hipLaunchKernelGGL((mx_linear_kernel<FA, FW>), dim3((unsigned)grid), dim3(256), 0, a.stream, \
-                       a.a_codes, a.a_scales, a.w_codes, a.w_scales, (int)a.M, (int)a.N, a.K, a.y);
-  OQ_CASE(0, 0) OQ_CASE(0, 1) OQ_CASE(1, 0) OQ_CASE(1, 1)
-#undef OQ_CASE
-  return hipGetLastError();
+  int cus = 256, dev = 0;
+  if (hipGetDevice(&dev) == hipSuccess)
+    (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (cus <= 0) cus = 256;
+  if (a.a_format == 0) return a.w_format == 0 ? launch_pair<0, 0>(a, cus) : launch_pair<0, 1>(a, cus);
+  return a.w_format == 0 ? launch_pair<1, 0>(a, cus) : launch_pair<1, 1>(a, cus);
 }
 
 }  // namespace oq
