@@ -45,21 +45,37 @@ struct MxTile {
   static constexpr int SBUF = 4 * SROWS * 4;     // scales of 16 blocks: 4 planes of one word a row
   static constexpr int SPG = 512 / KS;           // stages that one such group lasts
   static constexpr int EPI = 32 * 64 * JB;       // a wave's staging of 32 output rows
-  static constexpr int SC0 = 2 * STAGE, EP0 = SC0 + 2 * SBUF;
+  static constexpr int NST = 3;                  // stages in LDS
+  static constexpr int SC0 = NST * STAGE, EP0 = SC0 + 2 * SBUF;
   static constexpr int LDS = EP0 + 4 * EPI;
   static_assert(LDS * WGS <= 160 * 1024, "LDS of one CU");
 };
 
-// XOR swizzle of a row's 16-byte pieces in LDS: rows lie one after another,
-// so the stores are consecutive, and 8 or 16 rows' equal pieces fall into
-// different banks.
+// XOR swizzle of a row's 16-byte pieces in LDS (rows lie one after another).
+// A 16-byte LDS read serves lanes {0-3, 12-15, 20-23, 24-27} of 32 together,
+// then the others: of those, rows equal modulo 256 bytes differ in these bits.
 template <int RB>
 __device__ __forceinline__ int swizzle(int row) {
-  return RB == 64 ? ((row >> 1) ^ (row >> 3)) & 3 : ((row >> 2) ^ (row >> 3)) & 1;
+  return RB == 64 ? (row >> 2) & 3 : (row >> 3) & 1;
 }
 
-__device__ __forceinline__ u32x4 buf_load(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t base) {
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, base, 0));
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 64 lanes x 16 bytes from memory straight to LDS, lane after lane from `dst`
+// (uniform); lanes outside the buffer write zeros.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint8_t *dst, uint32_t off,
+                                            uint32_t base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)dst, 16, off, base, 0, 0);
+}
+
+// Waits until at most N of this wave's memory requests are outstanding and
+// its LDS requests are done, then for the other waves.
+template <int N>
+__device__ __forceinline__ void wait_and_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // Group-major tile order: index g -> tile (tm, tn), kGroupM tile rows per
@@ -94,15 +110,17 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
   const int nbm = (M + TL::TM - 1) / TL::TM, nbn = (N + TL::TN - 1) / TL::TN;
   const int count = nbm * nbn;
 
-  // loads of a stage: piece idx = tid + 256 i of an operand, CA / CW pieces a row
+  // Loads of a stage: piece idx = tid + 256 k of an operand, CA / CW pieces a
+  // row; the thread of LDS slot s of a row brings the row's piece s ^ swizzle.
   constexpr int CA = RA / 16, CW = RW / 16;
-  constexpr int LA = (TL::TM * CA + 255) / 256, LW = (TL::TN * CW + 255) / 256;
-  // (fewer pieces than threads: the upper half repeats the lower half's work)
-  const int ta = tid % (TL::TM * CA < 256 ? TL::TM * CA : 256);
-  const int tw = tid % (TL::TN * CW < 256 ? TL::TN * CW : 256);
-  const int ra0 = ta / CA, ca0 = ta % CA, rw0 = tw / CW, cw0 = tw % CW;
-  const int dstA = ra0 * RA + ((ca0 ^ swizzle<RA>(ra0)) << 4);
-  const int dstW = TL::AB + rw0 * RW + ((cw0 ^ swizzle<RW>(rw0)) << 4);
+  constexpr int PA = TL::TM * CA, PW = TL::TN * CW;  // pieces
+  constexpr int LA = (PA + 255) / 256, LW = (PW + 255) / 256, NL = LA + LW;
+  // (fewer pieces than threads: the upper waves repeat the lower ones' work)
+  const int ta = tid % (PA < 256 ? PA : 256), tw = tid % (PW < 256 ? PW : 256);
+  const int ra0 = ta / CA, ca0 = (ta % CA) ^ swizzle<RA>(ra0);
+  const int rw0 = tw / CW, cw0 = (tw % CW) ^ swizzle<RW>(rw0);
+  const int uw = __builtin_amdgcn_readfirstlane(wave);
+  const int la0 = (uw * 1024) % (PA * 16), lw0 = TL::AB + (uw * 1024) % (PW * 16);
   // fragments: the pieces of lane (r, g); step 1 of a 128-element stage and the
   // second half of an 8-bit fragment are one flipped bit away
   const int arow = wm * 32 * IB + r, wrow = wn * 32 * JB + r;
@@ -110,34 +128,41 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
   const int fw0 = TL::AB + wrow * RW + (((FW ? g : TL::STEPS * g) ^ swizzle<RW>(r)) << 4);
   const int sa0 = TL::SC0 + 4 * arow + TL::STEPS * g, sw0 = TL::SC0 + 4 * (TL::TM + wrow) + TL::STEPS * g;
 
-  for (int v = blockIdx.x; v < count; v += gridDim.x) {
-    // each XCD takes a contiguous run of the tile order
+  struct Tile {
+    int m0, n0, mr, nr;  // origin, rows and columns inside the matrix
+    __amdgpu_buffer_rsrc_t a, w;
+  };
+  // each XCD takes a contiguous run of the tile order; rows past the last lie
+  // outside the buffers
+  auto tile_at = [&](int v) {
     const int xcd = v & 7, per = count >> 3, rem = count & 7;
     int tm, tn;
     tile_of(xcd * per + (xcd < rem ? xcd : rem) + (v >> 3), nbm, nbn, tm, tn);
-    const int m0 = tm * TL::TM, n0 = tn * TL::TN;
-    const int mr = M - m0 < TL::TM ? M - m0 : TL::TM, nr = N - n0 < TL::TN ? N - n0 : TL::TN;
-    // rows past the last give zeros (outside the buffer)
-    const __amdgpu_buffer_rsrc_t bufA = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(A + (int64_t)m0 * rowA), 0, mr * rowA, 0x00027000);
-    const __amdgpu_buffer_rsrc_t bufW = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(W + (int64_t)n0 * rowW), 0, nr * rowW, 0x00027000);
+    Tile x;
+    x.m0 = tm * TL::TM, x.n0 = tn * TL::TN;
+    x.mr = M - x.m0 < TL::TM ? M - x.m0 : TL::TM, x.nr = N - x.n0 < TL::TN ? N - x.n0 : TL::TN;
+    x.a = __builtin_amdgcn_make_buffer_rsrc((void *)(A + (int64_t)x.m0 * rowA), 0, x.mr * rowA, 0x00027000);
+    x.w = __builtin_amdgcn_make_buffer_rsrc((void *)(W + (int64_t)x.n0 * rowW), 0, x.nr * rowW, 0x00027000);
+    return x;
+  };
+  // piece k of stage t of a tile into LDS stage `buf`: activations first.
+  // Pieces past K and stages past the last are sent outside the buffers.
+  auto load_piece = [&](const Tile &x, int t, int buf, int k) {
+    uint8_t *b = lds + buf * TL::STAGE;
+    if (k < LA) {
+      const bool in = ca0 * 16 < rowA - t * RA;
+      load_to_lds(x.a, b + la0 + k * 4096, in ? (ra0 + k * (256 / CA)) * rowA + ca0 * 16 : 0x7ffffff0u,
+                  t * RA);
+    } else {
+      const bool in = cw0 * 16 < rowW - t * RW;
+      load_to_lds(x.w, b + lw0 + (k - LA) * 4096,
+                  in ? (rw0 + (k - LA) * (256 / CW)) * rowW + cw0 * 16 : 0x7ffffff0u, t * RW);
+    }
+  };
 
-    // piece k of a stage: activations first.  Pieces past K and whole stages
-    // past the last are sent outside the buffer as well: zeros.
-    u32x4 st[LA + LW];
-    auto load_piece = [&](int t, int k) {
-      if (k < LA) {
-        const bool in = ca0 * 16 < rowA - t * RA;
-        st[k] = buf_load(bufA, in ? (ra0 + k * (256 / CA)) * rowA + ca0 * 16 : 0x7ffffff0u, t * RA);
-      } else {
-        const bool in = cw0 * 16 < rowW - t * RW;
-        st[k] = buf_load(bufW, in ? (rw0 + (k - LA) * (256 / CW)) * rowW + cw0 * 16 : 0x7ffffff0u, t * RW);
-      }
-    };
-    auto store_piece = [&](int buf, int k) {
-      *(u32x4 *)(lds + buf * TL::STAGE + (k < LA ? dstA + k * 4096 : dstW + (k - LA) * 4096)) = st[k];
-    };
+  for (int v = blockIdx.x; v < count; v += gridDim.x) {
+    const Tile x = tile_at(v);
+    const int m0 = x.m0, n0 = x.n0, mr = x.mr, nr = x.nr;
 
     // Scales: 16 blocks of every row at a time, one 16-byte load a row (its
     // address has no alignment).  A last, partial group goes byte by byte
@@ -190,7 +215,7 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
     // LDS read k of a step's fragments, in the order its products need them
     constexpr int NRA = FA ? 2 : 1, NRW = FW ? 2 : 1, NR = JB * NRW + IB * NRA;
     auto read_frag = [&](int buf, int step, Frag<FA> *fa, Frag<FW> *fw, int k) {
-      const uint8_t *b = lds + buf * TL::STAGE;
+      const uint8_t *b = lds + buf;
       const bool isa = k >= NRW && k < NRW + IB * NRA;  // w[0], every a, the other w
       if (isa) {
         const int i = (k - NRW) / NRA, h = (k - NRW) % NRA;
@@ -218,58 +243,40 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
           fw[j].op(), fa[i].op(), acc[j][i], FW ? 0 : 4, FA ? 0 : 4, S, xw[j], S, xa[i]);
     };
 
-    __syncthreads();  // the previous tile's buffers are free
     load_group(0);
 #pragma unroll
-    for (int k = 0; k < LA + LW; k++) load_piece(0, k);
-    store_group(0);
+    for (int t = 0; t < TL::NST; t++)
 #pragma unroll
-    for (int k = 0; k < LA + LW; k++) {
-      store_piece(0, k);
-      load_piece(1, k);
-    }
-    __syncthreads();
+      for (int k = 0; k < NL; k++) load_piece(x, t, t, k);
+    store_group(0);
+    wait_and_sync<(TL::NST - 1) * NL>();
 #pragma unroll
     for (int k = 0; k < NR; k++) read_frag(0, 0, a[0], w[0], k);
 #pragma unroll
     for (int k = 0; k < IB + JB; k++) read_scale(0, sa[0], sw[0], k);
 
-    // One stage t, in two parts with a barrier between.  Part one: stage t + 1
-    // goes from registers to the other LDS buffer and stage t + 2 is requested
-    // (and the stage's second step is read).  Part two: the first fragments
-    // and the scales of stage t + 1 are read.  Each memory operation is pinned
-    // behind a product, so that the matrix cores always have the next one.
+    // One stage t, in two parts with a barrier between that sees stage t + 1
+    // arrived and this stage's LDS buffer read for the last time.  Part one:
+    // the stage's second step is read.  Part two: the first fragments and the
+    // scales of stage t + 1 are read, and stage t + 3 is requested into this
+    // stage's buffer.  Each memory operation is pinned behind a product, so
+    // that the matrix cores always have the next one.
     using C0 = std::integral_constant<int, 0>;
     using C1 = std::integral_constant<int, 1>;
+    int cur = 0;  // LDS buffer of the stage, then of the next
     auto stage = [&](int t, auto par) {
-      constexpr int P = decltype(par)::value;         // t & 1: LDS buffer and scale registers
+      constexpr int P = decltype(par)::value;         // t & 1: scale registers
       constexpr bool TWO = TL::STEPS == 2;
       constexpr int F0 = TWO ? 0 : P, F1 = TWO ? 0 : 1 - P;  // fragments of this and the next stage
-      constexpr int NM = IB * JB, NL = LA + LW;
-      constexpr int M1 = TWO ? NM : NM / 2, O1 = (TWO ? NR : 0) + 2 * NL;
-      constexpr int M2 = TWO ? NM : NM - NM / 2, O2 = NR + IB + JB;
-      auto first = [&](int k) {
-        if (TWO && k < NR) {
-          read_frag(P, 1, a[1], w[1], k);
-        } else {
-          const int q = k - (TWO ? NR : 0);
-          if (q % 2 == 0) store_piece(1 - P, q / 2);
-          else load_piece(t + 2, q / 2);
-        }
-      };
-      auto second = [&](int k) {
-        if (k < NR) read_frag(1 - P, 0, a[F1], w[F1], k);
-        else read_scale(t + 1, sa[1 - P], sw[1 - P], k - NR);
-      };
-      if constexpr (M1 == 0) {
+      constexpr int NM = IB * JB;
+      constexpr int M1 = TWO ? NM : NM / 4, M2 = TWO ? NM : NM - NM / 4;
+      constexpr int O1 = TWO ? NR : 0, O2 = NR + IB + JB + NL;
+      const int nxt = cur + 1 == TL::NST ? 0 : cur + 1;
 #pragma unroll
-        for (int k = 0; k < O1; k++) first(k);
-      }
+      for (int k = 0; k < M1; k++) {
+        multiply(C0{}, a[F0], w[F0], sa[P], sw[P], k);
 #pragma unroll
-      for (int x = 0; x < M1; x++) {
-        multiply(C0{}, a[F0], w[F0], sa[P], sw[P], x);
-#pragma unroll
-        for (int k = x * O1 / (M1 ? M1 : 1); k < (x + 1) * O1 / (M1 ? M1 : 1); k++) first(k);
+        for (int o = k * O1 / M1; o < (k + 1) * O1 / M1; o++) read_frag(cur * TL::STAGE, 1, a[1], w[1], o);
         __builtin_amdgcn_sched_barrier(0);
       }
       const int ph = t & (TL::SPG - 1), grp = t / TL::SPG;
@@ -277,15 +284,20 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
         if (ph == 0) load_group(grp + 1);
         if (ph == TL::SPG / 2) store_group(grp + 1);
       }
-      __syncthreads();
+      wait_and_sync<(TL::NST - 2) * NL>();
 #pragma unroll
-      for (int x = 0; x < M2; x++) {
-        if constexpr (TWO) multiply(C1{}, a[1], w[1], sa[P], sw[P], x);
-        else multiply(C0{}, a[F0], w[F0], sa[P], sw[P], M1 + x);
+      for (int k = 0; k < M2; k++) {
+        if constexpr (TWO) multiply(C1{}, a[1], w[1], sa[P], sw[P], k);
+        else multiply(C0{}, a[F0], w[F0], sa[P], sw[P], M1 + k);
 #pragma unroll
-        for (int k = x * O2 / M2; k < (x + 1) * O2 / M2; k++) second(k);
+        for (int o = k * O2 / M2; o < (k + 1) * O2 / M2; o++) {
+          if (o < NR) read_frag(nxt * TL::STAGE, 0, a[F1], w[F1], o);
+          else if (o < NR + IB + JB) read_scale(t + 1, sa[1 - P], sw[1 - P], o - NR);
+          else load_piece(x, t + TL::NST, cur, o - NR - IB - JB);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
+      cur = nxt;
     };
     int t = 0;
     for (; t + 1 < T; t += 2) {
@@ -293,6 +305,7 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
       stage(t + 1, C1{});
     }
     if (t < T) stage(t, C0{});
+    wait_and_sync<0>();  // the requests past the last stage are done, every buffer is free
 
     // Epilogue: 32 output rows of the wave's block at a time through the
     // wave's own LDS region (16-byte pieces XOR-swizzled by the row), out as
