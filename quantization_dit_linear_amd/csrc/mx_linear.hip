@@ -115,6 +115,8 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
   constexpr int CA = RA / 16, CW = RW / 16;
   constexpr int PA = TL::TM * CA, PW = TL::TN * CW;  // pieces
   constexpr int LA = (PA + 255) / 256, LW = (PW + 255) / 256, NL = LA + LW;
+  // pieces requested in part one and in part two of a stage
+  constexpr int LP1 = TL::STEPS == 2 ? NL / 2 : IB * JB >= 16 ? NL / 4 : 0, LP2 = NL - LP1;
   // (fewer pieces than threads: the upper waves repeat the lower ones' work)
   const int ta = tid % (PA < 256 ? PA : 256), tw = tid % (PW < 256 ? PW : 256);
   const int ra0 = ta / CA, ca0 = (ta % CA) ^ swizzle<RA>(ra0);
@@ -247,9 +249,9 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
 #pragma unroll
     for (int t = 0; t < TL::NST; t++)
 #pragma unroll
-      for (int k = 0; k < NL; k++) load_piece(x, t, t, k);
+      for (int k = 0; k < (t + 1 < TL::NST ? NL : LP2); k++) load_piece(x, t, t, k);
     store_group(0);
-    wait_and_sync<(TL::NST - 1) * NL>();
+    wait_and_sync<(TL::NST - 2) * NL + LP2>();
 #pragma unroll
     for (int k = 0; k < NR; k++) read_frag(0, 0, a[0], w[0], k);
 #pragma unroll
@@ -257,10 +259,11 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
 
     // One stage t, in two parts with a barrier between that sees stage t + 1
     // arrived and this stage's LDS buffer read for the last time.  Part one:
-    // the stage's second step is read.  Part two: the first fragments and the
-    // scales of stage t + 1 are read, and stage t + 3 is requested into this
-    // stage's buffer.  Each memory operation is pinned behind a product, so
-    // that the matrix cores always have the next one.
+    // the stage's second step is read, and the rest of stage t + 2 requested.
+    // Part two: the first fragments and the scales of stage t + 1 are read,
+    // and the first pieces of stage t + 3 requested into this stage's buffer.
+    // Each memory operation is pinned behind a product, evenly, so that the
+    // matrix cores always have the next one.
     using C0 = std::integral_constant<int, 0>;
     using C1 = std::integral_constant<int, 1>;
     int cur = 0;  // LDS buffer of the stage, then of the next
@@ -269,14 +272,16 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
       constexpr bool TWO = TL::STEPS == 2;
       constexpr int F0 = TWO ? 0 : P, F1 = TWO ? 0 : 1 - P;  // fragments of this and the next stage
       constexpr int NM = IB * JB;
-      constexpr int M1 = TWO ? NM : NM / 4, M2 = TWO ? NM : NM - NM / 4;
-      constexpr int O1 = TWO ? NR : 0, O2 = NR + IB + JB + NL;
-      const int nxt = cur + 1 == TL::NST ? 0 : cur + 1;
+      constexpr int M1 = TWO ? NM : NM / 4, M2 = NM - (TWO ? 0 : NM / 4);
+      constexpr int R1 = TWO ? NR : 0, R2 = NR + IB + JB;  // LDS reads
+      const int nxt = cur + 1 == TL::NST ? 0 : cur + 1, prv = cur == 0 ? TL::NST - 1 : cur - 1;
 #pragma unroll
       for (int k = 0; k < M1; k++) {
         multiply(C0{}, a[F0], w[F0], sa[P], sw[P], k);
 #pragma unroll
-        for (int o = k * O1 / M1; o < (k + 1) * O1 / M1; o++) read_frag(cur * TL::STAGE, 1, a[1], w[1], o);
+        for (int o = k * R1 / M1; o < (k + 1) * R1 / M1; o++) read_frag(cur * TL::STAGE, 1, a[1], w[1], o);
+#pragma unroll
+        for (int o = k * LP1 / M1; o < (k + 1) * LP1 / M1; o++) load_piece(x, t + 2, prv, LP2 + o);
         __builtin_amdgcn_sched_barrier(0);
       }
       const int ph = t & (TL::SPG - 1), grp = t / TL::SPG;
@@ -290,11 +295,12 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
         if constexpr (TWO) multiply(C1{}, a[1], w[1], sa[P], sw[P], k);
         else multiply(C0{}, a[F0], w[F0], sa[P], sw[P], M1 + k);
 #pragma unroll
-        for (int o = k * O2 / M2; o < (k + 1) * O2 / M2; o++) {
+        for (int o = k * R2 / M2; o < (k + 1) * R2 / M2; o++) {
           if (o < NR) read_frag(nxt * TL::STAGE, 0, a[F1], w[F1], o);
-          else if (o < NR + IB + JB) read_scale(t + 1, sa[1 - P], sw[1 - P], o - NR);
-          else load_piece(x, t + TL::NST, cur, o - NR - IB - JB);
+          else read_scale(t + 1, sa[1 - P], sw[1 - P], o - NR);
         }
+#pragma unroll
+        for (int o = k * LP2 / M2; o < (k + 1) * LP2 / M2; o++) load_piece(x, t + TL::NST, cur, o);
         __builtin_amdgcn_sched_barrier(0);
       }
       cur = nxt;
