@@ -35,18 +35,19 @@ template <int FA, int FW, int IB_, int JB_, int WGS_>
 struct MxTile {
   static constexpr int IB = IB_, JB = JB_, WGS = WGS_;
   static constexpr int TM = 64 * IB, TN = 64 * JB;
-  // elements of K a stage: the same matrix-core time with 4-bit elements on
-  // both sides as with 8-bit ones, which run at half the rate
-  static constexpr int KS = (FA || FW) ? 64 : 128;
-  static constexpr int STEPS = KS / 64;
+  // Elements of K a stage: 128 bytes of a row (64 of 4-bit weights against
+  // 8-bit activations), so that a row's request is a whole line of the L2,
+  // and the same matrix-core time either way (8-bit elements run at half rate).
+  static constexpr int KS = (FA || FW) ? 128 : 256;
+  static constexpr int STEPS = KS / 64;                                 // products in depth
   static constexpr int RA = KS / (FA ? 1 : 2), RW = KS / (FW ? 1 : 2);  // row bytes a stage
   static constexpr int AB = TM * RA, STAGE = AB + TN * RW;
   static constexpr int SROWS = TM + TN;
   static constexpr int SBUF = 4 * SROWS * 4;     // scales of 16 blocks: 4 planes of one word a row
   static constexpr int SPG = 512 / KS;           // stages that one such group lasts
-  static constexpr int EPI = 32 * 64 * JB;       // a wave's staging of 32 output rows
-  static constexpr int NST = 3;                  // stages in LDS
-  static constexpr int SC0 = NST * STAGE, EP0 = SC0 + 2 * SBUF;
+  static constexpr int EROWS = 16;               // output rows a wave stages at once
+  static constexpr int EPI = EROWS * 64 * JB;
+  static constexpr int SC0 = 2 * STAGE, EP0 = SC0 + 2 * SBUF;
   static constexpr int LDS = EP0 + 4 * EPI;
   static_assert(LDS * WGS <= 160 * 1024, "LDS of one CU");
 };
@@ -56,7 +57,7 @@ struct MxTile {
 // then the others: of those, rows equal modulo 256 bytes differ in these bits.
 template <int RB>
 __device__ __forceinline__ int swizzle(int row) {
-  return RB == 64 ? (row >> 2) & 3 : (row >> 3) & 1;
+  return RB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
 }
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -114,21 +115,25 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
   // row; the thread of LDS slot s of a row brings the row's piece s ^ swizzle.
   constexpr int CA = RA / 16, CW = RW / 16;
   constexpr int PA = TL::TM * CA, PW = TL::TN * CW;  // pieces
-  constexpr int LA = (PA + 255) / 256, LW = (PW + 255) / 256, NL = LA + LW;
-  // pieces requested in part one and in part two of a stage
-  constexpr int LP1 = TL::STEPS == 2 ? NL / 2 : IB * JB >= 16 ? NL / 4 : 0, LP2 = NL - LP1;
-  // (fewer pieces than threads: the upper waves repeat the lower ones' work)
-  const int ta = tid % (PA < 256 ? PA : 256), tw = tid % (PW < 256 ? PW : 256);
-  const int ra0 = ta / CA, ca0 = (ta % CA) ^ swizzle<RA>(ra0);
-  const int rw0 = tw / CW, cw0 = (tw % CW) ^ swizzle<RW>(rw0);
+  constexpr int LA = PA / 256, LW = PW / 256, NL = LA + LW;
+  // pieces requested in the last step of a stage, the others in the first of the next
+  constexpr int LL = TL::STEPS == 4 ? NL / 2 : NL;
+  static_assert(PA % 256 == 0 && PW % 256 == 0, "whole rounds of requests");
+  const int ra0 = tid / CA, ca0 = (tid % CA) ^ swizzle<RA>(ra0);
+  const int rw0 = tid / CW, cw0 = (tid % CW) ^ swizzle<RW>(rw0);
   const int uw = __builtin_amdgcn_readfirstlane(wave);
-  const int la0 = (uw * 1024) % (PA * 16), lw0 = TL::AB + (uw * 1024) % (PW * 16);
-  // fragments: the pieces of lane (r, g); step 1 of a 128-element stage and the
-  // second half of an 8-bit fragment are one flipped bit away
+  const int la0 = uw * 1024, lw0 = TL::AB + uw * 1024;
+  // Fragments.  Of a stage's 2 STEPS blocks, step j multiplies blocks j and
+  // STEPS + j; lane (r, g) takes 4-bit block STEPS g + j, piece STEPS g + j
+  // of the row, or of 8-bit blocks j (h = 0) and STEPS + j (h = 1) piece
+  // 2 j + 4 h + g.  Pieces differ in the bits of j and h alone, which the
+  // swizzle leaves exclusive-or apart.
   const int arow = wm * 32 * IB + r, wrow = wn * 32 * JB + r;
   const int fa0 = arow * RA + (((FA ? g : TL::STEPS * g) ^ swizzle<RA>(r)) << 4);
   const int fw0 = TL::AB + wrow * RW + (((FW ? g : TL::STEPS * g) ^ swizzle<RW>(r)) << 4);
-  const int sa0 = TL::SC0 + 4 * arow + TL::STEPS * g, sw0 = TL::SC0 + 4 * (TL::TM + wrow) + TL::STEPS * g;
+  // the lane's scale bytes of a stage: blocks STEPS g .. STEPS g + STEPS - 1
+  const int sp = TL::STEPS == 4 ? g * TL::SROWS * 4 : 2 * g;
+  const int sa0 = TL::SC0 + 4 * arow + sp, sw0 = TL::SC0 + 4 * (TL::TM + wrow) + sp;
 
   struct Tile {
     int m0, n0, mr, nr;  // origin, rows and columns inside the matrix
@@ -213,143 +218,150 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
 
     Frag<FA> a[2][IB];
     Frag<FW> w[2][JB];
-    int sa[2][IB], sw[2][JB];
+    int sa[IB], sw[JB], sa1[IB], sw1[JB];
     // LDS read k of a step's fragments, in the order its products need them
     constexpr int NRA = FA ? 2 : 1, NRW = FW ? 2 : 1, NR = JB * NRW + IB * NRA;
-    auto read_frag = [&](int buf, int step, Frag<FA> *fa, Frag<FW> *fw, int k) {
-      const uint8_t *b = lds + buf;
+    auto read_frag = [&](int buf, int step, int k) {
+      const uint8_t *b = lds + buf * TL::STAGE;
       const bool isa = k >= NRW && k < NRW + IB * NRA;  // w[0], every a, the other w
       if (isa) {
         const int i = (k - NRW) / NRA, h = (k - NRW) % NRA;
-        fa[i].v[h] = *(const u32x4 *)(b + (fa0 ^ (FA ? h << 5 : step << 4)) + i * 32 * RA);
+        a[step & 1][i].v[h] =
+            *(const u32x4 *)(b + (fa0 ^ (FA ? step << 5 | h << 6 : step << 4)) + i * 32 * RA);
       } else {
         const int q = k < NRW ? k : k - IB * NRA, j = q / NRW, h = q % NRW;
-        fw[j].v[h] = *(const u32x4 *)(b + (fw0 ^ (FW ? h << 5 : step << 4)) + j * 32 * RW);
+        w[step & 1][j].v[h] =
+            *(const u32x4 *)(b + (fw0 ^ (FW ? step << 5 | h << 6 : step << 4)) + j * 32 * RW);
       }
     };
-    // scale bytes of stage t, read k: blocks STEPS g + step of it in byte `step`
-    auto read_scale = [&](int t, int *xa, int *xw, int k) {
+    // scale bytes of stage t, read k: block STEPS g + j of it in byte j
+    auto read_scale = [&](int t, int k) {
       const int blk = t * (TL::KS / 32);
-      const uint8_t *b = lds + ((blk >> 4) & 1) * TL::SBUF + ((blk >> 2) & 3) * (TL::SROWS * 4) + (blk & 3);
+      const uint8_t *b = lds + ((blk >> 4) & 1) * TL::SBUF + ((blk >> 2) & 3) * (TL::SROWS * 4);
       const bool isa = k >= 1 && k < 1 + IB;
       const int x = isa ? k - 1 : k < 1 ? 0 : k - IB;
       const uint8_t *p = b + (isa ? sa0 : sw0) + 128 * x;
-      (isa ? xa : xw)[x] = TL::STEPS == 2 ? *(const uint16_t *)p : *p;
+      (isa ? sa1 : sw1)[x] = TL::STEPS == 4 ? *(const int *)p : *(const uint16_t *)p;
     };
-    // product x of a step, column blocks first
-    auto multiply = [&](auto step, const Frag<FA> *fa, const Frag<FW> *fw, const int *xa, const int *xw,
-                        int x) {
+    auto take_scales = [&] {
+#pragma unroll
+      for (int i = 0; i < IB; i++) sa[i] = sa1[i];
+#pragma unroll
+      for (int j = 0; j < JB; j++) sw[j] = sw1[j];
+    };
+    // product k of step S, column blocks first
+    auto multiply = [&](auto step, int k) {
       constexpr int S = decltype(step)::value;
-      const int j = x / IB, i = x % IB;
+      const int j = k / IB, i = k % IB;
       acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          fw[j].op(), fa[i].op(), acc[j][i], FW ? 0 : 4, FA ? 0 : 4, S, xw[j], S, xa[i]);
+          w[S & 1][j].op(), a[S & 1][i].op(), acc[j][i], FW ? 0 : 4, FA ? 0 : 4, S, sw[j], S, sa[i]);
     };
 
     load_group(0);
 #pragma unroll
-    for (int t = 0; t < TL::NST; t++)
+    for (int t = 0; t < 2; t++)
 #pragma unroll
-      for (int k = 0; k < (t + 1 < TL::NST ? NL : LP2); k++) load_piece(x, t, t, k);
+      for (int k = 0; k < (t ? LL : NL); k++) load_piece(x, t, t, k);
     store_group(0);
-    wait_and_sync<(TL::NST - 2) * NL + LP2>();
+    wait_and_sync<LL>();
 #pragma unroll
-    for (int k = 0; k < NR; k++) read_frag(0, 0, a[0], w[0], k);
+    for (int k = 0; k < NR; k++) read_frag(0, 0, k);
 #pragma unroll
-    for (int k = 0; k < IB + JB; k++) read_scale(0, sa[0], sw[0], k);
+    for (int k = 0; k < IB + JB; k++) read_scale(0, k);
+    take_scales();
 
-    // One stage t, in two parts with a barrier between that sees stage t + 1
-    // arrived and this stage's LDS buffer read for the last time.  Part one:
-    // the stage's second step is read, and the rest of stage t + 2 requested.
-    // Part two: the first fragments and the scales of stage t + 1 are read,
-    // and the first pieces of stage t + 3 requested into this stage's buffer.
+    // One stage t: in each step but the last the next step's fragments are
+    // read.  Before the last step a barrier sees stage t + 1 arrived and this
+    // stage's LDS buffer read for the last time; in the last step the first
+    // fragments and the scales of stage t + 1 are read, and from there to the
+    // end of its first step stage t + 2 is requested into this stage's buffer.
     // Each memory operation is pinned behind a product, evenly, so that the
     // matrix cores always have the next one.
-    using C0 = std::integral_constant<int, 0>;
-    using C1 = std::integral_constant<int, 1>;
-    int cur = 0;  // LDS buffer of the stage, then of the next
-    auto stage = [&](int t, auto par) {
-      constexpr int P = decltype(par)::value;         // t & 1: scale registers
-      constexpr bool TWO = TL::STEPS == 2;
-      constexpr int F0 = TWO ? 0 : P, F1 = TWO ? 0 : 1 - P;  // fragments of this and the next stage
-      constexpr int NM = IB * JB;
-      constexpr int M1 = TWO ? NM : NM / 4, M2 = NM - (TWO ? 0 : NM / 4);
-      constexpr int R1 = TWO ? NR : 0, R2 = NR + IB + JB;  // LDS reads
-      const int nxt = cur + 1 == TL::NST ? 0 : cur + 1, prv = cur == 0 ? TL::NST - 1 : cur - 1;
+    constexpr int NM = IB * JB;
+    int cur = 0;
+    auto step = [&](int t, auto c) {
+      constexpr int S = decltype(c)::value;
+      constexpr bool LAST = S == TL::STEPS - 1;
+      constexpr int R = LAST ? NR + IB + JB : NR;
+      constexpr int L0 = LAST ? 0 : LL, L1 = LAST ? LL : S == 0 ? NL : LL;
 #pragma unroll
-      for (int k = 0; k < M1; k++) {
-        multiply(C0{}, a[F0], w[F0], sa[P], sw[P], k);
+      for (int k = 0; k < NM; k++) {
+        multiply(c, k);
 #pragma unroll
-        for (int o = k * R1 / M1; o < (k + 1) * R1 / M1; o++) read_frag(cur * TL::STAGE, 1, a[1], w[1], o);
-#pragma unroll
-        for (int o = k * LP1 / M1; o < (k + 1) * LP1 / M1; o++) load_piece(x, t + 2, prv, LP2 + o);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      const int ph = t & (TL::SPG - 1), grp = t / TL::SPG;
-      if ((grp + 1) * 16 < nb) {
-        if (ph == 0) load_group(grp + 1);
-        if (ph == TL::SPG / 2) store_group(grp + 1);
-      }
-      wait_and_sync<(TL::NST - 2) * NL>();
-#pragma unroll
-      for (int k = 0; k < M2; k++) {
-        if constexpr (TWO) multiply(C1{}, a[1], w[1], sa[P], sw[P], k);
-        else multiply(C0{}, a[F0], w[F0], sa[P], sw[P], M1 + k);
-#pragma unroll
-        for (int o = k * R2 / M2; o < (k + 1) * R2 / M2; o++) {
-          if (o < NR) read_frag(nxt * TL::STAGE, 0, a[F1], w[F1], o);
-          else read_scale(t + 1, sa[1 - P], sw[1 - P], o - NR);
+        for (int o = k * R / NM; o < (k + 1) * R / NM; o++) {
+          if (!LAST) read_frag(cur, S + 1, o);
+          else if (o < NR) read_frag(cur ^ 1, 0, o);
+          else read_scale(t + 1, o - NR);
         }
+        // pieces LL .. NL of stage t + 1, or 0 .. LL of stage t + 2
 #pragma unroll
-        for (int o = k * LP2 / M2; o < (k + 1) * LP2 / M2; o++) load_piece(x, t + TL::NST, cur, o);
+        for (int o = L0 + k * (L1 - L0) / NM; o < L0 + (k + 1) * (L1 - L0) / NM; o++)
+          load_piece(x, LAST ? t + 2 : t + 1, LAST ? cur : cur ^ 1, o);
         __builtin_amdgcn_sched_barrier(0);
       }
-      cur = nxt;
     };
-    int t = 0;
-    for (; t + 1 < T; t += 2) {
-      stage(t, C0{});
-      stage(t + 1, C1{});
+    for (int t = 0; t < T; t++) {
+      const int ph = t & (TL::SPG - 1), grp = t / TL::SPG;
+      const bool more = (grp + 1) * 16 < nb;
+      if (more && ph == 0) load_group(grp + 1);
+      step(t, std::integral_constant<int, 0>{});
+      if constexpr (TL::STEPS == 4) {
+        step(t, std::integral_constant<int, 1>{});
+        step(t, std::integral_constant<int, 2>{});
+      }
+      if (more && ph == TL::SPG / 2) store_group(grp + 1);
+      wait_and_sync<0>();
+      step(t, std::integral_constant<int, TL::STEPS - 1>{});
+      take_scales();
+      cur ^= 1;
     }
-    if (t < T) stage(t, C0{});
     wait_and_sync<0>();  // the requests past the last stage are done, every buffer is free
 
-    // Epilogue: 32 output rows of the wave's block at a time through the
+    // Epilogue: EROWS output rows of the wave's block at a time through the
     // wave's own LDS region (16-byte pieces XOR-swizzled by the row), out as
     // whole rows in 16-byte pieces.  Lane (r, g) holds row r, columns
-    // 32 j + 8 q + 4 g + (0..3).
+    // 32 j + 8 q + 4 g + (0..3); half of the lanes have a row of the pass.
     uint8_t *reg = lds + TL::EP0 + wave * TL::EPI;
-    constexpr int PPR = 4 * JB;  // pieces per row
-    int lane_ = lane;            // opaque: keeps the addresses below out of the K loop's registers
+    constexpr int PPR = 4 * JB, ER = TL::EROWS;  // pieces per row
+    int lane_ = lane;  // opaque: keeps the addresses below out of the K loop's registers
     asm volatile("" : "+v"(lane_));
-    const int er = lane_ & 31, eg = lane_ >> 5;
+    const int er = lane_ & (ER - 1), eg = lane_ >> 5, c = lane_ % PPR;
+    const int mw = m0 + wm * 32 * IB, n = n0 + wn * 32 * JB + 8 * c;
 #pragma unroll
     for (int i = 0; i < IB; i++) {
 #pragma unroll
-      for (int j = 0; j < JB; j++)
+      for (int half = 0; half < 32 / ER; half++) {
+        if (((lane_ >> 4) & 1) == half) {
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const bf16x2 p0 = {(__bf16)acc[j][i][4 * q], (__bf16)acc[j][i][4 * q + 1]};
-          const bf16x2 p1 = {(__bf16)acc[j][i][4 * q + 2], (__bf16)acc[j][i][4 * q + 3]};
-          *(u32x2 *)(reg + er * (64 * JB) + (((4 * j + q) ^ (er & (PPR - 1))) << 4) + 8 * eg) =
-              u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
-        }
-      __builtin_amdgcn_wave_barrier();  // LDS works in order within a wave
-      const int c = lane_ % PPR;
-#pragma unroll 4
-      for (int rr = lane_ / PPR; rr < 32; rr += 64 / PPR) {
-        const u32x4 o = *(const u32x4 *)(reg + rr * (64 * JB) + ((c ^ (rr & (PPR - 1))) << 4));
-        const int m = m0 + wm * 32 * IB + 32 * i + rr, n = n0 + wn * 32 * JB + 8 * c;
-        if (m >= M || n >= N) continue;
-        uint16_t *yp = Y + (int64_t)m * N + n;
-        if (vec && n + 7 < N) {
-          __builtin_nontemporal_store(o, (u32x4 *)yp);
-        } else {
+          for (int j = 0; j < JB; j++)
 #pragma unroll
-          for (int e = 0; e < 8; e++)
-            if (n + e < N) yp[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+            for (int q = 0; q < 4; q++) {
+              const bf16x2 p0 = {(__bf16)acc[j][i][4 * q], (__bf16)acc[j][i][4 * q + 1]};
+              const bf16x2 p1 = {(__bf16)acc[j][i][4 * q + 2], (__bf16)acc[j][i][4 * q + 3]};
+              *(u32x2 *)(reg + er * (64 * JB) + (((4 * j + q) ^ (er & (PPR - 1))) << 4) + 8 * eg) =
+                  u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
+            }
         }
+        __builtin_amdgcn_wave_barrier();  // LDS works in order within a wave
+        const int m1 = mw + 32 * i + ER * half;
+#pragma unroll
+        for (int k = 0; k < (ER * PPR + 63) / 64; k++) {
+          const int rr = lane_ / PPR + k * (64 / PPR);
+          const u32x4 o = *(const u32x4 *)(reg + rr * (64 * JB) + ((c ^ (rr & (PPR - 1))) << 4));
+          uint16_t *yp = Y + (int64_t)(m1 + rr) * N + n;
+          if (m1 + rr >= M || n >= N) continue;
+          if (vec) {
+            __builtin_nontemporal_store(o, (u32x4 *)yp);
+          } else {
+#pragma unroll 1
+            for (int e = 0; e < 8; e++) {
+              const uint32_t d = e & 4 ? (e & 2 ? o[3] : o[2]) : e & 2 ? o[1] : o[0];
+              if (n + e < N) yp[e] = (uint16_t)(d >> (16 * (e & 1)));
+            }
+          }
+        }
+        __builtin_amdgcn_wave_barrier();
       }
-      __builtin_amdgcn_wave_barrier();
     }
   }
 }
