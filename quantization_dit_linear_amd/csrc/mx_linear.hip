@@ -29,12 +29,13 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kGroupM = 8;  // tile rows per group of the tile order
 
-// A workgroup of 2 x 2 waves computes a (64 IB) x (64 JB) tile; each wave a
-// (32 IB) x (32 JB) block of it.
-template <int FA, int FW, int IB_, int JB_, int WGS_>
+// A workgroup of 2 x WN waves computes a (64 IB) x (32 WN JB) tile; each wave
+// a (32 IB) x (32 JB) block of it.
+template <int FA, int FW, int WN_, int IB_, int JB_, int WGS_>
 struct MxTile {
-  static constexpr int IB = IB_, JB = JB_, WGS = WGS_;
-  static constexpr int TM = 64 * IB, TN = 64 * JB;
+  static constexpr int WN = WN_, IB = IB_, JB = JB_, WGS = WGS_;
+  static constexpr int THREADS = 128 * WN;
+  static constexpr int TM = 64 * IB, TN = 32 * WN * JB;
   // Elements of K a stage: 128 bytes of a row (64 of 4-bit weights against
   // 8-bit activations), so that a row's request is a whole line of the L2,
   // and the same matrix-core time either way (8-bit elements run at half rate).
@@ -48,7 +49,7 @@ struct MxTile {
   static constexpr int EROWS = 16;               // output rows a wave stages at once
   static constexpr int EPI = EROWS * 64 * JB;
   static constexpr int SC0 = 2 * STAGE, EP0 = SC0 + 2 * SBUF;
-  static constexpr int LDS = EP0 + 4 * EPI;
+  static constexpr int LDS = EP0 + 2 * WN * EPI;
   static_assert(LDS * WGS <= 160 * 1024, "LDS of one CU");
 };
 
@@ -99,26 +100,27 @@ struct Frag {
 };
 
 template <int FA, int FW, class TL>
-__global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
+__global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_tile_kernel(
     const uint8_t *__restrict__ A, const uint8_t *__restrict__ As, const uint8_t *__restrict__ W,
     const uint8_t *__restrict__ Ws, int M, int N, int K, uint16_t *__restrict__ Y, int vec) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   constexpr int IB = TL::IB, JB = TL::JB, RA = TL::RA, RW = TL::RW;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave >> 1, wn = wave & 1, r = lane & 31, g = lane >> 5;
+  constexpr int TH = TL::THREADS;
+  const int wm = wave / TL::WN, wn = wave % TL::WN, r = lane & 31, g = lane >> 5;
   const int rowA = K / (FA ? 1 : 2), rowW = K / (FW ? 1 : 2), nb = K / 32;
   const int T = (K + TL::KS - 1) / TL::KS;
   const int nbm = (M + TL::TM - 1) / TL::TM, nbn = (N + TL::TN - 1) / TL::TN;
   const int count = nbm * nbn;
 
-  // Loads of a stage: piece idx = tid + 256 k of an operand, CA / CW pieces a
+  // Loads of a stage: piece idx = tid + TH k of an operand, CA / CW pieces a
   // row; the thread of LDS slot s of a row brings the row's piece s ^ swizzle.
   constexpr int CA = RA / 16, CW = RW / 16;
   constexpr int PA = TL::TM * CA, PW = TL::TN * CW;  // pieces
-  constexpr int LA = PA / 256, LW = PW / 256, NL = LA + LW;
+  constexpr int LA = PA / TH, LW = PW / TH, NL = LA + LW;
   // pieces requested in the last step of a stage, the others in the first of the next
   constexpr int LL = TL::STEPS == 4 ? NL / 2 : NL;
-  static_assert(PA % 256 == 0 && PW % 256 == 0, "whole rounds of requests");
+  static_assert(PA % TH == 0 && PW % TH == 0, "whole rounds of requests");
   const int ra0 = tid / CA, ca0 = (tid % CA) ^ swizzle<RA>(ra0);
   const int rw0 = tid / CW, cw0 = (tid % CW) ^ swizzle<RW>(rw0);
   const int uw = __builtin_amdgcn_readfirstlane(wave);
@@ -153,17 +155,18 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
     return x;
   };
   // piece k of stage t of a tile into LDS stage `buf`: activations first.
-  // Pieces past K and stages past the last are sent outside the buffers.
+  // Pieces past K and stages past the last are sent outside the buffers (the
+  // hardware's range check covers the uniform offset too).
+  const uint32_t offA = ra0 * rowA + ca0 * 16, offW = rw0 * rowW + cw0 * 16;
   auto load_piece = [&](const Tile &x, int t, int buf, int k) {
     uint8_t *b = lds + buf * TL::STAGE;
     if (k < LA) {
       const bool in = ca0 * 16 < rowA - t * RA;
-      load_to_lds(x.a, b + la0 + k * 4096, in ? (ra0 + k * (256 / CA)) * rowA + ca0 * 16 : 0x7ffffff0u,
-                  t * RA);
+      load_to_lds(x.a, b + la0 + k * (16 * TH), in ? offA : 0x7ffffff0u, t * RA + k * (TH / CA) * rowA);
     } else {
       const bool in = cw0 * 16 < rowW - t * RW;
-      load_to_lds(x.w, b + lw0 + (k - LA) * 4096,
-                  in ? (rw0 + (k - LA) * (256 / CW)) * rowW + cw0 * 16 : 0x7ffffff0u, t * RW);
+      load_to_lds(x.w, b + lw0 + (k - LA) * (16 * TH), in ? offW : 0x7ffffff0u,
+                  t * RW + (k - LA) * (TH / CW) * rowW);
     }
   };
 
@@ -171,41 +174,50 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
     const Tile x = tile_at(v);
     const int m0 = x.m0, n0 = x.n0, mr = x.mr, nr = x.nr;
 
-    // Scales: 16 blocks of every row at a time, one 16-byte load a row (its
-    // address has no alignment).  A last, partial group goes byte by byte
-    // straight to LDS, zero past K.
-    constexpr int LS = (TL::SROWS + 255) / 256;
-    u32x4 sts[LS];
-    auto group_rows = [&](auto f) {
+    // Scales: 32 blocks of a row are loaded at once (one request to the L2 for
+    // most; their address has no alignment), 16 a time go to LDS.  A last, partial group of 16 goes byte by byte, zero past K.
+    constexpr int LS = (TL::SROWS + TH - 1) / TH;
+    u32x4 sts[LS][2];
+    auto group_rows = [&](const Tile &x, auto f) {
 #pragma unroll
       for (int i = 0; i < LS; i++) {
-        const int row = tid + 256 * i;
-        if (row < TL::SROWS) {
+        const int row = tid + TH * i;
+        if (LS * TH == TL::SROWS || row < TL::SROWS) {
           const bool isw = row >= TL::TM;
-          const int lr = isw ? row - TL::TM : row, n = (isw ? nr : mr) - 1;
-          f(i, row, (isw ? Ws : As) + (int64_t)((isw ? n0 : m0) + (lr < n ? lr : n)) * nb);
+          const int lr = isw ? row - TL::TM : row, n = (isw ? x.nr : x.mr) - 1;
+          f(i, row, (isw ? Ws : As) + (int64_t)((isw ? x.n0 : x.m0) + (lr < n ? lr : n)) * nb);
         }
       }
     };
-    auto load_group = [&](int grp) {
+    auto load_groups = [&](const Tile &x, int grp) {  // grp even
+      group_rows(x, [&](int i, int, const uint8_t *p) {
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+          if (16 * (grp + h) + 16 <= nb) {
+            u32x4 s;
+            __builtin_memcpy(&s, p + 16 * (grp + h), 16);
+            sts[i][h] = s;
+          }
+      });
+    };
+    auto store_group = [&](const Tile &x, int grp) {
+      uint8_t *b = lds + TL::SC0 + (grp & 1) * TL::SBUF;
       if (16 * grp + 16 <= nb) {
-        group_rows([&](int i, int, const uint8_t *p) { __builtin_memcpy(&sts[i], p + 16 * grp, 16); });
+        auto put = [&](int h) {
+          group_rows(x, [&](int i, int row, const uint8_t *) {
+#pragma unroll
+            for (int p = 0; p < 4; p++) *(uint32_t *)(b + (p * TL::SROWS + row) * 4) = sts[i][h][p];
+          });
+        };
+        if (grp & 1) put(1);  // a constant index in each case: registers
+        else put(0);
       } else {
-        uint8_t *b = lds + TL::SC0 + (grp & 1) * TL::SBUF;
-        group_rows([&](int, int row, const uint8_t *p) {
+        group_rows(x, [&](int, int row, const uint8_t *p) {
 #pragma unroll 1
           for (int k = 0; k < 16; k++)
             b[((k >> 2) * TL::SROWS + row) * 4 + (k & 3)] = 16 * grp + k < nb ? p[16 * grp + k] : 0;
         });
       }
-    };
-    auto store_group = [&](int grp) {
-      if (16 * grp + 16 > nb) return;
-      uint8_t *b = lds + TL::SC0 + (grp & 1) * TL::SBUF;
-      group_rows([&](int i, int row, const uint8_t *) {
-#pragma unroll
-        for (int p = 0; p < 4; p++) *(uint32_t *)(b + (p * TL::SROWS + row) * 4) = sts[i][p];
-      });
     };
 
     f32x16 acc[JB][IB];
@@ -257,12 +269,12 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
           w[S & 1][j].op(), a[S & 1][i].op(), acc[j][i], FW ? 0 : 4, FA ? 0 : 4, S, sw[j], S, sa[i]);
     };
 
-    load_group(0);
+    load_groups(x, 0);
 #pragma unroll
     for (int t = 0; t < 2; t++)
 #pragma unroll
       for (int k = 0; k < (t ? LL : NL); k++) load_piece(x, t, t, k);
-    store_group(0);
+    store_group(x, 0);
     wait_and_sync<LL>();
 #pragma unroll
     for (int k = 0; k < NR; k++) read_frag(0, 0, k);
@@ -303,13 +315,14 @@ __global__ __launch_bounds__(256, TL::WGS) void mx_tile_kernel(
     for (int t = 0; t < T; t++) {
       const int ph = t & (TL::SPG - 1), grp = t / TL::SPG;
       const bool more = (grp + 1) * 16 < nb;
-      if (more && ph == 0) load_group(grp + 1);
+      // (branches only here: the products below stay one block, in order)
+      if (more && ph == 0 && (grp & 1)) load_groups(x, grp + 1);
+      if (more && ph == TL::SPG / 2) store_group(x, grp + 1);
       step(t, std::integral_constant<int, 0>{});
       if constexpr (TL::STEPS == 4) {
         step(t, std::integral_constant<int, 1>{});
         step(t, std::integral_constant<int, 2>{});
       }
-      if (more && ph == TL::SPG / 2) store_group(grp + 1);
       wait_and_sync<0>();
       step(t, std::integral_constant<int, TL::STEPS - 1>{});
       take_scales();
@@ -376,7 +389,7 @@ hipError_t launch_tiles(const MxLinearArgs &a, int cus) {
   const int64_t slots = (int64_t)cus * TL::WGS;
   const int vec = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
   hipLaunchKernelGGL((mx_tile_kernel<FA, FW, TL>), dim3((unsigned)(tiles < slots ? tiles : slots)),
-                     dim3(256), TL::LDS, a.stream, a.a_codes, a.a_scales, a.w_codes, a.w_scales,
+                     dim3(TL::THREADS), TL::LDS, a.stream, a.a_codes, a.a_scales, a.w_codes, a.w_scales,
                      (int)a.M, (int)a.N, a.K, a.y, vec);
   return hipGetLastError();
 }
@@ -385,9 +398,9 @@ template <int FA, int FW>
 hipError_t launch_pair(const MxLinearArgs &a, int cus) {
   const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
   const int64_t mid = ((a.M + 127) / 128) * ((a.N + 127) / 128);
-  if (big >= cus) return launch_tiles<FA, FW, MxTile<FA, FW, 4, 4, 1>>(a, cus);
-  if (mid >= cus) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 2, 2>>(a, cus);
-  return launch_tiles<FA, FW, MxTile<FA, FW, 1, 1, 4>>(a, cus);
+  if (big >= cus) return launch_tiles<FA, FW, MxTile<FA, FW, 4, 4, 2, 1>>(a, cus);
+  if (mid >= cus) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 2, 2, 2>>(a, cus);
+  return launch_tiles<FA, FW, MxTile<FA, FW, 2, 1, 1, 4>>(a, cus);
 }
 
 }  // namespace
