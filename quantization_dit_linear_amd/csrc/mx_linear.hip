@@ -27,7 +27,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kGroupM = 8;  // tile rows per group of the tile order
+constexpr int kGroupM = 4;  // tile rows per group of the tile order
 
 // A workgroup of 2 x WN waves computes a (64 IB) x (32 WN JB) tile; each wave
 // a (32 IB) x (32 JB) block of it.
