@@ -379,6 +379,125 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
   }
 }
 
+// Few rows: a workgroup of 8 waves computes 16 NB columns for 16 MB rows, the
+// waves taking every eighth 256-element chunk of K, straight from memory to
+// registers: the weights are read once and nothing is shared but the
+// activations, which the caches hold.  The waves' sums meet in LDS, in wave
+// order.
+template <int FA, int FW, int MB, int NB>
+__global__ __launch_bounds__(512) void mx_rows_kernel(
+    const uint8_t *__restrict__ A, const uint8_t *__restrict__ As, const uint8_t *__restrict__ W,
+    const uint8_t *__restrict__ Ws, int M, int N, int K, uint16_t *__restrict__ Y, int vec) {
+  constexpr int WAVES = 8;
+  __shared__ f32x4 part[WAVES][MB * NB][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * (16 * NB), m0 = blockIdx.y * (16 * MB);
+  const int rowA = K / (FA ? 1 : 2), rowW = K / (FW ? 1 : 2), nb = K / 32, C = (K + 255) / 256;
+  const int mr = M - m0 < 16 * MB ? M - m0 : 16 * MB, nr = N - n0 < 16 * NB ? N - n0 : 16 * NB;
+  // rows past the last and pieces past K lie outside the buffers: zeros
+  const __amdgpu_buffer_rsrc_t ba = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(A + (int64_t)m0 * rowA), 0, mr * rowA, 0x00027000);
+  const __amdgpu_buffer_rsrc_t bw = __builtin_amdgcn_make_buffer_rsrc(
+      (void *)(W + (int64_t)n0 * rowW), 0, nr * rowW, 0x00027000);
+
+  // a row's operand of step 0 or 1 of a chunk
+  auto load = [&](auto fmt, __amdgpu_buffer_rsrc_t b, int row, int rowb, int step) {
+    constexpr int F = decltype(fmt)::value;
+    Frag<F> f;
+    const int at = step * (F ? 128 : 64) + 16 * g, off = row * rowb + at;
+#pragma unroll
+    for (int h = 0; h < (F ? 2 : 1); h++)
+      f.v[h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             b, at + 64 * h < rowb ? off + 64 * h : 0x7ffffff0, 0, 0));
+    return f;
+  };
+  // the row's 8 scale bytes of a chunk, zero past K; the lane's are bytes g and 4 + g
+  auto scales = [&](const uint8_t *p, int row, int last, int c) {
+    p += (int64_t)(row < last ? row : last) * nb + 8 * c;
+    u32x2 s = {0, 0};
+    if (8 * c + 8 <= nb) {
+      __builtin_memcpy(&s, p, 8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+        if (8 * c + i < nb) s[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    }
+    return s;
+  };
+
+  f32x4 acc[NB][MB];
+#pragma unroll
+  for (int j = 0; j < NB; j++)
+#pragma unroll
+    for (int i = 0; i < MB; i++) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint8_t *as = As + (int64_t)m0 * nb, *ws = Ws + (int64_t)n0 * nb;
+#pragma unroll 2
+  for (int c = wave; c < C; c += WAVES) {
+    Frag<FW> w[NB][2];
+    Frag<FA> a[MB][2];
+    u32x2 sw[NB], sa[MB];
+#pragma unroll
+    for (int j = 0; j < NB; j++) {
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+        w[j][h] = load(std::integral_constant<int, FW>{}, bw, 16 * j + r, rowW, 2 * c + h);
+      sw[j] = scales(ws, 16 * j + r, nr - 1, c);
+    }
+#pragma unroll
+    for (int i = 0; i < MB; i++) {
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+        a[i][h] = load(std::integral_constant<int, FA>{}, ba, 16 * i + r, rowA, 2 * c + h);
+      sa[i] = scales(as, 16 * i + r, mr - 1, c);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int j = 0; j < NB; j++)
+#pragma unroll
+        for (int i = 0; i < MB; i++)
+          acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              w[j][h].op(), a[i][h].op(), acc[j][i], FW ? 0 : 4, FA ? 0 : 4, 0,
+              (int)(sw[j][h] >> (8 * g)), 0, (int)(sa[i][h] >> (8 * g)));
+  }
+#pragma unroll
+  for (int j = 0; j < NB; j++)
+#pragma unroll
+    for (int i = 0; i < MB; i++) part[wave][j * MB + i][lane] = acc[j][i];
+  __syncthreads();
+#pragma unroll
+  for (int b0 = 0; b0 < NB * MB; b0 += WAVES) {
+    const int blk = b0 + wave;
+    if (blk >= NB * MB) break;
+    f32x4 y = part[0][blk][lane];
+#pragma unroll
+    for (int v = 1; v < WAVES; v++) y += part[v][blk][lane];
+    const int m = m0 + 16 * (blk % MB) + r, n = n0 + 16 * (blk / MB) + 4 * g;  // four columns of a row
+    if (m >= M) continue;
+    uint16_t *yp = Y + (int64_t)m * N + n;
+    if (vec && n + 3 < N) {
+      const bf16x2 p0 = {(__bf16)y[0], (__bf16)y[1]}, p1 = {(__bf16)y[2], (__bf16)y[3]};
+      *(u32x2 *)yp = u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (n + e < N) yp[e] = __builtin_bit_cast(uint16_t, (__bf16)y[e]);
+    }
+  }
+}
+
+template <int FA, int FW, int MB, int NB>
+hipError_t launch_rows(const MxLinearArgs &a) {
+  const int vec = a.N % 4 == 0 && ((uintptr_t)a.y & 7) == 0;
+  const int64_t gx = (a.N + 16 * NB - 1) / (16 * NB), gy = (a.M + 16 * MB - 1) / (16 * MB);
+  if (gx > (1 << 22) || gy > 65535) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((mx_rows_kernel<FA, FW, MB, NB>), dim3((unsigned)gx, (unsigned)gy), dim3(512), 0,
+                     a.stream, a.a_codes, a.a_scales, a.w_codes, a.w_scales, (int)a.M, (int)a.N,
+                     a.K, a.y, vec);
+  return hipGetLastError();
+}
+
 template <int FA, int FW, class TL>
 hipError_t launch_tiles(const MxLinearArgs &a, int cus) {
   static std::atomic<uint64_t> lds_set{0};  // per instantiation and device
@@ -398,6 +517,21 @@ template <int FA, int FW>
 hipError_t launch_pair(const MxLinearArgs &a, int cus) {
   const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
   const int64_t mid = ((a.M + 127) / 128) * ((a.N + 127) / 128);
+#ifdef FORCE
+  if (FORCE == 4) return launch_tiles<FA, FW, MxTile<FA, FW, 4, 4, 2, 1>>(a, cus);
+  if (FORCE == 2) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 2, 2, 2>>(a, cus);
+  if (FORCE == 1) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 1, 1, 4>>(a, cus);
+#endif
+  // Rows kernel: up to 32 rows, or so few 64 x 64 tiles that they leave most
+  // CUs without one; 32 columns a workgroup where that still gives enough
+  // workgroups, 16 otherwise.
+  const int64_t small = ((a.M + 63) / 64) * ((a.N + 63) / 64);
+  if (a.M <= 32 || 2 * small <= cus) {
+    const bool wide = ((a.M + 63) / 64) * ((a.N + 31) / 32) > cus / 2;
+    if (a.M <= 16) return wide ? launch_rows<FA, FW, 1, 2>(a) : launch_rows<FA, FW, 1, 1>(a);
+    if (a.M <= 32) return wide ? launch_rows<FA, FW, 2, 2>(a) : launch_rows<FA, FW, 2, 1>(a);
+    return wide ? launch_rows<FA, FW, 4, 2>(a) : launch_rows<FA, FW, 4, 1>(a);
+  }
   if (big >= cus) return launch_tiles<FA, FW, MxTile<FA, FW, 4, 4, 2, 1>>(a, cus);
   if (mid >= cus) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 2, 2, 2>>(a, cus);
   return launch_tiles<FA, FW, MxTile<FA, FW, 2, 1, 1, 4>>(a, cus);
