@@ -5,8 +5,13 @@
 //   (u, v) -> (u cos t - v sin t, u sin t + v cos t).
 // Angles are counted in turns as 64-bit fractions: the host gives F =
 // theta^(-2i/size) / 2 pi in units of 2^-64, and p F modulo 2^64 is the turn's
-// fraction, exact to 2^-64 |p| at any position -- no reduction of a large
-// floating-point angle.
+// fraction at any int32 position -- no reduction of a large floating-point
+// angle, and no error that grows with the position beyond F's own rounding.
+//
+// Memory bound: x read and y written once, 16 bytes a lane.  A token's cosines
+// and sines serve all its heads, so a workgroup computes them once into LDS
+// (for several tokens, so that every thread has a pair to work on) and then
+// streams the heads.
 #include <hip/hip_runtime.h>
 
 #include "mx_codec.h"
@@ -15,68 +20,131 @@
 namespace oq {
 namespace {
 
-// cos and sin of pair j at position p
-__device__ __forceinline__ f32x2 turn(const RopeArgs &a, int64_t tok, int j) {
-  const int64_t p = a.pos[tok * a.axes + a.axis[j]];
-  const uint64_t f = (uint64_t)p * a.freq[j];
-  // nearest multiple of 2^-32 turn, as a signed fraction in [-1/2, 1/2]
-  const int32_t q = (int32_t)(uint32_t)((f + 0x80000000ull) >> 32);
-  float s, c;
-  sincospif((float)q * 0x1p-31f, &s, &c);
-  return f32x2{c, a.inverse ? -s : s};
+// (cos, sin) of 2 pi q / 2^32.  The nearest quarter turn apart, |x| <= pi/4,
+// where the Taylor polynomials to x^10 and x^9 are within 2e-9.
+__device__ __forceinline__ f32x2 cos_sin(uint32_t q) {
+  const uint32_t n = (q + 0x20000000u) >> 30;
+  const float x = (float)(int32_t)(q - (n << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float z = x * x;
+  float s = 1.f / 362880.f, c = -1.f / 3628800.f;
+  s = fmaf(s, z, -1.f / 5040.f);
+  s = fmaf(s, z, 1.f / 120.f);
+  s = fmaf(s, z, -1.f / 6.f);
+  s = fmaf(s * z, x, x);
+  c = fmaf(c, z, 1.f / 40320.f);
+  c = fmaf(c, z, -1.f / 720.f);
+  c = fmaf(c, z, 1.f / 24.f);
+  c = fmaf(c, z, -0.5f);
+  c = fmaf(c, z, 1.f);
+  const float a = n & 1 ? -s : c, b = n & 1 ? c : s;
+  return n & 2 ? f32x2{-a, -b} : f32x2{a, b};
 }
 
-// One thread: 8 consecutive elements of a head (interleaved pairs), or the 8
-// elements u and 8 elements v of pairs 8c .. 8c+7 (half-split).
+constexpr int kPairs = 256;  // LDS table: pairs of the tokens that a workgroup takes
+
+// blockIdx.x: a group of TOK tokens; blockIdx.y: a slice of `hs` heads.  One
+// item: 8 consecutive elements of a head (interleaved pairs), or elements u
+// and v of pairs 8c .. 8c+7 (half-split); the items behind them copy.
 template <class T, bool HALF>
-__global__ __launch_bounds__(256) void rope_kernel(RopeArgs a) {
-  const int per = HALF ? (a.turned / 16) + (a.head_dim - a.turned) / 8 : a.head_dim / 8;
-  const int64_t n = a.tokens * a.heads * per;
-  for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
-    const int c = (int)(t % per);
-    const int64_t th = t / per, head = th % a.heads, tok = th / a.heads;
-    const T *x = (const T *)a.x + tok * a.x_token + head * a.x_head;
-    T *y = (T *)a.y + tok * a.y_token + head * a.y_head;
-    float u[8];
-    if (HALF && c < a.turned / 16) {
-      const int half = a.turned / 2;
-      float v[8];
-      load8(x + 8 * c, u);
-      load8(x + half + 8 * c, v);
+__global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int tok_group, int hs) {
+  __shared__ __attribute__((aligned(16))) f32x2 table[kPairs + 8];
+  const int tid = threadIdx.x, half = a.turned / 2;
+  const int h0 = blockIdx.y * hs, nh = a.heads - h0 < hs ? a.heads - h0 : hs;
+
+  // items (token, head, c), c fastest; a thread's next is 256 further on
+  const int turned_items = HALF ? a.turned / 16 : (a.turned + 7) / 8;
+  const int per = HALF ? turned_items + (a.head_dim - a.turned) / 8 : a.head_dim / 8;
+  const int dc = 256 % per, dh = 256 / per % nh, dt = 256 / per / nh;
+
+  for (int64_t t0 = (int64_t)blockIdx.x * tok_group; t0 < a.tokens;
+       t0 += (int64_t)gridDim.x * tok_group) {
+  const int nt = a.tokens - t0 < tok_group ? (int)(a.tokens - t0) : tok_group;
+  __syncthreads();  // the table of the group before is read
+  for (int i = tid; i < nt * half; i += 256) {
+    const int t = i / half, j = i - t * half;
+    const uint64_t f = (uint64_t)(int64_t)a.pos[(t0 + t) * a.axes + a.axis[j]] * a.freq[j];
+    f32x2 z = cos_sin((uint32_t)((f + 0x80000000ull) >> 32));
+    if (a.inverse) z[1] = -z[1];
+    table[i] = z;
+  }
+  __syncthreads();
+
+  int c = tid % per, h = tid / per, t = h / nh;
+  h -= t * nh;
+  const T *xb = (const T *)a.x + t0 * a.x_token + (int64_t)h0 * a.x_head;
+  T *yb = (T *)a.y + t0 * a.y_token + (int64_t)h0 * a.y_head;
+  auto next = [&] {
+    c += dc, h += dh, t += dt;
+    if (c >= per) c -= per, h++;
+    if (h >= nh) h -= nh, t++;
+  };
+  // four items at a time, all loads first
+  constexpr int U = sizeof(T) == 2 ? 4 : 2;
+  while (t < nt) {
+    float u[U][8], v[U][8];
+    int it[U], ic[U];
+    const T *px[U];
+    T *py[U];
 #pragma unroll
-      for (int k = 0; k < 8; k++) {
-        const f32x2 z = turn(a, tok, 8 * c + k);
-        const float p = u[k] * z[0] - v[k] * z[1], q = u[k] * z[1] + v[k] * z[0];
-        u[k] = p, v[k] = q;
+    for (int k = 0; k < U; k++) {
+      it[k] = t, ic[k] = c;
+      const int at = !HALF || c < turned_items ? 8 * c : a.turned + 8 * (c - turned_items);
+      px[k] = xb + t * a.x_token + (int64_t)h * a.x_head + at;
+      py[k] = yb + t * a.y_token + (int64_t)h * a.y_head + at;
+      if (t < nt) {
+        load8(px[k], u[k]);
+        if (HALF && c < turned_items) load8(px[k] + half, v[k]);
       }
-      store8(y + 8 * c, u);
-      store8(y + half + 8 * c, v);
-    } else {
-      const int at = HALF ? a.turned + 8 * (c - a.turned / 16) : 8 * c;
-      load8(x + at, u);
-      if (!HALF)
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-          if (at + 2 * k < a.turned) {
-            const f32x2 z = turn(a, tok, at / 2 + k);
-            const float p = u[2 * k] * z[0] - u[2 * k + 1] * z[1];
-            const float q = u[2 * k] * z[1] + u[2 * k + 1] * z[0];
-            u[2 * k] = p, u[2 * k + 1] = q;
-          }
-      store8(y + at, u);
+      next();
     }
+#pragma unroll
+    for (int k = 0; k < U; k++) {
+      if (it[k] >= nt) break;
+      if (ic[k] < turned_items) {
+        const f32x2 *z = table + it[k] * half + (HALF ? 8 : 4) * ic[k];
+        if constexpr (HALF) {
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const float p = u[k][e] * z[e][0] - v[k][e] * z[e][1];
+            v[k][e] = u[k][e] * z[e][1] + v[k][e] * z[e][0];
+            u[k][e] = p;
+          }
+          store8(py[k] + half, v[k]);
+        } else {
+          // the last item may hold elements behind the turned ones
+          const int left = half - 4 * ic[k];
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const f32x2 w = e < left ? z[e] : f32x2{1.f, 0.f};
+            const float p = u[k][2 * e] * w[0] - u[k][2 * e + 1] * w[1];
+            const float q = u[k][2 * e] * w[1] + u[k][2 * e + 1] * w[0];
+            u[k][2 * e] = e < left ? p : u[k][2 * e];
+            u[k][2 * e + 1] = e < left ? q : u[k][2 * e + 1];
+          }
+        }
+      }
+      store8(py[k], u[k]);
+    }
+  }
   }
 }
 
 }  // namespace
 
 hipError_t launch_rope(const RopeArgs &a) {
-  const int per = a.half ? (a.turned / 16) + (a.head_dim - a.turned) / 8 : a.head_dim / 8;
-  const int64_t n = a.tokens * a.heads * per, g = (n + 255) / 256;
-  const dim3 grid((unsigned)(g < 65536 ? g : 65536)), block(256);
+  // as many tokens a workgroup as give its threads a pair each; one, and a
+  // slice of the heads, where tokens are too few to fill the card
+  const int half = a.turned / 2, fit = half > 0 ? kPairs / half : 8;
+  int group = fit < 1 ? 1 : fit > 8 ? 8 : fit;
+  if (a.tokens < 1024 * (int64_t)group) group = 1;
+  const int64_t gx = (a.tokens + group - 1) / group;
+  const int per = a.head_dim / 8;
+  int hs = a.heads;
+  while (gx * ((a.heads + hs - 1) / hs) < 1024 && hs * per > 256) hs = (hs + 1) / 2;
+  const dim3 grid((unsigned)(gx < (1 << 20) ? gx : 1 << 20), (unsigned)((a.heads + hs - 1) / hs)), block(256);
 #define OQ_CASE(DT, T, H)        \
   if (a.dtype == DT && a.half == H) \
-    hipLaunchKernelGGL((rope_kernel<T, H>), grid, block, 0, a.stream, a);
+    hipLaunchKernelGGL((rope_kernel<T, H>), grid, block, 0, a.stream, a, group, hs);
   OQ_CASE(0, float, false) OQ_CASE(0, float, true)
   OQ_CASE(1, uint16_t, false) OQ_CASE(1, uint16_t, true)
 #undef OQ_CASE
