@@ -7,7 +7,17 @@
 // The sum is written rounded to the stream's type; the norm runs over the
 // unrounded fp32 sum, so y carries one rounding (and the codes none but
 // their own).
+//
+// Memory bound: every row is read once, kept in registers between the sum
+// of squares and the scaling, and written once.  64, 128 or 256 threads take a
+// row (by its length alone, so that a row's bits do not depend on the batch),
+// workgroups walk the rows, the next row's loads are issued before the present
+// one's reduction, and bf16 parameters stay in registers from row to row
+// (fp32 ones would take half the register file; they are read again, from the
+// caches).
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "mx_codec.h"
 #include "oq_internal.h"
@@ -15,123 +25,220 @@
 namespace oq {
 namespace {
 
-// T: stream type, P: parameter type; OUT: 0 = y in T, 1 = e4m3, 2 = e2m1.
-// One workgroup of 256 a row, the row in registers.
-template <class T, class P, int OUT, int NCH>
-__global__ __launch_bounds__(256) void rms_norm_kernel(RmsNormArgs a) {
-  __shared__ float part[4];
-  const int tid = threadIdx.x, nch = a.d / 8;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-  const int64_t grp = row / a.rows_per_mod;
-  const T *x = (const T *)a.x + row * a.d, *res = (const T *)a.residual;
-  float h[NCH][8];
-  float ss = 0.f;
+// 8 elements as loaded
+template <class T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  u32x4 w;
+  __device__ __forceinline__ void load(const uint16_t *p) { w = *(const u32x4 *)p; }
+  __device__ __forceinline__ void get(float *v) const { unpack8(w, v); }
+  __device__ __forceinline__ void fill(float f) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, f) >> 16;
+    w = u32x4{b | b << 16, b | b << 16, b | b << 16, b | b << 16};
+  }
+};
+template <>
+struct Raw<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float *p) { a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4); }
+  __device__ __forceinline__ void get(float *v) const {
 #pragma unroll
-  for (int i = 0; i < NCH; i++) {
-    const int c = tid + 256 * i;
-    if (c < nch) {
-      load8(x + 8 * c, h[i]);
-      if (a.gate) {
+    for (int i = 0; i < 4; i++) v[i] = a[i], v[4 + i] = b[i];
+  }
+  __device__ __forceinline__ void fill(float f) { a = b = f32x4{f, f, f, f}; }
+};
+
+__device__ __forceinline__ float wave_sum(float v) {
+  auto dpp = [](float x, auto ctrl) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x),
+                                                                 decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  v += dpp(v, std::integral_constant<int, 0xB1>{});   // lane ^ 1
+  v += dpp(v, std::integral_constant<int, 0x4E>{});   // lane ^ 2
+  v += dpp(v, std::integral_constant<int, 0x141>{});  // the other four of 8
+  v += dpp(v, std::integral_constant<int, 0x140>{});  // the other eight of 16
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  return v;
+}
+
+// T: stream type, P: parameter type, TPR threads a row, NCH 8-element chunks
+// a thread; MOD: with gate, scale or shift.
+template <class T, class P, int TPR, int NCH, bool MOD>
+__global__ __launch_bounds__(256, 2) void rms_norm_kernel(RmsNormArgs a) {
+  constexpr int RPW = 256 / TPR, WPR = TPR / 64;  // rows a workgroup, waves a row
+  constexpr bool HOLD = sizeof(P) == 2;
+  __shared__ float part[2][4];
+  const int tid = threadIdx.x, slot = tid / TPR, lt = tid % TPR, nch = a.d / 8;
+  const float inv_d = 1.0f / (float)a.d;
+
+  Raw<P> pw[NCH], pg[NCH], ps[NCH], pb[NCH];
+  auto load_weight = [&](int i) {
+    const int c = lt + TPR * i;
+    if (a.weight && c < nch) pw[i].load((const P *)a.weight + 8 * c);
+    else pw[i].fill(1.f);
+  };
+  auto load_mod = [&](int i, int64_t grp) {
+    const int c = lt + TPR * i;
+    const int64_t at = grp * a.mod_stride + 8 * c;
+    if (a.gate && c < nch) pg[i].load((const P *)a.gate + at);
+    else pg[i].fill(1.f);
+    if (a.scale && c < nch) ps[i].load((const P *)a.scale + at);
+    else ps[i].fill(0.f);
+    if (a.shift && c < nch) pb[i].load((const P *)a.shift + at);
+    else pb[i].fill(0.f);
+  };
+  if constexpr (HOLD)
+#pragma unroll
+    for (int i = 0; i < NCH; i++) load_weight(i);
+
+  Raw<T> nx[NCH], nr[NCH];  // the next row
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NCH; i++) {
+      const int c = lt + TPR * i;
+      if (row < a.rows && c < nch) {
+        nx[i].load((const T *)a.x + row * a.d + 8 * c);
+        if (a.residual) nr[i].load((const T *)a.residual + row * a.d + 8 * c);
+      }
+    }
+  };
+  int64_t have = -1;  // the group whose parameters are held
+  int par = 0;
+  fetch((int64_t)blockIdx.x * RPW + slot);
+  for (int64_t r0 = (int64_t)blockIdx.x * RPW; r0 < a.rows; r0 += (int64_t)gridDim.x * RPW) {
+    const int64_t row = r0 + slot, grp = MOD ? row / a.rows_per_mod : 0;
+    const bool in = row < a.rows;
+    if constexpr (MOD)
+      if (in && (!HOLD || grp != have)) {
+#pragma unroll
+        for (int i = 0; i < NCH; i++) load_mod(i, grp);
+        have = grp;
+      }
+    float h[NCH][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NCH; i++) {
+      if (!in || lt + TPR * i >= nch) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) h[i][k] = 0.f;
+        continue;
+      }
+      nx[i].get(h[i]);
+      if constexpr (MOD) {
         float g[8];
-        load8((const P *)a.gate + grp * a.mod_stride + 8 * c, g);
+        pg[i].get(g);
 #pragma unroll
         for (int k = 0; k < 8; k++) h[i][k] *= g[k];
       }
-      if (res) {
+      if (a.residual) {
         float r[8];
-        load8(res + row * a.d + 8 * c, r);
+        nr[i].get(r);
 #pragma unroll
         for (int k = 0; k < 8; k++) h[i][k] += r[k];
       }
 #pragma unroll
-      for (int k = 0; k < 8; k++) ss += h[i][k] * h[i][k];
+      for (int k = 0; k < 8; k++) ss = fmaf(h[i][k], h[i][k], ss);
     }
-  }
-  auto total = [&](float v) {
+    fetch(row + (int64_t)gridDim.x * RPW);
+
+    // the row's total; `other`: any row's of the workgroup that is not finite
+    auto total = [&](float v, bool &other) {
+      v = wave_sum(v);
+      if constexpr (WPR > 1) {
+        if ((tid & 63) == 0) part[par][tid >> 6] = v;
+        __syncthreads();
+        float all[4], t = 0.f;
+        other = false;
 #pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    __syncthreads();
-    if ((tid & 63) == 0) part[tid >> 6] = v;
-    __syncthreads();
-    return part[0] + part[1] + part[2] + part[3];
-  };
-  ss = total(ss);
-  const float inv_d = 1.0f / (float)a.d;
-  float r;
-  if (ss < __builtin_huge_valf()) {
-    r = rsqrtf(ss * inv_d + a.eps);
-  } else {
-    // the squares overflowed: once more at 2^-64 (a row with a NaN or an
-    // infinity stays one)
-    float s2 = 0.f;
+        for (int w = 0; w < 4; w++) all[w] = part[par][w];
 #pragma unroll
-    for (int i = 0; i < NCH; i++)
-      if (tid + 256 * i < nch)
+        for (int s = 0; s < RPW; s++) {
+          float u = all[s * WPR];
+#pragma unroll
+          for (int w = 1; w < WPR; w++) u += all[s * WPR + w];
+          other |= !(u < __builtin_huge_valf());
+          if (s == slot) t = u;
+        }
+        par ^= 1;
+        return t;
+      } else {
+        other = !(v < __builtin_huge_valf());
+        return v;
+      }
+    };
+    bool redo;
+    ss = total(ss, redo);
+    float rs = rsqrtf(ss * inv_d + a.eps);
+    if (redo) {
+      // a sum of squares overflowed: once more at 2^-64 (a row with a NaN or an
+      // infinity stays one); eps is nothing beside it
+      float s2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < NCH; i++)
 #pragma unroll
         for (int k = 0; k < 8; k++) {
           const float t = h[i][k] * 0x1p-64f;
-          s2 += t * t;
+          s2 = fmaf(t, t, s2);
         }
-    r = rsqrtf(total(s2) * inv_d) * 0x1p-64f;
-  }
-#pragma unroll
-  for (int i = 0; i < NCH; i++) {
-    const int c = tid + 256 * i;
-    if (c >= nch) continue;
-    if (a.sum) store8((T *)a.sum + row * a.d + 8 * c, h[i]);
-    float y[8], p[8];
-#pragma unroll
-    for (int k = 0; k < 8; k++) y[k] = h[i][k] * r;
-    if (a.weight) {
-      load8((const P *)a.weight + 8 * c, p);
-#pragma unroll
-      for (int k = 0; k < 8; k++) y[k] *= p[k];
+      s2 = total(s2, redo);
+      if (!(ss < __builtin_huge_valf())) rs = rsqrtf(s2 * inv_d) * 0x1p-64f;
     }
-    if (a.scale) {
-      load8((const P *)a.scale + grp * a.mod_stride + 8 * c, p);
+    if (!in) continue;
 #pragma unroll
-      for (int k = 0; k < 8; k++) y[k] *= 1.0f + p[k];
-    }
-    if (a.shift) {
-      load8((const P *)a.shift + grp * a.mod_stride + 8 * c, p);
+    for (int i = 0; i < NCH; i++) {
+      const int c = lt + TPR * i;
+      if (c >= nch) continue;
+      if (a.sum) store8((T *)a.sum + row * a.d + 8 * c, h[i]);
+      float y[8], w[8];
+      if constexpr (!HOLD) load_weight(i);
+      pw[i].get(w);
 #pragma unroll
-      for (int k = 0; k < 8; k++) y[k] += p[k];
+      for (int k = 0; k < 8; k++) y[k] = h[i][k] * rs;
+      if constexpr (MOD) {
+        float s[8], b[8];
+        ps[i].get(s), pb[i].get(b);
+#pragma unroll
+        for (int k = 0; k < 8; k++) y[k] = fmaf(y[k], w[k] * (1.0f + s[k]), b[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; k++) y[k] *= w[k];
+      }
+      if (a.out == 0) store8((T *)a.y + row * a.d + 8 * c, y);
+      else if (a.out == 1) mx_store8<1>(y, row * nch + c, (uint8_t *)a.y, a.y_scales);
+      else mx_store8<0>(y, row * nch + c, (uint8_t *)a.y, a.y_scales);
     }
-    if constexpr (OUT == 0)
-      store8((T *)a.y + row * a.d + 8 * c, y);
-    else
-      mx_store8<OUT == 1 ? 1 : 0>(y, row * nch + c, (uint8_t *)a.y, a.y_scales);
-  }
   }
 }
 
-template <class T, class P, int OUT>
+template <class T, class P, bool MOD>
 hipError_t launch_d(const RmsNormArgs &a) {
-  const int need = (a.d / 8 + 255) / 256;
-  const dim3 g((unsigned)(a.rows < 65536 ? a.rows : 65536)), b(256);
-#define OQ_CASE(n) \
-  if (need <= n) { \
-    hipLaunchKernelGGL((rms_norm_kernel<T, P, OUT, n>), g, b, 0, a.stream, a); \
-    return hipGetLastError(); \
-  }
-  OQ_CASE(1) OQ_CASE(2) OQ_CASE(4) OQ_CASE(8)
-#undef OQ_CASE
-  return hipErrorInvalidValue;
+  auto go = [&](auto kernel, int rows_per_wg) {
+    const int64_t wgs = (a.rows + rows_per_wg - 1) / rows_per_wg;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(wgs < 2048 ? wgs : 2048)), dim3(256), 0, a.stream, a);
+    return hipGetLastError();
+  };
+  const int d = a.d;
+  if (d <= 512) return go(rms_norm_kernel<T, P, 64, 1, MOD>, 4);
+  if (d <= 1024) return go(rms_norm_kernel<T, P, 64, 2, MOD>, 4);
+  if (d <= 2048) return go(rms_norm_kernel<T, P, 64, 4, MOD>, 4);
+  if (d <= 5 * 1024) return go(rms_norm_kernel<T, P, 128, 5, MOD>, 2);
+  if (d <= 8 * 1024) return go(rms_norm_kernel<T, P, 256, 4, MOD>, 1);
+  return go(rms_norm_kernel<T, P, 256, 8, MOD>, 1);
 }
 
 template <class T, class P>
-hipError_t launch_out(const RmsNormArgs &a) {
-  if (a.out == 0) return launch_d<T, P, 0>(a);
-  if (a.out == 1) return launch_d<T, P, 1>(a);
-  return launch_d<T, P, 2>(a);
+hipError_t launch_mod(const RmsNormArgs &a) {
+  return a.gate || a.scale || a.shift ? launch_d<T, P, true>(a) : launch_d<T, P, false>(a);
 }
 
 }  // namespace
 
 hipError_t launch_rms_norm(const RmsNormArgs &a) {
   if (a.dtype == 0)
-    return a.param_dtype == 0 ? launch_out<float, float>(a) : launch_out<float, uint16_t>(a);
-  return a.param_dtype == 0 ? launch_out<uint16_t, float>(a) : launch_out<uint16_t, uint16_t>(a);
+    return a.param_dtype == 0 ? launch_mod<float, float>(a) : launch_mod<float, uint16_t>(a);
+  return a.param_dtype == 0 ? launch_mod<uint16_t, float>(a) : launch_mod<uint16_t, uint16_t>(a);
 }
 
 }  // namespace oq
