@@ -329,47 +329,98 @@ def rtn4_linear(x, q4, scales, *, out=None, stream=None):
 
 
 # ------------------------------------------------- the microscaled path --
+#
+# Calls of a few microseconds: the checks below are the ones above, written for
+# the case that passes (the slow forms name what is wrong).
 
 _MX = {"fp4": OQ_MX_FP4, "fp8": OQ_MX_FP8}
+_C_INTS = [ctypes.c_int * n for n in range(5)]
 
 
 def _mx(fmt, name="fmt"):
-    if fmt not in _MX:
-        raise ValueError(f"{name} must be 'fp4' or 'fp8' (got {fmt!r})")
-    return _MX[fmt]
+    try:
+        return _MX[fmt]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} must be 'fp4' or 'fp8' (got {fmt!r})") from None
 
 
-def _empty(shape, dtype, device, stream):
-    """A fresh output, owned by the stream that the call runs on."""
-    import torch
+def _empty(shape, dtype, like, stream):
+    """A fresh output beside `like`, owned by the stream that the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
+    import torch
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _mx_outputs(codes, scales, rows, d, bits, device, stream):
+def _shaped(t, shape, dtype, name):
+    try:
+        if t.shape == shape and t.dtype == dtype:
+            return
+    except AttributeError:
+        pass
+    _expect(t, shape, dtype, name)
+
+
+def _call_device(*named):
+    """The current device's index; every (tensor, name) must live there."""
+    import torch
+    for t, name in named:
+        if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda):
+            _on_device(t, name)
+    dev = torch.cuda.current_device()
+    for t, name in named:
+        if t is not None and t.get_device() != dev:
+            _on_device(t, name)
+    return dev
+
+
+def _ptr(t, name):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _strided_ptr(t, name):
+    """Device pointer of a tensor whose last dimension is dense (the other
+    strides are the call's arguments)."""
+    if t.stride(-1) != 1 and t.numel():
+        raise ValueError(f"{name} must be dense in its last dimension")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _mx_outputs(codes, scales, rows, d, bits, like, stream):
     import torch
     if codes is None:
-        codes = _empty((rows, d * bits // 8), torch.uint8, device, stream)
+        codes = _empty((rows, d * bits // 8), torch.uint8, like, stream)
+    else:
+        _shaped(codes, (rows, d * bits // 8), torch.uint8, "codes")
     if scales is None:
-        scales = _empty((rows, d // 32), torch.uint8, device, stream)
-    _expect(codes, (rows, d * bits // 8), torch.uint8, "codes")
-    _expect(scales, (rows, d // 32), torch.uint8, "scales")
+        scales = _empty((rows, d // 32), torch.uint8, like, stream)
+    else:
+        _shaped(scales, (rows, d // 32), torch.uint8, "scales")
     return codes, scales
 
 
-def _mx_pair(codes, scales, bits, names):
+def _mx_pair(codes, scales, bits, codes_name, scales_name):
     """(rows, d) of a pair of MX arrays, whose shapes must agree."""
     import torch
-    for t, n in zip((codes, scales), names):
+    for t, n in ((codes, codes_name), (scales, scales_name)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{n} must be a torch.Tensor")
         if t.dim() != 2:
             raise ValueError(f"{n} must be two-dimensional")
-    rows, d = scales.shape[0], 32 * scales.shape[1]
-    _expect(codes, (rows, d * bits // 8), torch.uint8, names[0])
-    _expect(scales, (rows, d // 32), torch.uint8, names[1])
+    rows, d = scales.shape
+    d *= 32
+    _shaped(codes, (rows, d * bits // 8), torch.uint8, codes_name)
+    _shaped(scales, (rows, d // 32), torch.uint8, scales_name)
     return rows, d
 
 
@@ -381,10 +432,10 @@ def mx_quantize(x, fmt, *, codes=None, scales=None, stream=None):
     if x.dim() != 2:
         raise ValueError("x must be [rows, d]")
     rows, d = x.shape
-    codes, scales = _mx_outputs(codes, scales, rows, d, bits, x.device, stream)
-    rc = lib().oq_mx_quantize(_dev_ptr(x, "x"), _dtype_code(x), rows, d, bits,
-                              _dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"),
-                              _stream(stream))
+    codes, scales = _mx_outputs(codes, scales, rows, d, bits, x, stream)
+    dev = _call_device((x, "x"), (codes, "codes"), (scales, "scales"))
+    rc = lib().oq_mx_quantize(_ptr(x, "x"), _dtype_code(x), rows, d, bits, _ptr(codes, "codes"),
+                              _ptr(scales, "scales"), _raw_stream(stream, dev))
     _check(rc, "oq_mx_quantize")
     return codes, scales
 
@@ -394,12 +445,14 @@ def mx_dequantize(codes, scales, fmt, *, dtype=None, out=None, stream=None):
     out says float32)."""
     import torch
     bits = _mx(fmt)
-    rows, d = _mx_pair(codes, scales, bits, ("codes", "scales"))
+    rows, d = _mx_pair(codes, scales, bits, "codes", "scales")
     if out is None:
-        out = _empty((rows, d), dtype or torch.bfloat16, codes.device, stream)
-    _expect(out, (rows, d), dtype or out.dtype, "out")
-    rc = lib().oq_mx_dequantize(_dev_ptr(codes, "codes"), _dev_ptr(scales, "scales"), bits, rows,
-                                d, _dtype_code(out), _dev_ptr(out, "out"), _stream(stream))
+        out = _empty((rows, d), dtype or torch.bfloat16, codes, stream)
+    else:
+        _shaped(out, (rows, d), dtype or out.dtype, "out")
+    dev = _call_device((codes, "codes"), (scales, "scales"), (out, "out"))
+    rc = lib().oq_mx_dequantize(_ptr(codes, "codes"), _ptr(scales, "scales"), bits, rows, d,
+                                _dtype_code(out), _ptr(out, "out"), _raw_stream(stream, dev))
     _check(rc, "oq_mx_dequantize")
     return out
 
@@ -408,27 +461,21 @@ def mx_linear(a_codes, a_scales, a_fmt, w_codes, w_scales, w_fmt, *, out=None, s
     """bf16 y [M, N] = A W^T of MX activations [M, K] and weights [N, K]."""
     import torch
     a_bits, w_bits = _mx(a_fmt, "a_fmt"), _mx(w_fmt, "w_fmt")
-    M, K = _mx_pair(a_codes, a_scales, a_bits, ("a_codes", "a_scales"))
-    N, Kw = _mx_pair(w_codes, w_scales, w_bits, ("w_codes", "w_scales"))
+    M, K = _mx_pair(a_codes, a_scales, a_bits, "a_codes", "a_scales")
+    N, Kw = _mx_pair(w_codes, w_scales, w_bits, "w_codes", "w_scales")
     if K != Kw:
         raise ValueError(f"activations have {K} columns, weights {Kw}")
     if out is None:
-        out = _empty((M, N), torch.bfloat16, a_codes.device, stream)
-    _expect(out, (M, N), torch.bfloat16, "out")
-    rc = lib().oq_mx_linear(_dev_ptr(a_codes, "a_codes"), _dev_ptr(a_scales, "a_scales"), a_bits,
-                            _dev_ptr(w_codes, "w_codes"), _dev_ptr(w_scales, "w_scales"), w_bits,
-                            M, N, K, _dev_ptr(out, "y"), _stream(stream))
+        out = _empty((M, N), torch.bfloat16, a_codes, stream)
+    else:
+        _shaped(out, (M, N), torch.bfloat16, "out")
+    dev = _call_device((a_codes, "a_codes"), (a_scales, "a_scales"), (w_codes, "w_codes"),
+                       (w_scales, "w_scales"), (out, "out"))
+    rc = lib().oq_mx_linear(_ptr(a_codes, "a_codes"), _ptr(a_scales, "a_scales"), a_bits,
+                            _ptr(w_codes, "w_codes"), _ptr(w_scales, "w_scales"), w_bits, M, N, K,
+                            _ptr(out, "out"), _raw_stream(stream, dev))
     _check(rc, "oq_mx_linear")
     return out
-
-
-def _strided_ptr(t, name):
-    """Device pointer of a tensor whose last dimension is dense (the other
-    strides are the call's arguments)."""
-    _on_device(t, name)
-    if t.numel() and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be dense in its last dimension")
-    return ctypes.c_void_p(t.data_ptr())
 
 
 def add_rms_norm(x, residual=None, *, weight=None, gate=None, scale=None, shift=None,
@@ -443,56 +490,60 @@ def add_rms_norm(x, residual=None, *, weight=None, gate=None, scale=None, shift=
     (h, codes, scales): y in MX codes.  sum_out (for h) and out may be x or
     residual themselves; sum_out=False computes no h and returns None for it.
     """
-    import torch
     if x.dim() != 2:
         raise ValueError("x must be [rows, d]")
     rows, d = x.shape
     if residual is not None:
-        _expect(residual, (rows, d), x.dtype, "residual")
-    params = [p for p in (weight, gate, scale, shift) if p is not None]
+        _shaped(residual, (rows, d), x.dtype, "residual")
+    first, groups, stride, mods = None, 1, d, False
     for p, n in ((weight, "weight"), (gate, "gate"), (scale, "scale"), (shift, "shift")):
-        if p is not None and (p.shape[-1:] != (d,) or p.dtype != params[0].dtype):
+        if p is None:
+            continue
+        first = p if first is None else first
+        if p.shape[-1:] != (d,) or p.dtype != first.dtype:
             raise ValueError(f"{n} must have {d} columns and the other parameters' dtype")
-    if weight is not None and weight.dim() != 1:
-        raise ValueError("weight must be [d]")
-    groups, stride = 1, d
-    mods = {n: p for n, p in (("gate", gate), ("scale", scale), ("shift", shift)) if p is not None}
-    for i, (n, p) in enumerate(mods.items()):
-        if p.dim() not in (1, 2):
+        if p is weight:
+            if p.dim() != 1:
+                raise ValueError("weight must be [d]")
+            continue
+        if p.dim() > 2:
             raise ValueError(f"{n} must be [groups, d] or [d]")
-        g = 1 if p.dim() == 1 else p.shape[0]
-        s = d if g == 1 else p.stride(0)
-        if i and (g, s) != (groups, stride):
+        g, st = (1, d) if p.dim() == 1 or p.shape[0] == 1 else (p.shape[0], p.stride(0))
+        if mods and (g, st) != (groups, stride):
             raise ValueError("gate, scale and shift must have the same groups and row stride")
-        groups, stride = g, s
+        groups, stride, mods = g, st, True
     if rows_per_mod is None:
         rows_per_mod = max(1, -(-rows // max(1, groups)))
     if mods and (rows_per_mod < 1 or -(-rows // rows_per_mod) > groups):
         raise ValueError(f"{rows} rows at {rows_per_mod} per group need more than {groups} groups")
     if sum_out is None:
-        sum_out = _empty((rows, d), x.dtype, x.device, stream)
+        sum_out = _empty((rows, d), x.dtype, x, stream)
     elif sum_out is False:
         sum_out = None
-    if sum_out is not None:
-        _expect(sum_out, (rows, d), x.dtype, "sum_out")
-    if fmt is None:
-        if scales_out is not None:
-            raise ValueError("scales_out needs a fmt")
-        if out is None:
-            out = _empty((rows, d), x.dtype, x.device, stream)
-        _expect(out, (rows, d), x.dtype, "out")
-        bits, scales = 0, None
     else:
+        _shaped(sum_out, (rows, d), x.dtype, "sum_out")
+    scales, bits = None, 0
+    if fmt is not None:
         bits = _mx(fmt)
-        out, scales = _mx_outputs(out, scales_out, rows, d, bits, x.device, stream)
-    opt = lambda t, n: None if t is None else _dev_ptr(t, n)  # noqa: E731
-    mod = lambda t, n: None if t is None else _strided_ptr(t, n)  # noqa: E731
+        out, scales = _mx_outputs(out, scales_out, rows, d, bits, x, stream)
+    elif scales_out is not None:
+        raise ValueError("scales_out needs a fmt")
+    elif out is None:
+        out = _empty((rows, d), x.dtype, x, stream)
+    else:
+        _shaped(out, (rows, d), x.dtype, "out")
+    dev = _call_device((x, "x"), (residual, "residual"), (weight, "weight"), (gate, "gate"),
+                       (scale, "scale"), (shift, "shift"), (sum_out, "sum_out"), (out, "out"),
+                       (scales, "scales_out"))
     rc = lib().oq_add_rms_norm(
-        _dev_ptr(x, "x"), opt(residual, "residual"), _dtype_code(x), rows, d, eps,
-        opt(weight, "weight"), mod(gate, "gate"), mod(scale, "scale"), mod(shift, "shift"),
-        _dtype_code(params[0]) if params else OQ_F32, rows_per_mod, stride,
-        opt(sum_out, "sum_out"), bits, _dev_ptr(out, "out"), opt(scales, "scales_out"),
-        _stream(stream))
+        _ptr(x, "x"), None if residual is None else _ptr(residual, "residual"), _dtype_code(x),
+        rows, d, eps, None if weight is None else _ptr(weight, "weight"),
+        None if gate is None else _strided_ptr(gate, "gate"),
+        None if scale is None else _strided_ptr(scale, "scale"),
+        None if shift is None else _strided_ptr(shift, "shift"),
+        OQ_F32 if first is None else _dtype_code(first), rows_per_mod, stride,
+        None if sum_out is None else _ptr(sum_out, "sum_out"), bits, _ptr(out, "out"),
+        None if scales is None else _ptr(scales, "scales_out"), _raw_stream(stream, dev))
     _check(rc, "oq_add_rms_norm")
     return (sum_out, out) if fmt is None else (sum_out, out, scales)
 
@@ -501,22 +552,27 @@ def rope(x, pos, axis_dims, *, theta=10000.0, half=False, inverse=False, out=Non
     """Rotary embedding of x [tokens, heads, head_dim] (bfloat16 or float32, any
     16-byte strides, dense heads: a slice of a fused projection's output is
     taken as it lies) at pos int32 [tokens, axes]; axis_dims: elements of a
-    head that turn with each axis.  half: pairs (j, j + R/2) instead of
-    (2j, 2j+1); inverse: the opposite turn, which is the gradient.  out may be x."""
+    head that turn with each axis (one to four).  half: pairs (j, j + R/2)
+    instead of (2j, 2j+1); inverse: the opposite turn, which is the gradient.
+    out may be x."""
     import torch
     if x.dim() != 3:
         raise ValueError("x must be [tokens, heads, head_dim]")
     tokens, heads, hd = x.shape
-    dims = [int(v) for v in axis_dims]
-    _expect(pos, (tokens, len(dims)), torch.int32, "pos")
+    axes = len(axis_dims)
+    if not 1 <= axes <= 4:
+        raise ValueError(f"axis_dims must name one to four axes (got {axes})")
+    _shaped(pos, (tokens, axes), torch.int32, "pos")
     if out is None:
-        out = _empty((tokens, heads, hd), x.dtype, x.device, stream)
-    _expect(out, (tokens, heads, hd), x.dtype, "out")
+        out = _empty((tokens, heads, hd), x.dtype, x, stream)
+    else:
+        _shaped(out, (tokens, heads, hd), x.dtype, "out")
+    dev = _call_device((x, "x"), (pos, "pos"), (out, "out"))
     flags = (OQ_ROPE_HALF if half else 0) | (OQ_ROPE_INVERSE if inverse else 0)
     rc = lib().oq_rope(_strided_ptr(x, "x"), _dtype_code(x), tokens, heads, hd, x.stride(0),
-                       x.stride(1), _dev_ptr(pos, "pos"), len(dims),
-                       (ctypes.c_int * len(dims))(*dims), theta, flags, _strided_ptr(out, "out"),
-                       out.stride(0), out.stride(1), _stream(stream))
+                       x.stride(1), _ptr(pos, "pos"), axes, _C_INTS[axes](*axis_dims), theta,
+                       flags, _strided_ptr(out, "out"), out.stride(0), out.stride(1),
+                       _raw_stream(stream, dev))
     _check(rc, "oq_rope")
     return out
 

@@ -172,7 +172,7 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
 
   for (int v = blockIdx.x; v < count; v += gridDim.x) {
     const Tile x = tile_at(v);
-    const int m0 = x.m0, n0 = x.n0, mr = x.mr, nr = x.nr;
+    const int m0 = x.m0, n0 = x.n0;
 
     // Scales: 32 blocks of a row are loaded at once (one request to the L2 for
     // most; their address has no alignment), 16 a time go to LDS.  A last, partial group of 16 goes byte by byte, zero past K.
@@ -540,10 +540,17 @@ hipError_t launch_pair(const MxLinearArgs &a, int cus) {
 }  // namespace
 
 hipError_t launch_mx_linear(const MxLinearArgs &a) {
-  int cus = 256, dev = 0;
-  if (hipGetDevice(&dev) == hipSuccess)
-    (void)hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-  if (cus <= 0) cus = 256;
+  // CUs of the current device, asked once a device
+  static std::atomic<int> known[64];
+  int cus = 0, dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return hipErrorInvalidDevice;
+  const bool slot = dev >= 0 && dev < 64;
+  if (slot) cus = known[dev].load(std::memory_order_relaxed);
+  if (cus <= 0) {
+    const hipError_t e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess) return e;
+    if (slot) known[dev].store(cus, std::memory_order_relaxed);
+  }
   if (a.a_format == 0) return a.w_format == 0 ? launch_pair<0, 0>(a, cus) : launch_pair<0, 1>(a, cus);
   return a.w_format == 0 ? launch_pair<1, 0>(a, cus) : launch_pair<1, 1>(a, cus);
 }
