@@ -50,6 +50,32 @@ __device__ __forceinline__ void store8(float *p, const float *v) {
   *(f32x4 *)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
 }
 
+// 16 bytes of a row: 8 bf16 or 4 fp32 elements
+__device__ __forceinline__ void load16(const uint16_t *p, float *v) { load8(p, v); }
+
+__device__ __forceinline__ void load16(const float *p, float *v) {
+  const f32x4 a = *(const f32x4 *)p;
+#pragma unroll
+  for (int i = 0; i < 4; i++) v[i] = a[i];
+}
+
+// stores of rows that the kernel does not read again: non-temporal, so that
+// they do not push what is still to be read out of the caches
+__device__ __forceinline__ void store8_nt(uint16_t *p, const float *v) {
+  __builtin_nontemporal_store(pack8(v), (u32x4 *)p);
+}
+
+__device__ __forceinline__ void store8_nt(float *p, const float *v) {
+  __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4 *)p);
+  __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4 *)(p + 4));
+}
+
+__device__ __forceinline__ void store16_nt(uint16_t *p, const float *v) { store8_nt(p, v); }
+
+__device__ __forceinline__ void store16_nt(float *p, const float *v) {
+  __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4 *)p);
+}
+
 // 2^(s - 127) of a scale byte; 255 stands for a block that held a NaN or an
 // infinity and reads back as NaN.
 __device__ __forceinline__ float mx_scale(uint32_t s) {

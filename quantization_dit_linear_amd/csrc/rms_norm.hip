@@ -9,12 +9,11 @@
 // their own).
 //
 // Memory bound: every row is read once, kept in registers between the sum
-// of squares and the scaling, and written once.  64, 128 or 256 threads take a
-// row (by its length alone, so that a row's bits do not depend on the batch),
-// workgroups walk the rows, the next row's loads are issued before the present
-// one's reduction, and bf16 parameters stay in registers from row to row
-// (fp32 ones would take half the register file; they are read again, from the
-// caches).
+// of squares and the scaling, and written once.  64 to 512 threads take a row
+// (by its length alone, so that a row's bits do not depend on the batch), a
+// workgroup one row or a few short ones: workgroups that walk the rows with
+// their parameters held in registers and the next row prefetched were 10%
+// slower (32760 x 5120: 280 against 255 us), the parameters come from the L2.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -66,56 +65,46 @@ __device__ __forceinline__ float wave_sum(float v) {
 // T: stream type, P: parameter type, TPR threads a row, NCH 8-element chunks
 // a thread; MOD: with gate, scale or shift.
 template <class T, class P, int TPR, int NCH, bool MOD>
-__global__ __launch_bounds__(256, 2) void rms_norm_kernel(RmsNormArgs a) {
-  constexpr int RPW = 256 / TPR, WPR = TPR / 64;  // rows a workgroup, waves a row
-  constexpr bool HOLD = sizeof(P) == 2;
-  __shared__ float part[2][4];
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256, 2) void rms_norm_kernel(RmsNormArgs a) {
+  constexpr int TH = TPR > 256 ? TPR : 256;  // threads a workgroup
+  constexpr int RPW = TH / TPR, WPR = TPR / 64, WAVES = TH / 64;  // rows a workgroup, waves a row
+  // a bf16 weight is requested with the row (229 against 241 us at 32760 x
+  // 5120); more parameters than that, where they are used (242 against 254 us):
+  // waves in flight count more than the wait for the caches
+  constexpr bool EARLY = sizeof(P) == 2 && !MOD;
+  __shared__ float part[2][WAVES];
   const int tid = threadIdx.x, slot = tid / TPR, lt = tid % TPR, nch = a.d / 8;
   const float inv_d = 1.0f / (float)a.d;
-
-  Raw<P> pw[NCH], pg[NCH], ps[NCH], pb[NCH];
-  auto load_weight = [&](int i) {
-    const int c = lt + TPR * i;
-    if (a.weight && c < nch) pw[i].load((const P *)a.weight + 8 * c);
-    else pw[i].fill(1.f);
+  auto load_rest = [&](bool on, int c, int64_t mod, Raw<P> &w, Raw<P> &s, Raw<P> &b) {
+    if (on && a.weight) w.load((const P *)a.weight + 8 * c);
+    else w.fill(1.f);
+    if constexpr (MOD) {
+      if (on && a.scale) s.load((const P *)a.scale + mod + 8 * c);
+      else s.fill(0.f);
+      if (on && a.shift) b.load((const P *)a.shift + mod + 8 * c);
+      else b.fill(0.f);
+    }
   };
-  auto load_mod = [&](int i, int64_t grp) {
-    const int c = lt + TPR * i;
-    const int64_t at = grp * a.mod_stride + 8 * c;
-    if (a.gate && c < nch) pg[i].load((const P *)a.gate + at);
-    else pg[i].fill(1.f);
-    if (a.scale && c < nch) ps[i].load((const P *)a.scale + at);
-    else ps[i].fill(0.f);
-    if (a.shift && c < nch) pb[i].load((const P *)a.shift + at);
-    else pb[i].fill(0.f);
-  };
-  if constexpr (HOLD)
-#pragma unroll
-    for (int i = 0; i < NCH; i++) load_weight(i);
 
-  Raw<T> nx[NCH], nr[NCH];  // the next row
-  auto fetch = [&](int64_t row) {
+  int par = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPW; r0 < a.rows; r0 += (int64_t)gridDim.x * RPW) {
+    const int64_t row = r0 + slot, mod = MOD ? row / a.rows_per_mod * a.mod_stride : 0;
+    const bool in = row < a.rows;
+    // everything the row needs is requested before any of it is used
+    Raw<T> nx[NCH], nr[NCH];
+    Raw<P> pw[NCH], pg[NCH], ps[NCH], pb[NCH];
 #pragma unroll
     for (int i = 0; i < NCH; i++) {
       const int c = lt + TPR * i;
-      if (row < a.rows && c < nch) {
-        nx[i].load((const T *)a.x + row * a.d + 8 * c);
-        if (a.residual) nr[i].load((const T *)a.residual + row * a.d + 8 * c);
+      const bool on = in && c < nch;
+      if (on) nx[i].load((const T *)a.x + row * a.d + 8 * c);
+      if (on && a.residual) nr[i].load((const T *)a.residual + row * a.d + 8 * c);
+      if constexpr (MOD) {
+        if (on && a.gate) pg[i].load((const P *)a.gate + mod + 8 * c);
+        else pg[i].fill(1.f);
       }
+      if constexpr (EARLY) load_rest(on, c, mod, pw[i], ps[i], pb[i]);
     }
-  };
-  int64_t have = -1;  // the group whose parameters are held
-  int par = 0;
-  fetch((int64_t)blockIdx.x * RPW + slot);
-  for (int64_t r0 = (int64_t)blockIdx.x * RPW; r0 < a.rows; r0 += (int64_t)gridDim.x * RPW) {
-    const int64_t row = r0 + slot, grp = MOD ? row / a.rows_per_mod : 0;
-    const bool in = row < a.rows;
-    if constexpr (MOD)
-      if (in && (!HOLD || grp != have)) {
-#pragma unroll
-        for (int i = 0; i < NCH; i++) load_mod(i, grp);
-        have = grp;
-      }
     float h[NCH][8];
     float ss = 0.f;
 #pragma unroll
@@ -141,7 +130,6 @@ __global__ __launch_bounds__(256, 2) void rms_norm_kernel(RmsNormArgs a) {
 #pragma unroll
       for (int k = 0; k < 8; k++) ss = fmaf(h[i][k], h[i][k], ss);
     }
-    fetch(row + (int64_t)gridDim.x * RPW);
 
     // the row's total; `other`: any row's of the workgroup that is not finite
     auto total = [&](float v, bool &other) {
@@ -149,10 +137,10 @@ __global__ __launch_bounds__(256, 2) void rms_norm_kernel(RmsNormArgs a) {
       if constexpr (WPR > 1) {
         if ((tid & 63) == 0) part[par][tid >> 6] = v;
         __syncthreads();
-        float all[4], t = 0.f;
+        float all[WAVES], t = 0.f;
         other = false;
 #pragma unroll
-        for (int w = 0; w < 4; w++) all[w] = part[par][w];
+        for (int w = 0; w < WAVES; w++) all[w] = part[par][w];
 #pragma unroll
         for (int s = 0; s < RPW; s++) {
           float u = all[s * WPR];
@@ -190,9 +178,9 @@ __global__ __launch_bounds__(256, 2) void rms_norm_kernel(RmsNormArgs a) {
     for (int i = 0; i < NCH; i++) {
       const int c = lt + TPR * i;
       if (c >= nch) continue;
-      if (a.sum) store8((T *)a.sum + row * a.d + 8 * c, h[i]);
+      if (a.sum) store8_nt((T *)a.sum + row * a.d + 8 * c, h[i]);
       float y[8], w[8];
-      if constexpr (!HOLD) load_weight(i);
+      if constexpr (!EARLY) load_rest(true, c, mod, pw[i], ps[i], pb[i]);
       pw[i].get(w);
 #pragma unroll
       for (int k = 0; k < 8; k++) y[k] = h[i][k] * rs;
@@ -205,7 +193,7 @@ __global__ __launch_bounds__(256, 2) void rms_norm_kernel(RmsNormArgs a) {
 #pragma unroll
         for (int k = 0; k < 8; k++) y[k] *= w[k];
       }
-      if (a.out == 0) store8((T *)a.y + row * a.d + 8 * c, y);
+      if (a.out == 0) store8_nt((T *)a.y + row * a.d + 8 * c, y);
       else if (a.out == 1) mx_store8<1>(y, row * nch + c, (uint8_t *)a.y, a.y_scales);
       else mx_store8<0>(y, row * nch + c, (uint8_t *)a.y, a.y_scales);
     }
@@ -214,9 +202,9 @@ __global__ __launch_bounds__(256, 2) void rms_norm_kernel(RmsNormArgs a) {
 
 template <class T, class P, bool MOD>
 hipError_t launch_d(const RmsNormArgs &a) {
-  auto go = [&](auto kernel, int rows_per_wg) {
+  auto go = [&](auto kernel, int rows_per_wg, int threads = 256) {
     const int64_t wgs = (a.rows + rows_per_wg - 1) / rows_per_wg;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(wgs < 2048 ? wgs : 2048)), dim3(256), 0, a.stream, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(wgs < (1 << 20) ? wgs : 1 << 20)), dim3(threads), 0, a.stream, a);
     return hipGetLastError();
   };
   const int d = a.d;
@@ -225,7 +213,7 @@ hipError_t launch_d(const RmsNormArgs &a) {
   if (d <= 2048) return go(rms_norm_kernel<T, P, 64, 4, MOD>, 4);
   if (d <= 5 * 1024) return go(rms_norm_kernel<T, P, 128, 5, MOD>, 2);
   if (d <= 8 * 1024) return go(rms_norm_kernel<T, P, 256, 4, MOD>, 1);
-  return go(rms_norm_kernel<T, P, 256, 8, MOD>, 1);
+  return go(rms_norm_kernel<T, P, 512, 4, MOD>, 1, 512);
 }
 
 template <class T, class P>

@@ -40,20 +40,21 @@ __device__ __forceinline__ f32x2 cos_sin(uint32_t q) {
   return n & 2 ? f32x2{-a, -b} : f32x2{a, b};
 }
 
-constexpr int kPairs = 256;  // LDS table: pairs of the tokens that a workgroup takes
+constexpr int kPairs = 1024;  // LDS table: pairs of the tokens that a workgroup takes
 
-// blockIdx.x: a group of TOK tokens; blockIdx.y: a slice of `hs` heads.  One
-// item: 8 consecutive elements of a head (interleaved pairs), or elements u
-// and v of pairs 8c .. 8c+7 (half-split); the items behind them copy.
+// blockIdx.x: a group of tokens; blockIdx.y: a slice of `hs` heads.  One item:
+// E consecutive elements of a head, 16 bytes (interleaved pairs), or elements
+// u and v of pairs E c .. E c + E - 1 (half-split); the items behind them copy.
 template <class T, bool HALF>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int tok_group, int hs) {
   __shared__ __attribute__((aligned(16))) f32x2 table[kPairs + 8];
+  constexpr int E = 16 / sizeof(T);
   const int tid = threadIdx.x, half = a.turned / 2;
   const int h0 = blockIdx.y * hs, nh = a.heads - h0 < hs ? a.heads - h0 : hs;
 
   // items (token, head, c), c fastest; a thread's next is 256 further on
-  const int turned_items = HALF ? a.turned / 16 : (a.turned + 7) / 8;
-  const int per = HALF ? turned_items + (a.head_dim - a.turned) / 8 : a.head_dim / 8;
+  const int turned_items = HALF ? half / E : (a.turned + E - 1) / E;
+  const int per = HALF ? turned_items + (a.head_dim - a.turned) / E : a.head_dim / E;
   const int dc = 256 % per, dh = 256 / per % nh, dt = 256 / per / nh;
 
   for (int64_t t0 = (int64_t)blockIdx.x * tok_group; t0 < a.tokens;
@@ -79,21 +80,21 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int tok_group, in
     if (h >= nh) h -= nh, t++;
   };
   // four items at a time, all loads first
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;
+  constexpr int U = 4;
   while (t < nt) {
-    float u[U][8], v[U][8];
+    float u[U][E], v[U][E];
     int it[U], ic[U];
     const T *px[U];
     T *py[U];
 #pragma unroll
     for (int k = 0; k < U; k++) {
       it[k] = t, ic[k] = c;
-      const int at = !HALF || c < turned_items ? 8 * c : a.turned + 8 * (c - turned_items);
+      const int at = !HALF || c < turned_items ? E * c : a.turned + E * (c - turned_items);
       px[k] = xb + t * a.x_token + (int64_t)h * a.x_head + at;
       py[k] = yb + t * a.y_token + (int64_t)h * a.y_head + at;
       if (t < nt) {
-        load8(px[k], u[k]);
-        if (HALF && c < turned_items) load8(px[k] + half, v[k]);
+        load16(px[k], u[k]);
+        if (HALF && c < turned_items) load16(px[k] + half, v[k]);
       }
       next();
     }
@@ -101,20 +102,20 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int tok_group, in
     for (int k = 0; k < U; k++) {
       if (it[k] >= nt) break;
       if (ic[k] < turned_items) {
-        const f32x2 *z = table + it[k] * half + (HALF ? 8 : 4) * ic[k];
+        const f32x2 *z = table + it[k] * half + (HALF ? E : E / 2) * ic[k];
         if constexpr (HALF) {
 #pragma unroll
-          for (int e = 0; e < 8; e++) {
+          for (int e = 0; e < E; e++) {
             const float p = u[k][e] * z[e][0] - v[k][e] * z[e][1];
             v[k][e] = u[k][e] * z[e][1] + v[k][e] * z[e][0];
             u[k][e] = p;
           }
-          store8(py[k] + half, v[k]);
+          store16_nt(py[k] + half, v[k]);
         } else {
           // the last item may hold elements behind the turned ones
-          const int left = half - 4 * ic[k];
+          const int left = half - E / 2 * ic[k];
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
+          for (int e = 0; e < E / 2; e++) {
             const f32x2 w = e < left ? z[e] : f32x2{1.f, 0.f};
             const float p = u[k][2 * e] * w[0] - u[k][2 * e + 1] * w[1];
             const float q = u[k][2 * e] * w[1] + u[k][2 * e + 1] * w[0];
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int tok_group, in
           }
         }
       }
-      store8(py[k], u[k]);
+      store16_nt(py[k], u[k]);
     }
   }
   }
@@ -132,13 +133,16 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int tok_group, in
 }  // namespace
 
 hipError_t launch_rope(const RopeArgs &a) {
-  // as many tokens a workgroup as give its threads a pair each; one, and a
-  // slice of the heads, where tokens are too few to fill the card
-  const int half = a.turned / 2, fit = half > 0 ? kPairs / half : 8;
-  int group = fit < 1 ? 1 : fit > 8 ? 8 : fit;
-  if (a.tokens < 1024 * (int64_t)group) group = 1;
+  // as many tokens a workgroup as give its threads a pair and four items
+  // each; one, and a slice of the heads, where tokens are too few to fill the
+  // card
+  const int half = a.turned / 2, per = a.head_dim / 8, most = half > 0 ? kPairs / half : 64;
+  const int64_t items = 1024 / ((int64_t)a.heads * per);
+  int group = half > 0 ? 256 / half : 1;
+  if (group < items) group = (int)items;
+  if (group > most) group = most;
+  if (group < 1 || a.tokens < 1024 * (int64_t)group) group = 1;
   const int64_t gx = (a.tokens + group - 1) / group;
-  const int per = a.head_dim / 8;
   int hs = a.heads;
   while (gx * ((a.heads + hs - 1) / hs) < 1024 && hs * per > 256) hs = (hs + 1) / 2;
   const dim3 grid((unsigned)(gx < (1 << 20) ? gx : 1 << 20), (unsigned)((a.heads + hs - 1) / hs)), block(256);
