@@ -335,6 +335,15 @@ def rtn4_linear(x, q4, scales, *, out=None, stream=None):
 
 _MX = {"fp4": OQ_MX_FP4, "fp8": OQ_MX_FP8}
 _C_INTS = [ctypes.c_int * n for n in range(5)]
+_T = None  # torch, from the first call on
+
+
+def _torch():
+    global _T
+    if _T is None:
+        import torch
+        _T = torch
+    return _T
 
 
 def _mx(fmt, name="fmt"):
@@ -348,8 +357,7 @@ def _empty(shape, dtype, like, stream):
     """A fresh output beside `like`, owned by the stream that the call runs on."""
     if stream is None:
         return like.new_empty(shape, dtype=dtype)
-    import torch
-    with torch.cuda.stream(stream):
+    with _torch().cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
 
@@ -364,13 +372,15 @@ def _shaped(t, shape, dtype, name):
 
 def _call_device(*named):
     """The current device's index; every (tensor, name) must live there."""
-    import torch
+    tensor, dev = _torch().Tensor, -1
     for t, name in named:
-        if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda):
+        if t is None:
+            continue
+        if not isinstance(t, tensor) or not t.is_cuda:
             _on_device(t, name)
-    dev = torch.cuda.current_device()
-    for t, name in named:
-        if t is not None and t.get_device() != dev:
+        if dev < 0:
+            dev = _T.cuda.current_device()
+        if t.get_device() != dev:
             _on_device(t, name)
     return dev
 
@@ -392,35 +402,40 @@ def _strided_ptr(t, name):
 def _raw_stream(stream, dev):
     if stream is not None:
         return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev)
+    return _torch()._C._cuda_getCurrentRawStream(dev)
+
+
+def _element(t):
+    """OQ_F32 or OQ_BF16."""
+    dtype = t.dtype
+    return OQ_BF16 if dtype is _torch().bfloat16 else OQ_F32 if dtype is _T.float32 else _dtype_code(t)
 
 
 def _mx_outputs(codes, scales, rows, d, bits, like, stream):
-    import torch
+    u8 = _torch().uint8
     if codes is None:
-        codes = _empty((rows, d * bits // 8), torch.uint8, like, stream)
+        codes = _empty((rows, d * bits // 8), u8, like, stream)
     else:
-        _shaped(codes, (rows, d * bits // 8), torch.uint8, "codes")
+        _shaped(codes, (rows, d * bits // 8), u8, "codes")
     if scales is None:
-        scales = _empty((rows, d // 32), torch.uint8, like, stream)
+        scales = _empty((rows, d // 32), u8, like, stream)
     else:
-        _shaped(scales, (rows, d // 32), torch.uint8, "scales")
+        _shaped(scales, (rows, d // 32), u8, "scales")
     return codes, scales
 
 
 def _mx_pair(codes, scales, bits, codes_name, scales_name):
     """(rows, d) of a pair of MX arrays, whose shapes must agree."""
-    import torch
+    torch = _torch()
     for t, n in ((codes, codes_name), (scales, scales_name)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{n} must be a torch.Tensor")
-        if t.dim() != 2:
-            raise ValueError(f"{n} must be two-dimensional")
+        if t.dim() != 2 or t.dtype is not torch.uint8:
+            raise ValueError(f"{n} must be two-dimensional, of dtype torch.uint8")
     rows, d = scales.shape
     d *= 32
-    _shaped(codes, (rows, d * bits // 8), torch.uint8, codes_name)
-    _shaped(scales, (rows, d // 32), torch.uint8, scales_name)
+    if codes.shape != (rows, d * bits // 8):
+        _expect(codes, (rows, d * bits // 8), torch.uint8, codes_name)
     return rows, d
 
 
@@ -434,7 +449,7 @@ def mx_quantize(x, fmt, *, codes=None, scales=None, stream=None):
     rows, d = x.shape
     codes, scales = _mx_outputs(codes, scales, rows, d, bits, x, stream)
     dev = _call_device((x, "x"), (codes, "codes"), (scales, "scales"))
-    rc = lib().oq_mx_quantize(_ptr(x, "x"), _dtype_code(x), rows, d, bits, _ptr(codes, "codes"),
+    rc = lib().oq_mx_quantize(_ptr(x, "x"), _element(x), rows, d, bits, _ptr(codes, "codes"),
                               _ptr(scales, "scales"), _raw_stream(stream, dev))
     _check(rc, "oq_mx_quantize")
     return codes, scales
@@ -443,32 +458,30 @@ def mx_quantize(x, fmt, *, codes=None, scales=None, stream=None):
 def mx_dequantize(codes, scales, fmt, *, dtype=None, out=None, stream=None):
     """The values [rows, d] that MX codes stand for (bfloat16 unless dtype or
     out says float32)."""
-    import torch
     bits = _mx(fmt)
     rows, d = _mx_pair(codes, scales, bits, "codes", "scales")
     if out is None:
-        out = _empty((rows, d), dtype or torch.bfloat16, codes, stream)
+        out = _empty((rows, d), dtype or _T.bfloat16, codes, stream)
     else:
         _shaped(out, (rows, d), dtype or out.dtype, "out")
     dev = _call_device((codes, "codes"), (scales, "scales"), (out, "out"))
     rc = lib().oq_mx_dequantize(_ptr(codes, "codes"), _ptr(scales, "scales"), bits, rows, d,
-                                _dtype_code(out), _ptr(out, "out"), _raw_stream(stream, dev))
+                                _element(out), _ptr(out, "out"), _raw_stream(stream, dev))
     _check(rc, "oq_mx_dequantize")
     return out
 
 
 def mx_linear(a_codes, a_scales, a_fmt, w_codes, w_scales, w_fmt, *, out=None, stream=None):
     """bf16 y [M, N] = A W^T of MX activations [M, K] and weights [N, K]."""
-    import torch
     a_bits, w_bits = _mx(a_fmt, "a_fmt"), _mx(w_fmt, "w_fmt")
     M, K = _mx_pair(a_codes, a_scales, a_bits, "a_codes", "a_scales")
     N, Kw = _mx_pair(w_codes, w_scales, w_bits, "w_codes", "w_scales")
     if K != Kw:
         raise ValueError(f"activations have {K} columns, weights {Kw}")
     if out is None:
-        out = _empty((M, N), torch.bfloat16, a_codes, stream)
+        out = _empty((M, N), _T.bfloat16, a_codes, stream)
     else:
-        _shaped(out, (M, N), torch.bfloat16, "out")
+        _shaped(out, (M, N), _T.bfloat16, "out")
     dev = _call_device((a_codes, "a_codes"), (a_scales, "a_scales"), (w_codes, "w_codes"),
                        (w_scales, "w_scales"), (out, "out"))
     rc = lib().oq_mx_linear(_ptr(a_codes, "a_codes"), _ptr(a_scales, "a_scales"), a_bits,
@@ -536,12 +549,12 @@ def add_rms_norm(x, residual=None, *, weight=None, gate=None, scale=None, shift=
                        (scale, "scale"), (shift, "shift"), (sum_out, "sum_out"), (out, "out"),
                        (scales, "scales_out"))
     rc = lib().oq_add_rms_norm(
-        _ptr(x, "x"), None if residual is None else _ptr(residual, "residual"), _dtype_code(x),
+        _ptr(x, "x"), None if residual is None else _ptr(residual, "residual"), _element(x),
         rows, d, eps, None if weight is None else _ptr(weight, "weight"),
         None if gate is None else _strided_ptr(gate, "gate"),
         None if scale is None else _strided_ptr(scale, "scale"),
         None if shift is None else _strided_ptr(shift, "shift"),
-        OQ_F32 if first is None else _dtype_code(first), rows_per_mod, stride,
+        OQ_F32 if first is None else _element(first), rows_per_mod, stride,
         None if sum_out is None else _ptr(sum_out, "sum_out"), bits, _ptr(out, "out"),
         None if scales is None else _ptr(scales, "scales_out"), _raw_stream(stream, dev))
     _check(rc, "oq_add_rms_norm")
@@ -555,21 +568,20 @@ def rope(x, pos, axis_dims, *, theta=10000.0, half=False, inverse=False, out=Non
     head that turn with each axis (one to four).  half: pairs (j, j + R/2)
     instead of (2j, 2j+1); inverse: the opposite turn, which is the gradient.
     out may be x."""
-    import torch
     if x.dim() != 3:
         raise ValueError("x must be [tokens, heads, head_dim]")
     tokens, heads, hd = x.shape
     axes = len(axis_dims)
     if not 1 <= axes <= 4:
         raise ValueError(f"axis_dims must name one to four axes (got {axes})")
-    _shaped(pos, (tokens, axes), torch.int32, "pos")
+    _shaped(pos, (tokens, axes), _torch().int32, "pos")
     if out is None:
         out = _empty((tokens, heads, hd), x.dtype, x, stream)
     else:
         _shaped(out, (tokens, heads, hd), x.dtype, "out")
     dev = _call_device((x, "x"), (pos, "pos"), (out, "out"))
     flags = (OQ_ROPE_HALF if half else 0) | (OQ_ROPE_INVERSE if inverse else 0)
-    rc = lib().oq_rope(_strided_ptr(x, "x"), _dtype_code(x), tokens, heads, hd, x.stride(0),
+    rc = lib().oq_rope(_strided_ptr(x, "x"), _element(x), tokens, heads, hd, x.stride(0),
                        x.stride(1), _ptr(pos, "pos"), axes, _C_INTS[axes](*axis_dims), theta,
                        flags, _strided_ptr(out, "out"), out.stride(0), out.stride(1),
                        _raw_stream(stream, dev))
