@@ -31,25 +31,22 @@ constexpr int kGroupM = 4;  // tile rows per group of the tile order
 
 // A workgroup of 2 x WN waves computes a (64 IB) x (32 WN JB) tile; each wave
 // a (32 IB) x (32 JB) block of it.
-template <int FA, int FW, int WN_, int IB_, int JB_, int WGS_>
+template <int FA, int FW, int WN_, int IB_, int JB_, int WGS_, int KS_, int NST_>
 struct MxTile {
-  static constexpr int WN = WN_, IB = IB_, JB = JB_, WGS = WGS_;
+  static constexpr int WN = WN_, IB = IB_, JB = JB_, WGS = WGS_, NST = NST_;
   static constexpr int THREADS = 128 * WN;
   static constexpr int TM = 64 * IB, TN = 32 * WN * JB;
-  // Elements of K a stage: 128 bytes of a row (64 of 4-bit weights against
-  // 8-bit activations), so that a row's request is a whole line of the L2,
-  // and the same matrix-core time either way (8-bit elements run at half rate).
-  static constexpr int KS = (FA || FW) ? 128 : 256;
+  static constexpr int KS = KS_;                                        // elements of K a stage
   static constexpr int STEPS = KS / 64;                                 // products in depth
   static constexpr int RA = KS / (FA ? 1 : 2), RW = KS / (FW ? 1 : 2);  // row bytes a stage
   static constexpr int AB = TM * RA, STAGE = AB + TN * RW;
   static constexpr int SROWS = TM + TN;
   static constexpr int SBUF = 4 * SROWS * 4;     // scales of 16 blocks: 4 planes of one word a row
   static constexpr int SPG = 512 / KS;           // stages that one such group lasts
-  static constexpr int EROWS = 16;               // output rows a wave stages at once
+  static constexpr int EROWS = 32;               // output rows a wave stages at once
   static constexpr int EPI = EROWS * 64 * JB;
-  static constexpr int SC0 = 2 * STAGE, EP0 = SC0 + 2 * SBUF;
-  static constexpr int LDS = EP0 + 2 * WN * EPI;
+  static constexpr int SC0 = NST * STAGE, LDS = SC0 + 2 * SBUF;
+  static_assert(2 * WN * EPI <= SC0, "the output goes through the stages' LDS");
   static_assert(LDS * WGS <= 160 * 1024, "LDS of one CU");
 };
 
@@ -70,8 +67,6 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint8_t *
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)dst, 16, off, base, 0, 0);
 }
 
-// Waits until at most N of this wave's memory requests are outstanding and
-// its LDS requests are done, then for the other waves.
 template <int N>
 __device__ __forceinline__ void wait_and_sync() {
   asm volatile("" ::: "memory");
@@ -120,6 +115,7 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
   constexpr int LA = PA / TH, LW = PW / TH, NL = LA + LW;
   // pieces requested in the last step of a stage, the others in the first of the next
   constexpr int LL = TL::STEPS == 4 ? NL / 2 : NL;
+  constexpr int NST = TL::NST;
   static_assert(PA % TH == 0 && PW % TH == 0, "whole rounds of requests");
   const int ra0 = tid / CA, ca0 = (tid % CA) ^ swizzle<RA>(ra0);
   const int rw0 = tid / CW, cw0 = (tid % CW) ^ swizzle<RW>(rw0);
@@ -269,13 +265,14 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
           w[S & 1][j].op(), a[S & 1][i].op(), acc[j][i], FW ? 0 : 4, FA ? 0 : 4, S, sw[j], S, sa[i]);
     };
 
+    wait_and_sync<63>();  // the previous tile's output has left LDS
     load_groups(x, 0);
 #pragma unroll
-    for (int t = 0; t < 2; t++)
+    for (int t = 0; t < NST; t++)
 #pragma unroll
-      for (int k = 0; k < (t ? LL : NL); k++) load_piece(x, t, t, k);
+      for (int k = 0; k < (t == NST - 1 ? LL : NL); k++) load_piece(x, t, t, k);
     store_group(x, 0);
-    wait_and_sync<LL>();
+    wait_and_sync<(NST - 2) * NL + LL>();
 #pragma unroll
     for (int k = 0; k < NR; k++) read_frag(0, 0, k);
 #pragma unroll
@@ -291,7 +288,7 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
     // matrix cores always have the next one.
     constexpr int NM = IB * JB;
     int cur = 0;
-    auto step = [&](int t, auto c) {
+    auto step = [&](int t, int nxt, int prv, auto c) {
       constexpr int S = decltype(c)::value;
       constexpr bool LAST = S == TL::STEPS - 1;
       constexpr int R = LAST ? NR + IB + JB : NR;
@@ -302,13 +299,13 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
 #pragma unroll
         for (int o = k * R / NM; o < (k + 1) * R / NM; o++) {
           if (!LAST) read_frag(cur, S + 1, o);
-          else if (o < NR) read_frag(cur ^ 1, 0, o);
+          else if (o < NR) read_frag(nxt, 0, o);
           else read_scale(t + 1, o - NR);
         }
-        // pieces LL .. NL of stage t + 1, or 0 .. LL of stage t + 2
+        // pieces 0 .. LL of stage t + NST, or LL .. NL of the stage before it
 #pragma unroll
         for (int o = L0 + k * (L1 - L0) / NM; o < L0 + (k + 1) * (L1 - L0) / NM; o++)
-          load_piece(x, LAST ? t + 2 : t + 1, LAST ? cur : cur ^ 1, o);
+          load_piece(x, LAST ? t + NST : t + NST - 1, LAST ? cur : prv, o);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -318,15 +315,16 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
       // (branches only here: the products below stay one block, in order)
       if (more && ph == 0 && (grp & 1)) load_groups(x, grp + 1);
       if (more && ph == TL::SPG / 2) store_group(x, grp + 1);
-      step(t, std::integral_constant<int, 0>{});
+      const int nxt = cur + 1 == NST ? 0 : cur + 1, prv = cur == 0 ? NST - 1 : cur - 1;
+      step(t, nxt, prv, std::integral_constant<int, 0>{});
       if constexpr (TL::STEPS == 4) {
-        step(t, std::integral_constant<int, 1>{});
-        step(t, std::integral_constant<int, 2>{});
+        step(t, nxt, prv, std::integral_constant<int, 1>{});
+        step(t, nxt, prv, std::integral_constant<int, 2>{});
       }
-      wait_and_sync<0>();
-      step(t, std::integral_constant<int, TL::STEPS - 1>{});
+      wait_and_sync<(NST - 2) * NL>();
+      step(t, nxt, prv, std::integral_constant<int, TL::STEPS - 1>{});
       take_scales();
-      cur ^= 1;
+      cur = nxt;
     }
     wait_and_sync<0>();  // the requests past the last stage are done, every buffer is free
 
@@ -334,7 +332,7 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
     // wave's own LDS region (16-byte pieces XOR-swizzled by the row), out as
     // whole rows in 16-byte pieces.  Lane (r, g) holds row r, columns
     // 32 j + 8 q + 4 g + (0..3); half of the lanes have a row of the pass.
-    uint8_t *reg = lds + TL::EP0 + wave * TL::EPI;
+    uint8_t *reg = lds + wave * TL::EPI;
     constexpr int PPR = 4 * JB, ER = TL::EROWS;  // pieces per row
     int lane_ = lane;  // opaque: keeps the addresses below out of the K loop's registers
     asm volatile("" : "+v"(lane_));
@@ -344,7 +342,7 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
     for (int i = 0; i < IB; i++) {
 #pragma unroll
       for (int half = 0; half < 32 / ER; half++) {
-        if (((lane_ >> 4) & 1) == half) {
+        if (ER == 32 || ((lane_ >> 4) & 1) == half) {
 #pragma unroll
           for (int j = 0; j < JB; j++)
 #pragma unroll
@@ -517,10 +515,27 @@ template <int FA, int FW>
 hipError_t launch_pair(const MxLinearArgs &a, int cus) {
   const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
   const int64_t mid = ((a.M + 127) / 128) * ((a.N + 127) / 128);
+#ifndef B_KS
+#define B_KS (FA || FW ? 128 : 256)
+#define B_NST 2
+#endif
+#ifndef M_KS
+#define M_KS (FA || FW ? 128 : 256)
+#define M_NST 2
+#define M_WGS 2
+#endif
+#ifndef S_KS
+#define S_KS (FA || FW ? 128 : 256)
+#define S_NST 2
+#define S_WGS 4
+#endif
+#define TB MxTile<FA, FW, 4, 4, 2, 1, B_KS, B_NST>
+#define TMID MxTile<FA, FW, 2, 2, 2, M_WGS, M_KS, M_NST>
+#define TS MxTile<FA, FW, 2, 1, 1, S_WGS, S_KS, S_NST>
 #ifdef FORCE
-  if (FORCE == 4) return launch_tiles<FA, FW, MxTile<FA, FW, 4, 4, 2, 1>>(a, cus);
-  if (FORCE == 2) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 2, 2, 2>>(a, cus);
-  if (FORCE == 1) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 1, 1, 4>>(a, cus);
+  if (FORCE == 4) return launch_tiles<FA, FW, TB>(a, cus);
+  if (FORCE == 2) return launch_tiles<FA, FW, TMID>(a, cus);
+  if (FORCE == 1) return launch_tiles<FA, FW, TS>(a, cus);
 #endif
   // Rows kernel: up to 32 rows, or so few 64 x 64 tiles that they leave most
   // CUs without one; 32 columns a workgroup where that still gives enough
@@ -532,9 +547,9 @@ hipError_t launch_pair(const MxLinearArgs &a, int cus) {
     if (a.M <= 32) return wide ? launch_rows<FA, FW, 2, 2>(a) : launch_rows<FA, FW, 2, 1>(a);
     return wide ? launch_rows<FA, FW, 4, 2>(a) : launch_rows<FA, FW, 4, 1>(a);
   }
-  if (big >= cus) return launch_tiles<FA, FW, MxTile<FA, FW, 4, 4, 2, 1>>(a, cus);
-  if (mid >= cus) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 2, 2, 2>>(a, cus);
-  return launch_tiles<FA, FW, MxTile<FA, FW, 2, 1, 1, 4>>(a, cus);
+  if (big >= cus) return launch_tiles<FA, FW, TB>(a, cus);
+  if (mid >= cus) return launch_tiles<FA, FW, TMID>(a, cus);
+  return launch_tiles<FA, FW, TS>(a, cus);
 }
 
 }  // namespace
