@@ -511,45 +511,37 @@ hipError_t launch_tiles(const MxLinearArgs &a, int cus) {
   return hipGetLastError();
 }
 
+// Which kernel, by the number of 64 x 64, 128 x 128 tiles that the output has
+// (us at K = 5120, e2m1 on both sides):
+//   rows, up to 32 rows, or so few 64 tiles that they leave half of the CUs
+//     without one (64 x 5120: 10.9 against 16.6); 32 columns a workgroup where
+//     that still gives a workgroup to half of the CUs, else 16 (1 x 5120: 6.0
+//     against 6.8; 64 x 1024 at K = 16384: 34 against 28.7)
+//   64 tiles as long as all of them are resident, two a CU with three stages
+//     each (128 x 5120: 13.1, 128 tiles 16.9; 256 x 13824, three a CU: 38, 30)
+//   128 tiles likewise, two a CU (1024 x 5120: 24, 256 tiles 34; 509 x 13824:
+//     26, 34)
+//   256 tiles beyond (2048 x 5120: 36, 128 tiles in two rounds 44)
 template <int FA, int FW>
 hipError_t launch_pair(const MxLinearArgs &a, int cus) {
-  const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  const int64_t mid = ((a.M + 127) / 128) * ((a.N + 127) / 128);
-#ifndef B_KS
-#define B_KS (FA || FW ? 128 : 256)
-#define B_NST 2
-#endif
-#ifndef M_KS
-#define M_KS (FA || FW ? 128 : 256)
-#define M_NST 2
-#define M_WGS 2
-#endif
-#ifndef S_KS
-#define S_KS (FA || FW ? 128 : 256)
-#define S_NST 2
-#define S_WGS 4
-#endif
-#define TB MxTile<FA, FW, 4, 4, 2, 1, B_KS, B_NST>
-#define TMID MxTile<FA, FW, 2, 2, 2, M_WGS, M_KS, M_NST>
-#define TS MxTile<FA, FW, 2, 1, 1, S_WGS, S_KS, S_NST>
-#ifdef FORCE
-  if (FORCE == 4) return launch_tiles<FA, FW, TB>(a, cus);
-  if (FORCE == 2) return launch_tiles<FA, FW, TMID>(a, cus);
-  if (FORCE == 1) return launch_tiles<FA, FW, TS>(a, cus);
-#endif
-  // Rows kernel: up to 32 rows, or so few 64 x 64 tiles that they leave most
-  // CUs without one; 32 columns a workgroup where that still gives enough
-  // workgroups, 16 otherwise.
-  const int64_t small = ((a.M + 63) / 64) * ((a.N + 63) / 64);
+  // a stage: 128 bytes of a row (64 of 4-bit weights against 8-bit
+  // activations), so that a row's request is a whole line of the L2, and the
+  // same matrix-core time either way (8-bit elements run at half rate);
+  // 64-byte pieces in a deeper ring: 1.38 against 1.24 ms at 32760 x 15360 x 5120
+  constexpr int KS = FA || FW ? 128 : 256;
+  auto tiles = [&](int64_t t) { return ((a.M + t - 1) / t) * ((a.N + t - 1) / t); };
+  const int64_t small = tiles(64);
   if (a.M <= 32 || 2 * small <= cus) {
-    const bool wide = ((a.M + 63) / 64) * ((a.N + 31) / 32) > cus / 2;
+    const bool wide = 2 * ((a.M + 63) / 64) * ((a.N + 31) / 32) > cus;
     if (a.M <= 16) return wide ? launch_rows<FA, FW, 1, 2>(a) : launch_rows<FA, FW, 1, 1>(a);
     if (a.M <= 32) return wide ? launch_rows<FA, FW, 2, 2>(a) : launch_rows<FA, FW, 2, 1>(a);
     return wide ? launch_rows<FA, FW, 4, 2>(a) : launch_rows<FA, FW, 4, 1>(a);
   }
-  if (big >= cus) return launch_tiles<FA, FW, TB>(a, cus);
-  if (mid >= cus) return launch_tiles<FA, FW, TMID>(a, cus);
-  return launch_tiles<FA, FW, TS>(a, cus);
+  if (small <= 2 * cus) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 1, 1, 2, KS, 3>>(a, cus);
+  if (tiles(128) <= 2 * cus) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 2, 2, 2, KS, 2>>(a, cus);
+  // three stages where they fit: 1.68 against 1.70 ms at 32760 x 5120 x 13824
+  constexpr int NST = (FA || FW) && !(FA && FW) ? 3 : 2;
+  return launch_tiles<FA, FW, MxTile<FA, FW, 4, 4, 2, 1, KS, NST>>(a, cus);
 }
 
 }  // namespace
