@@ -329,7 +329,7 @@ int oq_mx_linear(const uint8_t *a_codes, const uint8_t *a_scales, int a_format,
  *     row g at g * mod_stride elements (mod_stride >= d, a multiple of 16
  *     bytes, where there is more than one group: the slices of one modulation
  *     projection [groups][6 d] are passed as they lie)
- *   eps > 0
+ *   eps: finite, at least the smallest normal fp32 number
  *   sum: device, dtype [rows][d], receives h; may be NULL
  *   y_format 0: y is dtype [rows][d] and y_scales is NULL; OQ_MX_FP4 or
  *     OQ_MX_FP8: y are MX codes and y_scales their scale bytes, as

@@ -401,6 +401,8 @@ def _strided_ptr(t, name):
 
 def _raw_stream(stream, dev):
     if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"stream belongs to {stream.device}, not to the current device cuda:{dev}")
         return stream.cuda_stream
     return _torch()._C._cuda_getCurrentRawStream(dev)
 
@@ -411,16 +413,18 @@ def _element(t):
     return OQ_BF16 if dtype is _torch().bfloat16 else OQ_F32 if dtype is _T.float32 else _dtype_code(t)
 
 
+def _check_mx_outputs(codes, scales, rows, d, bits):
+    if codes is not None:
+        _shaped(codes, (rows, d * bits // 8), _torch().uint8, "codes")
+    if scales is not None:
+        _shaped(scales, (rows, d // 32), _torch().uint8, "scales")
+
+
 def _mx_outputs(codes, scales, rows, d, bits, like, stream):
-    u8 = _torch().uint8
     if codes is None:
-        codes = _empty((rows, d * bits // 8), u8, like, stream)
-    else:
-        _shaped(codes, (rows, d * bits // 8), u8, "codes")
+        codes = _empty((rows, d * bits // 8), _T.uint8, like, stream)
     if scales is None:
-        scales = _empty((rows, d // 32), u8, like, stream)
-    else:
-        _shaped(scales, (rows, d // 32), u8, "scales")
+        scales = _empty((rows, d // 32), _T.uint8, like, stream)
     return codes, scales
 
 
@@ -447,8 +451,9 @@ def mx_quantize(x, fmt, *, codes=None, scales=None, stream=None):
     if x.dim() != 2:
         raise ValueError("x must be [rows, d]")
     rows, d = x.shape
-    codes, scales = _mx_outputs(codes, scales, rows, d, bits, x, stream)
+    _check_mx_outputs(codes, scales, rows, d, bits)
     dev = _call_device((x, "x"), (codes, "codes"), (scales, "scales"))
+    codes, scales = _mx_outputs(codes, scales, rows, d, bits, x, stream)
     rc = lib().oq_mx_quantize(_ptr(x, "x"), _element(x), rows, d, bits, _ptr(codes, "codes"),
                               _ptr(scales, "scales"), _raw_stream(stream, dev))
     _check(rc, "oq_mx_quantize")
@@ -460,11 +465,11 @@ def mx_dequantize(codes, scales, fmt, *, dtype=None, out=None, stream=None):
     out says float32)."""
     bits = _mx(fmt)
     rows, d = _mx_pair(codes, scales, bits, "codes", "scales")
-    if out is None:
-        out = _empty((rows, d), dtype or _T.bfloat16, codes, stream)
-    else:
+    if out is not None:
         _shaped(out, (rows, d), dtype or out.dtype, "out")
     dev = _call_device((codes, "codes"), (scales, "scales"), (out, "out"))
+    if out is None:
+        out = _empty((rows, d), dtype or _T.bfloat16, codes, stream)
     rc = lib().oq_mx_dequantize(_ptr(codes, "codes"), _ptr(scales, "scales"), bits, rows, d,
                                 _element(out), _ptr(out, "out"), _raw_stream(stream, dev))
     _check(rc, "oq_mx_dequantize")
@@ -478,12 +483,12 @@ def mx_linear(a_codes, a_scales, a_fmt, w_codes, w_scales, w_fmt, *, out=None, s
     N, Kw = _mx_pair(w_codes, w_scales, w_bits, "w_codes", "w_scales")
     if K != Kw:
         raise ValueError(f"activations have {K} columns, weights {Kw}")
-    if out is None:
-        out = _empty((M, N), _T.bfloat16, a_codes, stream)
-    else:
+    if out is not None:
         _shaped(out, (M, N), _T.bfloat16, "out")
     dev = _call_device((a_codes, "a_codes"), (a_scales, "a_scales"), (w_codes, "w_codes"),
                        (w_scales, "w_scales"), (out, "out"))
+    if out is None:
+        out = _empty((M, N), _T.bfloat16, a_codes, stream)
     rc = lib().oq_mx_linear(_ptr(a_codes, "a_codes"), _ptr(a_scales, "a_scales"), a_bits,
                             _ptr(w_codes, "w_codes"), _ptr(w_scales, "w_scales"), w_bits, M, N, K,
                             _ptr(out, "out"), _raw_stream(stream, dev))
@@ -529,25 +534,28 @@ def add_rms_norm(x, residual=None, *, weight=None, gate=None, scale=None, shift=
         rows_per_mod = max(1, -(-rows // max(1, groups)))
     if mods and (rows_per_mod < 1 or -(-rows // rows_per_mod) > groups):
         raise ValueError(f"{rows} rows at {rows_per_mod} per group need more than {groups} groups")
+    if sum_out is not None and sum_out is not False:
+        _shaped(sum_out, (rows, d), x.dtype, "sum_out")
+    bits = 0
+    if fmt is not None:
+        bits = _mx(fmt)
+        _check_mx_outputs(out, scales_out, rows, d, bits)
+    elif scales_out is not None:
+        raise ValueError("scales_out needs a fmt")
+    elif out is not None:
+        _shaped(out, (rows, d), x.dtype, "out")
+    dev = _call_device((x, "x"), (residual, "residual"), (weight, "weight"), (gate, "gate"),
+                       (scale, "scale"), (shift, "shift"), (None if sum_out is False else sum_out, "sum_out"),
+                       (out, "out"), (scales_out, "scales_out"))
     if sum_out is None:
         sum_out = _empty((rows, d), x.dtype, x, stream)
     elif sum_out is False:
         sum_out = None
-    else:
-        _shaped(sum_out, (rows, d), x.dtype, "sum_out")
-    scales, bits = None, 0
+    scales = None
     if fmt is not None:
-        bits = _mx(fmt)
         out, scales = _mx_outputs(out, scales_out, rows, d, bits, x, stream)
-    elif scales_out is not None:
-        raise ValueError("scales_out needs a fmt")
     elif out is None:
         out = _empty((rows, d), x.dtype, x, stream)
-    else:
-        _shaped(out, (rows, d), x.dtype, "out")
-    dev = _call_device((x, "x"), (residual, "residual"), (weight, "weight"), (gate, "gate"),
-                       (scale, "scale"), (shift, "shift"), (sum_out, "sum_out"), (out, "out"),
-                       (scales, "scales_out"))
     rc = lib().oq_add_rms_norm(
         _ptr(x, "x"), None if residual is None else _ptr(residual, "residual"), _element(x),
         rows, d, eps, None if weight is None else _ptr(weight, "weight"),
@@ -575,11 +583,11 @@ def rope(x, pos, axis_dims, *, theta=10000.0, half=False, inverse=False, out=Non
     if not 1 <= axes <= 4:
         raise ValueError(f"axis_dims must name one to four axes (got {axes})")
     _shaped(pos, (tokens, axes), _torch().int32, "pos")
-    if out is None:
-        out = _empty((tokens, heads, hd), x.dtype, x, stream)
-    else:
+    if out is not None:
         _shaped(out, (tokens, heads, hd), x.dtype, "out")
     dev = _call_device((x, "x"), (pos, "pos"), (out, "out"))
+    if out is None:
+        out = _empty((tokens, heads, hd), x.dtype, x, stream)
     flags = (OQ_ROPE_HALF if half else 0) | (OQ_ROPE_INVERSE if inverse else 0)
     rc = lib().oq_rope(_strided_ptr(x, "x"), _element(x), tokens, heads, hd, x.stride(0),
                        x.stride(1), _ptr(pos, "pos"), axes, _C_INTS[axes](*axis_dims), theta,

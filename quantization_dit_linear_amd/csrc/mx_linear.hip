@@ -531,7 +531,7 @@ hipError_t launch_pair(const MxLinearArgs &a, int cus) {
   constexpr int KS = FA || FW ? 128 : 256;
   auto tiles = [&](int64_t t) { return ((a.M + t - 1) / t) * ((a.N + t - 1) / t); };
   const int64_t small = tiles(64);
-  if (a.M <= 32 || 2 * small <= cus) {
+  if ((a.M <= 32 && a.N <= 1 << 26) || 2 * small <= cus) {
     const bool wide = 2 * ((a.M + 63) / 64) * ((a.N + 31) / 32) > cus;
     if (a.M <= 16) return wide ? launch_rows<FA, FW, 1, 2>(a) : launch_rows<FA, FW, 1, 1>(a);
     if (a.M <= 32) return wide ? launch_rows<FA, FW, 2, 2>(a) : launch_rows<FA, FW, 2, 1>(a);

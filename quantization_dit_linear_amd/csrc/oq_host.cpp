@@ -582,14 +582,14 @@ const char *oq_strerror(int status) {
   switch (status) {
     case OQ_OK: return "success";
     case OQ_EINVAL: return "invalid argument (null or misaligned pointer, bad size, dtype or flag)";
-    case OQ_EUNSUPPORTED: return "unsupported configuration (d must be a multiple of 32 in [32, 16384], and the linear's K a multiple of 64; bits in {2,3,4,8}; 8 bits on both sides of a linear; the sphere codebook at 1-4 and 8 bits)";
+    case OQ_EUNSUPPORTED: return "unsupported configuration (d must be a multiple of 32 in [32, 16384], and the linear's K a multiple of 64; bits in {2,3,4,8}; 8 bits on both sides of a linear; the sphere codebook at 1-4 and 8 bits; the MX calls at up to 2^30 rows; the rotary embedding at head_dim a multiple of 8 up to 512, up to 4 axes, a multiple of 16 turned elements in halves)";
     case OQ_ENOMEM: return "out of device memory for the rotation plan";
     case OQ_EDEVICE: return "HIP runtime or kernel launch failure";
     default: return "unknown status";
   }
 }
 
-int oq_version(void) { return 100; }
+int oq_version(void) { return 101; }
 
 int oq_codebook_ex(int d, int bits, uint32_t flags, float *levels, float *thresholds) {
   if (!levels || !thresholds || d < 1) return OQ_EINVAL;
@@ -881,7 +881,7 @@ int oq_add_rms_norm(const void *x, const void *residual, int dtype, int64_t rows
   if (dtype != OQ_F32 && dtype != OQ_BF16) return OQ_EINVAL;
   if (param_dtype != OQ_F32 && param_dtype != OQ_BF16) return OQ_EINVAL;
   const int f = y_format == 0 ? 0 : mx_format(y_format);
-  if (f < 0 || !(eps > 0.f) || !std::isfinite(eps)) return OQ_EINVAL;
+  if (f < 0 || !(eps >= std::numeric_limits<float>::min()) || !std::isfinite(eps)) return OQ_EINVAL;
   const int rc = check_mx_shape(rows, d);
   if (rc != OQ_OK) return rc;
   const bool mod = gate || scale || shift;
@@ -961,6 +961,8 @@ int oq_rope(const void *x, int dtype, int64_t tokens, int heads, int head_dim, i
   if (tokens > kMaxRows) return OQ_EUNSUPPORTED;
   if (tokens == 0 || heads == 0) return OQ_OK;
   if (!x || !y || !pos) return OQ_EINVAL;
+  if (tokens == 1) x_token = y_token = 0;  // the stride of a single one is not used
+  if (heads == 1) x_head = y_head = 0;
   const int size = elem_bytes(dtype), unit = 16 / size;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(pos, 4)) return OQ_EINVAL;
   if (x_token % unit || x_head % unit || y_token % unit || y_head % unit) return OQ_EINVAL;

@@ -141,10 +141,13 @@ def _check_linear(q, M, N, K, fa, fw):
     assert np.linalg.norm(y - want) <= 2.0 ** -8 * np.linalg.norm(want) + 1e-37
 
 
+# few rows; few tiles; resident 64, 128 and 256 tiles: each with whole and
+# ragged edges, K below, at and above one load of scales
 LINEAR = [(1, 1, 32), (1, 16, 64), (3, 5, 96), (16, 16, 128), (17, 33, 160), (31, 257, 256),
           (2, 640, 5120), (64, 64, 512), (128, 130, 544), (255, 257, 1024), (513, 300, 416),
           (300, 515, 2592), (1, 5120, 1024), (5, 128, 16384), (16, 1000, 3200), (33, 4096, 1280),
-          (1000, 1000, 288), (1025, 2049, 480)]
+          (1000, 1000, 288), (1025, 2049, 480), (700, 900, 2592), (1500, 1600, 2080), (2900, 2950, 2592),
+          (3000, 3100, 480), (2817, 3090, 32)]
 
 
 @pytest.mark.parametrize("fa,fw", [("fp4", "fp4"), ("fp8", "fp4"), ("fp4", "fp8"), ("fp8", "fp8")])
@@ -155,7 +158,8 @@ def test_linear(q, M, N, K, fa, fw):
 
 
 @pytest.mark.parametrize("fa", ["fp4", "fp8"])
-@pytest.mark.parametrize("M,N,K", [(4, 48, 320), (40, 200, 320), (600, 520, 320)])
+@pytest.mark.parametrize("M,N,K", [(4, 48, 320), (40, 200, 320), (600, 520, 320), (1000, 900, 320), (1500, 1600, 320),
+                                   (3000, 3100, 320)])
 def test_linear_is_exact_on_small_integers(q, M, N, K, fa):
     """Elements in {-1, 0, 1} under scale 1: every sum is a whole number below
     256, which bf16 holds, so a misplaced element or scale shows at once."""
@@ -170,7 +174,8 @@ def test_linear_is_exact_on_small_integers(q, M, N, K, fa):
 
 
 @pytest.mark.parametrize("fa,fw", [("fp4", "fp4"), ("fp8", "fp4"), ("fp8", "fp8")])
-@pytest.mark.parametrize("M,N,K", [(5, 70, 160), (70, 90, 288), (520, 513, 160)])
+@pytest.mark.parametrize("M,N,K", [(5, 70, 160), (70, 90, 288), (520, 513, 160), (900, 800, 1184),
+                                   (1500, 1600, 160), (2900, 3000, 544)])
 def test_linear_nan_block_reaches_its_row_only(q, M, N, K, fa, fw):
     say("mx linear nan", M, N, K, fa, fw)
     ac, as_ = _codes(M, K, fa, 1)
@@ -193,7 +198,8 @@ def test_linear_nan_block_reaches_its_row_only(q, M, N, K, fa, fw):
 def test_linear_writes_only_y(q):
     """Guard bytes around y stay as they were, at sizes that end inside a tile."""
     import torch
-    for M, N, K in ((3, 19, 96), (65, 77, 128), (300, 270, 224)):
+    for M, N, K in ((3, 19, 96), (65, 77, 128), (300, 270, 224), (900, 801, 96), (1500, 1607, 96),
+                    (2900, 2951, 224)):
         say("mx linear guards", M, N, K)
         buf = torch.full((M * N + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
         out = buf[2048:2048 + M * N].view(M, N)
@@ -209,7 +215,7 @@ def test_linear_writes_only_y(q):
 def test_linear_odd_output_address(q):
     """y at 2-byte alignment (one element into a buffer), whole and ragged N."""
     import torch
-    for M, N, K in ((3, 64, 96), (300, 256, 128)):
+    for M, N, K in ((3, 64, 96), (300, 256, 128), (900, 800, 128), (1500, 1600, 128), (2900, 3000, 128)):
         say("mx linear odd y", M, N, K)
         ac, as_ = _codes(M, K, "fp8", 1)
         wc, ws = _codes(N, K, "fp4", 2)
@@ -219,6 +225,35 @@ def test_linear_odd_output_address(q):
         y = q.mx_linear(*args, out=buf[1:].view(M, N))
         torch.testing.assert_close(y, q.mx_linear(*args), rtol=0, atol=0)
         assert float(buf[0]) == 0.0
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_offsets_beyond_32_bits(q, fmt):
+    """The last rows of arrays of more than 2^32 elements are the rows alone."""
+    import torch
+    rows, d = 262200, 16384
+    say("mx far offsets", rows, d, fmt)
+    x = torch.empty((rows, d), dtype=torch.bfloat16, device="cuda")
+    x[:64].normal_()
+    x[-64:].normal_()
+    x[64:-64].zero_()
+    codes, scales = q.mx_quantize(x, fmt)
+    for part in (slice(0, 64), slice(rows - 64, rows)):
+        c, s = q.mx_quantize(x[part].contiguous(), fmt)
+        assert torch.equal(codes[part], c) and torch.equal(scales[part], s)
+    back = q.mx_dequantize(codes, scales, fmt, out=x)
+    c, s = codes[-64:].contiguous(), scales[-64:].contiguous()
+    assert torch.equal(back[-64:], q.mx_dequantize(c, s, fmt))
+    w = q.mx_quantize(torch.randn((40, d), device="cuda"), "fp4")
+    y = q.mx_linear(codes, scales, fmt, *w, "fp4")
+    torch.testing.assert_close(y[-64:], q.mx_linear(c, s, fmt, *w, "fp4"), rtol=2.0 ** -7, atol=0.05)
+    assert bool((y[64:-64] == 0).all())
+    # y itself beyond 2^32 elements
+    del x, back, codes, y
+    a, b = (q.mx_quantize(torch.randn((n, 32), device="cuda"), fmt) for n in (140000, 32000))
+    y = q.mx_linear(*a, fmt, *b, fmt)
+    tail = tuple(t[-300:].contiguous() for t in a)
+    torch.testing.assert_close(y[-300:], q.mx_linear(*tail, fmt, *b, fmt), rtol=2.0 ** -7, atol=1e-3)
 
 
 def test_empty(q):

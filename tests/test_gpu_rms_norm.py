@@ -223,6 +223,19 @@ def test_rows_do_not_depend_on_the_batch(q):
             assert torch.equal(h1[0], h[k]) and torch.equal(y1[0], y[k])
 
 
+def test_offsets_beyond_32_bits(q):
+    import torch
+    rows, d = 262200, 16384
+    say("rms norm far offsets", rows, d)
+    x = torch.zeros((rows, d), dtype=torch.bfloat16, device="cuda")
+    x[-5:].normal_()
+    want = q.add_rms_norm(x[-5:].clone(), x[-5:].clone(), fmt="fp4")
+    h, codes, scales = q.add_rms_norm(x, x, sum_out=x, fmt="fp4")
+    assert h is x and torch.equal(h[-5:], want[0])
+    assert torch.equal(codes[-5:], want[1]) and torch.equal(scales[-5:], want[2])
+    assert bool((codes[:-5] == 0).all())
+
+
 def test_empty(q):
     import torch
     h, y = q.add_rms_norm(torch.zeros((0, 64), device="cuda"))

@@ -143,6 +143,27 @@ def test_inverse_is_the_gradient(q, half):
     assert float((back - x.double()).abs().max()) <= 2 * 2.0 ** -21 * 2 * float(x.abs().max()) * 1.5
 
 
+@pytest.mark.parametrize("half", [False, True])
+def test_offsets_beyond_32_bits_and_unused_strides(q, half):
+    """Three tokens 2^31 elements apart, and single tokens or heads whose
+    strides are no multiple of 16 bytes."""
+    import torch
+    say("rope far offsets", half)
+    x = torch.randn((3, 2, 64), device="cuda").bfloat16()
+    pos = torch.tensor([[3], [70000], [-9]], dtype=torch.int32, device="cuda")
+    want = q.rope(x, pos, [48], half=half)
+    buf = torch.empty((2 * 2 ** 31 + 128,), dtype=torch.bfloat16, device="cuda")
+    far = buf.as_strided((3, 2, 64), (2 ** 31, 64, 1))
+    far.copy_(x)
+    assert torch.equal(q.rope(far, pos, [48], half=half), want)
+    q.rope(far, pos, [48], half=half, out=far)
+    assert torch.equal(far, want)
+    one = x[:1].as_strided((1, 2, 64), (7, 64, 1))
+    assert torch.equal(q.rope(one, pos[:1], [48], half=half), want[:1])
+    head = x[:, :1].as_strided((3, 1, 64), (128, 3, 1))
+    assert torch.equal(q.rope(head, pos, [48], half=half), want[:, :1])
+
+
 def test_empty(q):
     import torch
     x = torch.zeros((0, 4, 64), device="cuda")

@@ -55,7 +55,7 @@ def test_norm():
               pdt=1, per=2, stride=384, sum=E, fmt=0, y=E + 0x1000, ys=None, stream=None)
     call = _caller("oq_add_rms_norm", ok)
     nan, inf = float("nan"), float("inf")
-    for kw in (dict(x=None), dict(y=None), dict(dt=7), dict(pdt=7), dict(eps=0.0), dict(eps=-1.0),
+    for kw in (dict(x=None), dict(y=None), dict(dt=7), dict(pdt=7), dict(eps=0.0), dict(eps=-1.0), dict(eps=1e-40),
                dict(eps=nan), dict(eps=inf), dict(rows=-1), dict(d=0), dict(per=0), dict(stride=-8),
                dict(stride=32), dict(stride=388), dict(fmt=5), dict(fmt=8), dict(ys=E + 0x2000),
                dict(x=A + 8), dict(res=B + 2), dict(w=C + 4), dict(gate=D + 2), dict(sum=E + 8),
