@@ -26,6 +26,10 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+// output pieces at any row length and address of y: the memory takes them at
+// two-byte alignment
+typedef uint32_t u32x4_y __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_y __attribute__((ext_vector_type(2), aligned(2)));
 
 constexpr int kGroupM = 4;  // tile rows per group of the tile order
 
@@ -97,7 +101,7 @@ struct Frag {
 template <int FA, int FW, class TL>
 __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_tile_kernel(
     const uint8_t *__restrict__ A, const uint8_t *__restrict__ As, const uint8_t *__restrict__ W,
-    const uint8_t *__restrict__ Ws, int M, int N, int K, uint16_t *__restrict__ Y, int vec) {
+    const uint8_t *__restrict__ Ws, int M, int N, int K, uint16_t *__restrict__ Y) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   constexpr int IB = TL::IB, JB = TL::JB, RA = TL::RA, RW = TL::RW;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -361,8 +365,8 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
           const u32x4 o = *(const u32x4 *)(reg + rr * (64 * JB) + ((c ^ (rr & (PPR - 1))) << 4));
           uint16_t *yp = Y + (int64_t)(m1 + rr) * N + n;
           if (m1 + rr >= M || n >= N) continue;
-          if (vec) {
-            __builtin_nontemporal_store(o, (u32x4 *)yp);
+          if (n + 8 <= N) {
+            __builtin_nontemporal_store(o, (u32x4_y *)yp);
           } else {
 #pragma unroll 1
             for (int e = 0; e < 8; e++) {
@@ -385,7 +389,7 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
 template <int FA, int FW, int MB, int NB>
 __global__ __launch_bounds__(512) void mx_rows_kernel(
     const uint8_t *__restrict__ A, const uint8_t *__restrict__ As, const uint8_t *__restrict__ W,
-    const uint8_t *__restrict__ Ws, int M, int N, int K, uint16_t *__restrict__ Y, int vec) {
+    const uint8_t *__restrict__ Ws, int M, int N, int K, uint16_t *__restrict__ Y) {
   constexpr int WAVES = 8;
   __shared__ f32x4 part[WAVES][MB * NB][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -474,9 +478,9 @@ __global__ __launch_bounds__(512) void mx_rows_kernel(
     const int m = m0 + 16 * (blk % MB) + r, n = n0 + 16 * (blk / MB) + 4 * g;  // four columns of a row
     if (m >= M) continue;
     uint16_t *yp = Y + (int64_t)m * N + n;
-    if (vec && n + 3 < N) {
+    if (n + 4 <= N) {
       const bf16x2 p0 = {(__bf16)y[0], (__bf16)y[1]}, p1 = {(__bf16)y[2], (__bf16)y[3]};
-      *(u32x2 *)yp = u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
+      *(u32x2_y *)yp = u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
     } else {
 #pragma unroll
       for (int e = 0; e < 4; e++)
@@ -487,12 +491,11 @@ __global__ __launch_bounds__(512) void mx_rows_kernel(
 
 template <int FA, int FW, int MB, int NB>
 hipError_t launch_rows(const MxLinearArgs &a) {
-  const int vec = a.N % 4 == 0 && ((uintptr_t)a.y & 7) == 0;
   const int64_t gx = (a.N + 16 * NB - 1) / (16 * NB), gy = (a.M + 16 * MB - 1) / (16 * MB);
   if (gx > (1 << 22) || gy > 65535) return hipErrorInvalidValue;
   hipLaunchKernelGGL((mx_rows_kernel<FA, FW, MB, NB>), dim3((unsigned)gx, (unsigned)gy), dim3(512), 0,
                      a.stream, a.a_codes, a.a_scales, a.w_codes, a.w_scales, (int)a.M, (int)a.N,
-                     a.K, a.y, vec);
+                     a.K, a.y);
   return hipGetLastError();
 }
 
@@ -504,10 +507,9 @@ hipError_t launch_tiles(const MxLinearArgs &a, int cus) {
   const int64_t tiles = ((a.M + TL::TM - 1) / TL::TM) * ((a.N + TL::TN - 1) / TL::TN);
   if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
   const int64_t slots = (int64_t)cus * TL::WGS;
-  const int vec = a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
   hipLaunchKernelGGL((mx_tile_kernel<FA, FW, TL>), dim3((unsigned)(tiles < slots ? tiles : slots)),
                      dim3(TL::THREADS), TL::LDS, a.stream, a.a_codes, a.a_scales, a.w_codes, a.w_scales,
-                     (int)a.M, (int)a.N, a.K, a.y, vec);
+                     (int)a.M, (int)a.N, a.K, a.y);
   return hipGetLastError();
 }
 
