@@ -521,9 +521,12 @@ hipError_t launch_tiles(const MxLinearArgs &a, int cus) {
 //     against 6.8; 64 x 1024 at K = 16384: 34 against 28.7)
 //   64 tiles as long as all of them are resident, two a CU with three stages
 //     each (128 x 5120: 13.1, 128 tiles 16.9; 256 x 13824, three a CU: 38, 30)
-//   128 tiles likewise, two a CU (1024 x 5120: 24, 256 tiles 34; 509 x 13824:
-//     26, 34)
-//   256 tiles beyond (2048 x 5120: 36, 128 tiles in two rounds 44)
+//   128 tiles, two a CU, or 256 tiles, one a CU: whichever needs less time for
+//     its rounds over the CUs, a round of 128 tiles taken as 0.6 of one of 256
+//     tiles (measured 0.54 at K = 512, 0.64 at K = 5120).  128 tiles: 509 x
+//     13824: 26, 256 tiles 34; 6000 x 6000 at K = 3200, 5 against 3 rounds:
+//     118, 125.  256 tiles: 2048 x 5120: 36, 128 tiles 44; 32768 x 4096 at K =
+//     2048: 155, 187
 template <int FA, int FW>
 hipError_t launch_pair(const MxLinearArgs &a, int cus) {
   // a stage: 128 bytes of a row (64 of 4-bit weights against 8-bit
@@ -540,7 +543,9 @@ hipError_t launch_pair(const MxLinearArgs &a, int cus) {
     return wide ? launch_rows<FA, FW, 4, 2>(a) : launch_rows<FA, FW, 4, 1>(a);
   }
   if (small <= 2 * cus) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 1, 1, 2, KS, 3>>(a, cus);
-  if (tiles(128) <= 2 * cus) return launch_tiles<FA, FW, MxTile<FA, FW, 2, 2, 2, 2, KS, 2>>(a, cus);
+  auto rounds = [](int64_t t, int64_t slots) { return (t + slots - 1) / slots; };
+  if (3 * rounds(tiles(128), 2 * cus) <= 5 * rounds(tiles(256), cus))
+    return launch_tiles<FA, FW, MxTile<FA, FW, 2, 2, 2, 2, KS, 2>>(a, cus);
   // three stages where they fit: 1.68 against 1.70 ms at 32760 x 5120 x 13824
   constexpr int NST = (FA || FW) && !(FA && FW) ? 3 : 2;
   return launch_tiles<FA, FW, MxTile<FA, FW, 4, 4, 2, 1, KS, NST>>(a, cus);
