@@ -12,7 +12,27 @@
 // Either way the lane's scale byte is that of block g.  Any assignment of
 // the row's blocks to (instruction, g) will do that both operands share.
 // (16x16x128: r = lane % 16, four groups g; 4-bit block g; 8-bit bytes 16 g of
-// each 64-element half; scale of block g.)
+// each 64-element half; scale of block g.)  The 32 x 32 form does the same
+// work with half of the operand reads: 8.1 against 6.5 PFLOP/s for 4-bit
+// elements, registers only.
+//
+// Two kernels.  Many rows: 64, 128 or 256 square tiles.  Codes go from memory
+// straight to LDS, in stages of 128 bytes of a row (whole lines of the L2),
+// several stages in a ring; the waves read fragments one step ahead of the
+// products.  Few rows: no tile has enough of them to share, the weights are
+// streamed once, K split over the waves of a workgroup.
+//
+// Measured (one MI355X): 32760 x 15360 x 5120, e2m1 both: 1.24-1.30 ms, 4.0-4.2
+// PFLOP/s; 32760 x 5120 x 13824, e4m3 x e2m1: 1.68 ms, 2.75 PFLOP/s; e4m3 both:
+// 1.82 ms, 2.55 PFLOP/s.  The matrix instructions alone, on random registers,
+// keep 6.6, 4.3 and 3.9 PFLOP/s on this card: power, not issue, is what bounds
+// them (about 1.8 GHz under this load; the matrix cores are busy 57% of the
+// time), and the requests for the next stage, drained at each barrier, take
+// most of the rest (without them 1.04 ms).  At the first of those sizes four
+// waves of 128 x 128 took 1.26 ms, stages of 128 elements (64-byte pieces) with
+// four of them in LDS 1.38, 256 x 128 tiles with three stages 1.51, 128 tiles
+// 1.63.  2 x 30720 x 5120: 16.4 us, 5.1 TB/s of weights, the rate of a large
+// copy.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -31,7 +51,10 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4_y __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_y __attribute__((ext_vector_type(2), aligned(2)));
 
-constexpr int kGroupM = 4;  // tile rows per group of the tile order
+// Tile rows per group of the tile order: an XCD's resident tiles share 4 row
+// blocks and 8 column blocks, and the 4 row blocks stay in its L2 while the
+// columns pass (8 rows: 2% slower; 16: 7% to 17%).
+constexpr int kGroupM = 4;
 
 // A workgroup of 2 x WN waves computes a (64 IB) x (32 WN JB) tile; each wave
 // a (32 IB) x (32 JB) block of it.
@@ -117,7 +140,8 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
   constexpr int CA = RA / 16, CW = RW / 16;
   constexpr int PA = TL::TM * CA, PW = TL::TN * CW;  // pieces
   constexpr int LA = PA / TH, LW = PW / TH, NL = LA + LW;
-  // pieces requested in the last step of a stage, the others in the first of the next
+  // pieces requested in the last step of a stage, the others in the first of the
+  // next (all of them in one burst: 3% slower)
   constexpr int LL = TL::STEPS == 4 ? NL / 2 : NL;
   constexpr int NST = TL::NST;
   static_assert(PA % TH == 0 && PW % TH == 0, "whole rounds of requests");
@@ -175,7 +199,8 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
     const int m0 = x.m0, n0 = x.n0;
 
     // Scales: 32 blocks of a row are loaded at once (one request to the L2 for
-    // most; their address has no alignment), 16 a time go to LDS.  A last, partial group of 16 goes byte by byte, zero past K.
+    // most; their address has no alignment), 16 a time go to LDS.  A last,
+    // partial group of 16 goes byte by byte, zero past K.
     constexpr int LS = (TL::SROWS + TH - 1) / TH;
     u32x4 sts[LS][2];
     auto group_rows = [&](const Tile &x, auto f) {
@@ -287,7 +312,7 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
     // read.  Before the last step a barrier sees stage t + 1 arrived and this
     // stage's LDS buffer read for the last time; in the last step the first
     // fragments and the scales of stage t + 1 are read, and from there to the
-    // end of its first step stage t + 2 is requested into this stage's buffer.
+    // end of its first step stage t + NST is requested into this stage's buffer.
     // Each memory operation is pinned behind a product, evenly, so that the
     // matrix cores always have the next one.
     constexpr int NM = IB * JB;

@@ -14,6 +14,11 @@
 // workgroup one row or a few short ones: workgroups that walk the rows with
 // their parameters held in registers and the next row prefetched were 10%
 // slower (32760 x 5120: 280 against 255 us), the parameters come from the L2.
+// Stores are non-temporal (30000 x 512: 24 against 20 us).
+//
+// Measured: 32760 x 5120 bf16 228 us (5.9 TB/s; a large copy 5.3), with gate
+// and modulation 246 us (5.4), into e4m3 242 us (4.9); fp32 4111 x 1536 23 us
+// (4.3).  One row of 5120: 4.9 us, one wait for memory after another.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
