@@ -43,7 +43,6 @@
 namespace oq {
 namespace {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 // output pieces at any row length and address of y: the memory takes them at

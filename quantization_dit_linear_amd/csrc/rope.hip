@@ -14,7 +14,7 @@
 // streams the heads.  Measured: 32760 tokens x 80 heads x 128 bf16, strided
 // input, 255 us (5.2 TB/s; each thread computing its own: 443 us); 24 heads of
 // 64: 35 us (5.7 TB/s); two heads of 128: 19 us (3.2 TB/s, the table's
-// arithmetic); one token 3.4 us.
+// arithmetic); one token 3.8 us.
 #include <hip/hip_runtime.h>
 
 #include "mx_codec.h"
@@ -62,74 +62,74 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int tok_group, in
 
   for (int64_t t0 = (int64_t)blockIdx.x * tok_group; t0 < a.tokens;
        t0 += (int64_t)gridDim.x * tok_group) {
-  const int nt = a.tokens - t0 < tok_group ? (int)(a.tokens - t0) : tok_group;
-  __syncthreads();  // the table of the group before is read
-  for (int i = tid; i < nt * half; i += 256) {
-    const int t = i / half, j = i - t * half;
-    const uint64_t f = (uint64_t)(int64_t)a.pos[(t0 + t) * a.axes + a.axis[j]] * a.freq[j];
-    f32x2 z = cos_sin((uint32_t)((f + 0x80000000ull) >> 32));
-    if (a.inverse) z[1] = -z[1];
-    table[i] = z;
-  }
-  __syncthreads();
-
-  int c = tid % per, h = tid / per, t = h / nh;
-  h -= t * nh;
-  const T *xb = (const T *)a.x + t0 * a.x_token + (int64_t)h0 * a.x_head;
-  T *yb = (T *)a.y + t0 * a.y_token + (int64_t)h0 * a.y_head;
-  auto next = [&] {
-    c += dc, h += dh, t += dt;
-    if (c >= per) c -= per, h++;
-    if (h >= nh) h -= nh, t++;
-  };
-  // four items at a time, all loads first
-  constexpr int U = 4;
-  while (t < nt) {
-    float u[U][E], v[U][E];
-    int it[U], ic[U];
-    const T *px[U];
-    T *py[U];
-#pragma unroll
-    for (int k = 0; k < U; k++) {
-      it[k] = t, ic[k] = c;
-      const int at = !HALF || c < turned_items ? E * c : a.turned + E * (c - turned_items);
-      px[k] = xb + t * a.x_token + (int64_t)h * a.x_head + at;
-      py[k] = yb + t * a.y_token + (int64_t)h * a.y_head + at;
-      if (t < nt) {
-        load16(px[k], u[k]);
-        if (HALF && c < turned_items) load16(px[k] + half, v[k]);
-      }
-      next();
+    const int nt = a.tokens - t0 < tok_group ? (int)(a.tokens - t0) : tok_group;
+    __syncthreads();  // the table of the group before is read
+    for (int i = tid; i < nt * half; i += 256) {
+      const int t = i / half, j = i - t * half;
+      const uint64_t f = (uint64_t)(int64_t)a.pos[(t0 + t) * a.axes + a.axis[j]] * a.freq[j];
+      f32x2 z = cos_sin((uint32_t)((f + 0x80000000ull) >> 32));
+      if (a.inverse) z[1] = -z[1];
+      table[i] = z;
     }
+    __syncthreads();
+
+    int c = tid % per, h = tid / per, t = h / nh;
+    h -= t * nh;
+    const T *xb = (const T *)a.x + t0 * a.x_token + (int64_t)h0 * a.x_head;
+    T *yb = (T *)a.y + t0 * a.y_token + (int64_t)h0 * a.y_head;
+    auto next = [&] {
+      c += dc, h += dh, t += dt;
+      if (c >= per) c -= per, h++;
+      if (h >= nh) h -= nh, t++;
+    };
+    // four items at a time, all loads first
+    constexpr int U = 4;
+    while (t < nt) {
+      float u[U][E], v[U][E];
+      int it[U], ic[U];
+      const T *px[U];
+      T *py[U];
 #pragma unroll
-    for (int k = 0; k < U; k++) {
-      if (it[k] >= nt) break;
-      if (ic[k] < turned_items) {
-        const f32x2 *z = table + it[k] * half + (HALF ? E : E / 2) * ic[k];
-        if constexpr (HALF) {
+      for (int k = 0; k < U; k++) {
+        it[k] = t, ic[k] = c;
+        const int at = !HALF || c < turned_items ? E * c : a.turned + E * (c - turned_items);
+        px[k] = xb + t * a.x_token + (int64_t)h * a.x_head + at;
+        py[k] = yb + t * a.y_token + (int64_t)h * a.y_head + at;
+        if (t < nt) {
+          load16(px[k], u[k]);
+          if (HALF && c < turned_items) load16(px[k] + half, v[k]);
+        }
+        next();
+      }
 #pragma unroll
-          for (int e = 0; e < E; e++) {
-            const float p = u[k][e] * z[e][0] - v[k][e] * z[e][1];
-            v[k][e] = u[k][e] * z[e][1] + v[k][e] * z[e][0];
-            u[k][e] = p;
-          }
-          store16_nt(py[k] + half, v[k]);
-        } else {
-          // the last item may hold elements behind the turned ones
-          const int left = half - E / 2 * ic[k];
+      for (int k = 0; k < U; k++) {
+        if (it[k] >= nt) break;
+        if (ic[k] < turned_items) {
+          const f32x2 *z = table + it[k] * half + (HALF ? E : E / 2) * ic[k];
+          if constexpr (HALF) {
 #pragma unroll
-          for (int e = 0; e < E / 2; e++) {
-            const f32x2 w = e < left ? z[e] : f32x2{1.f, 0.f};
-            const float p = u[k][2 * e] * w[0] - u[k][2 * e + 1] * w[1];
-            const float q = u[k][2 * e] * w[1] + u[k][2 * e + 1] * w[0];
-            u[k][2 * e] = e < left ? p : u[k][2 * e];
-            u[k][2 * e + 1] = e < left ? q : u[k][2 * e + 1];
+            for (int e = 0; e < E; e++) {
+              const float p = u[k][e] * z[e][0] - v[k][e] * z[e][1];
+              v[k][e] = u[k][e] * z[e][1] + v[k][e] * z[e][0];
+              u[k][e] = p;
+            }
+            store16_nt(py[k] + half, v[k]);
+          } else {
+            // the last item may hold elements behind the turned ones
+            const int left = half - E / 2 * ic[k];
+#pragma unroll
+            for (int e = 0; e < E / 2; e++) {
+              const f32x2 w = e < left ? z[e] : f32x2{1.f, 0.f};
+              const float p = u[k][2 * e] * w[0] - u[k][2 * e + 1] * w[1];
+              const float q = u[k][2 * e] * w[1] + u[k][2 * e + 1] * w[0];
+              u[k][2 * e] = e < left ? p : u[k][2 * e];
+              u[k][2 * e + 1] = e < left ? q : u[k][2 * e + 1];
+            }
           }
         }
+        store16_nt(py[k], u[k]);
       }
-      store16_nt(py[k], u[k]);
     }
-  }
   }
 }
 
