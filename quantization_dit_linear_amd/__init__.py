@@ -520,7 +520,7 @@ def add_rms_norm(x, residual=None, *, weight=None, gate=None, scale=None, shift=
         first = p if first is None else first
         if p.shape[-1:] != (d,) or p.dtype != first.dtype:
             raise ValueError(f"{n} must have {d} columns and the other parameters' dtype")
-        if p is weight:
+        if n == "weight":  # by name: one tensor may be passed as several parameters
             if p.dim() != 1:
                 raise ValueError("weight must be [d]")
             continue

@@ -125,3 +125,13 @@ def test_binding_rejects_mismatched_buffers():
             call()
     with pytest.raises(TypeError, match="codes"):
         q.mx_dequantize([1], u8(1, 1), "fp8")
+
+
+def test_one_tensor_as_weight_and_modulation():
+    """The same tensor as weight and as gate, scale or shift is both: its one
+    group has to cover the rows like any other's."""
+    w = torch.zeros(64, dtype=torch.bfloat16)
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    for name in ("gate", "scale", "shift"):
+        with pytest.raises(ValueError, match="groups"):
+            q.add_rms_norm(x, weight=w, rows_per_mod=1, **{name: w})
