@@ -136,7 +136,9 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, 2) void rms_norm_kernel(RmsN
       for (int k = 0; k < 8; k++) ss = fmaf(h[i][k], h[i][k], ss);
     }
 
-    // the row's total; `other`: any row's of the workgroup that is not finite
+    // the mean of squares and eps; of a row at 2^-64, with eps brought there too
+    auto mean = [&](float sum, float unit) { return fmaf(sum, inv_d, a.eps * unit); };
+    // the row's total; `other`: any row of the workgroup whose mean is not finite
     auto total = [&](float v, bool &other) {
       v = wave_sum(v);
       if constexpr (WPR > 1) {
@@ -151,22 +153,23 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, 2) void rms_norm_kernel(RmsN
           float u = all[s * WPR];
 #pragma unroll
           for (int w = 1; w < WPR; w++) u += all[s * WPR + w];
-          other |= !(u < __builtin_huge_valf());
+          other |= !(mean(u, 1.f) < __builtin_huge_valf());
           if (s == slot) t = u;
         }
         par ^= 1;
         return t;
       } else {
-        other = !(v < __builtin_huge_valf());
+        other = !(mean(v, 1.f) < __builtin_huge_valf());
         return v;
       }
     };
     bool redo;
     ss = total(ss, redo);
-    float rs = rsqrtf(ss * inv_d + a.eps);
+    const float ms = mean(ss, 1.f);
+    float rs = rsqrtf(ms);
     if (redo) {
-      // a sum of squares overflowed: once more at 2^-64 (a row with a NaN or an
-      // infinity stays one); eps is nothing beside it
+      // a mean overflowed: once more at 2^-64 (a row with a NaN or an infinity
+      // stays one)
       float s2 = 0.f;
 #pragma unroll
       for (int i = 0; i < NCH; i++)
@@ -176,7 +179,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, 2) void rms_norm_kernel(RmsN
           s2 = fmaf(t, t, s2);
         }
       s2 = total(s2, redo);
-      if (!(ss < __builtin_huge_valf())) rs = rsqrtf(s2 * inv_d) * 0x1p-64f;
+      if (!(ms < __builtin_huge_valf())) rs = rsqrtf(mean(s2, 0x1p-128f)) * 0x1p-64f;
     }
     if (!in) continue;
 #pragma unroll

@@ -212,6 +212,22 @@ def test_zero_huge_and_non_finite_rows(q, d):
         assert torch.equal(codes[k], c2[k]) and torch.equal(scales[k], s2[k])
 
 
+@pytest.mark.parametrize("eps", [1e30, 3e38])
+@pytest.mark.parametrize("d", [128, 2048, 5120, 16384])
+def test_the_largest_eps(q, d, eps):
+    """Rows whose sum of squares, or whose mean with eps, passes fp32's range,
+    beside ordinary ones: eps counts in each.  40 roundings as above."""
+    say("rms norm eps", d, eps)
+    r = np.random.default_rng([d, 12])
+    x = (r.standard_normal((6, d)) * np.array([1.0, 1e15, 1e18, 4e18, 2e19, 1e25])[:, None]).astype(np.float32)
+    x[4] = 1.8e19  # its sum of squares overflows, its mean is 3.2e38
+    e = float(np.float32(eps))
+    _, y = q.add_rms_norm(_dev(x, False), eps=eps)
+    v = x.astype(np.float64)
+    want = v / np.sqrt((v * v).mean(1, keepdims=True) + e)
+    assert np.all(np.abs(_np(y) - want) <= 40 * U * np.abs(want))
+
+
 def test_rows_do_not_depend_on_the_batch(q):
     """Row r alone gives the bits that it has in a batch."""
     import torch
