@@ -146,12 +146,13 @@ hipError_t launch_rope(const RopeArgs &a) {
   if (group > most) group = most;
   if (group < 1 || a.tokens < 1024 * (int64_t)group) group = 1;
   const int64_t gx = (a.tokens + group - 1) / group;
-  int hs = a.heads;
-  while (gx * ((a.heads + hs - 1) / hs) < 1024 && hs * per > 256) hs = (hs + 1) / 2;
-  const dim3 grid((unsigned)(gx < (1 << 20) ? gx : 1 << 20), (unsigned)((a.heads + hs - 1) / hs)), block(256);
+  int64_t hs = a.heads;
+  auto slices = [&] { return (a.heads + hs - 1) / hs; };
+  while (gx * slices() < 1024 && hs * per > 256) hs = (hs + 1) / 2;
+  const dim3 grid((unsigned)(gx < (1 << 20) ? gx : 1 << 20), (unsigned)slices()), block(256);
 #define OQ_CASE(DT, T, H)        \
   if (a.dtype == DT && a.half == H) \
-    hipLaunchKernelGGL((rope_kernel<T, H>), grid, block, 0, a.stream, a, group, hs);
+    hipLaunchKernelGGL((rope_kernel<T, H>), grid, block, 0, a.stream, a, group, (int)hs);
   OQ_CASE(0, float, false) OQ_CASE(0, float, true)
   OQ_CASE(1, uint16_t, false) OQ_CASE(1, uint16_t, true)
 #undef OQ_CASE
