@@ -173,6 +173,29 @@ def test_linear_is_exact_on_small_integers(q, M, N, K, fa):
     np.testing.assert_array_equal(y, a @ w.T)
 
 
+@pytest.mark.parametrize("fa,fw", [("fp4", "fp4"), ("fp8", "fp4"), ("fp4", "fp8"), ("fp8", "fp8")])
+@pytest.mark.parametrize("M,N", [(5, 70), (70, 90), (600, 520), (3000, 3100)])
+def test_linear_over_the_range_of_the_scales(q, M, N, fa, fw):
+    """Scale bytes from 0 to 254 against each other.  One element a block, one
+    block a row holds a value, so an output is one product 2^(sa + sw - 254):
+    exact where fp32 holds it as a normal number, infinite from 2^128 on, at
+    most 2^-126 below the normal ones (the sum may flush them)."""
+    say("mx linear scales", M, N, fa, fw)
+    r = np.random.default_rng([M, 6])
+    K, one = 96, {"fp4": 2, "fp8": 0x38}
+    sa, sw = (r.choice([0, 1, 2, 60, 126, 127, 128, 190, 253, 254], (n, 3)).astype(np.uint8) for n in (M, N))
+    ac, wc = np.zeros((M, K), np.uint8), np.zeros((N, K), np.uint8)
+    ac[:, 37], wc[:, 37] = one[fa], one[fw]
+    y = bf16_to_np(q.mx_linear(to_device(ref.pack(ac, fa)), to_device(sa), fa,
+                               to_device(ref.pack(wc, fw)), to_device(sw), fw))
+    e = sa[:, 1].astype(int)[:, None] + sw[:, 1].astype(int)[None] - 254
+    want = np.ldexp(1.0, e)
+    normal = (e >= -126) & (e <= 127)
+    np.testing.assert_array_equal(y[normal], want[normal])
+    assert np.all(y[e >= 128] == np.inf)
+    assert np.all(np.abs(y[e < -126]) <= 2.0 ** -126)
+
+
 @pytest.mark.parametrize("fa,fw", [("fp4", "fp4"), ("fp8", "fp4"), ("fp8", "fp8")])
 @pytest.mark.parametrize("M,N,K", [(5, 70, 160), (70, 90, 288), (520, 513, 160), (900, 800, 1184),
                                    (1500, 1600, 160), (2900, 3000, 544)])
