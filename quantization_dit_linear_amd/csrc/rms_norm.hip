@@ -136,8 +136,8 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, 2) void rms_norm_kernel(RmsN
       for (int k = 0; k < 8; k++) ss = fmaf(h[i][k], h[i][k], ss);
     }
 
-    // the mean of squares and eps; of a row at 2^-64, with eps brought there too
-    auto mean = [&](float sum, float unit) { return fmaf(sum, inv_d, a.eps * unit); };
+    // the mean of squares and eps; of a row times `unit`, with eps brought there too
+    auto mean = [&](float sum, float unit) { return fmaf(sum, inv_d, a.eps * unit * unit); };
     // the row's total; `other`: any row of the workgroup whose mean is not finite
     auto total = [&](float v, bool &other) {
       v = wave_sum(v);
@@ -166,20 +166,23 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, 2) void rms_norm_kernel(RmsN
     bool redo;
     ss = total(ss, redo);
     const float ms = mean(ss, 1.f);
-    float rs = rsqrtf(ms);
+    float rs = rsqrtf(ms), back = 1.f;
     if (redo) {
-      // a mean overflowed: once more at 2^-64 (a row with a NaN or an infinity
-      // stays one)
+      // a mean overflowed: once more at 2^-72, where the squares of 16384
+      // values below 2^128 sum to 2^126 at most, and those of a row whose sum
+      // passed 2^128 to 2^-16 at least.  The factor's 2^-72 is applied behind
+      // the product, exactly: 1 / rms itself may be subnormal.  (A row with a
+      // NaN or an infinity stays one.)
       float s2 = 0.f;
 #pragma unroll
       for (int i = 0; i < NCH; i++)
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-          const float t = h[i][k] * 0x1p-64f;
+          const float t = h[i][k] * 0x1p-72f;
           s2 = fmaf(t, t, s2);
         }
       s2 = total(s2, redo);
-      if (!(ms < __builtin_huge_valf())) rs = rsqrtf(mean(s2, 0x1p-128f)) * 0x1p-64f;
+      if (!(ms < __builtin_huge_valf())) rs = rsqrtf(mean(s2, 0x1p-72f)), back = 0x1p-72f;
     }
     if (!in) continue;
 #pragma unroll
@@ -191,7 +194,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256, 2) void rms_norm_kernel(RmsN
       if constexpr (!EARLY) load_rest(true, c, mod, pw[i], ps[i], pb[i]);
       pw[i].get(w);
 #pragma unroll
-      for (int k = 0; k < 8; k++) y[k] = h[i][k] * rs;
+      for (int k = 0; k < 8; k++) y[k] = h[i][k] * rs * back;
       if constexpr (MOD) {
         float s[8], b[8];
         ps[i].get(s), pb[i].get(b);

@@ -228,6 +228,41 @@ def test_the_largest_eps(q, d, eps):
     assert np.all(np.abs(_np(y) - want) <= 40 * U * np.abs(want))
 
 
+@pytest.mark.parametrize("mod", [False, True])
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("d", [32, 128, 2048, 5120, 8192, 16384])
+def test_rows_of_the_largest_values(q, d, bf16, mod):
+    """Finite rows up to the type's largest value, whose norm passes 2^128,
+    beside ordinary ones: the formula's values, also in codes.  The tolerance
+    above, and where y is subnormal half of the type's smallest step (the
+    normalised value's 2^-150 times at most 8 of weight and scale)."""
+    say("rms norm largest", d, bf16, mod)
+    top = 3.3895313892515355e38 if bf16 else 3.4028234663852886e38
+    c = _inputs(9, d, d, bf16, bf16, mod, mod, mod, mod, 3)
+    r = np.random.default_rng([d, 15])
+    sign = r.choice([-1.0, 1.0], (9, d))
+    x = c["x"].astype(np.float64)
+    x[1] = sign[1] * top
+    x[2] = sign[2] * r.uniform(3e36, 3e38, d)
+    x[3, d // 2] = top
+    x[4] = sign[4] * np.exp2(r.uniform(-100, 127, d))
+    x[6] = sign[6] * 2.0 ** 116
+    x[7] = sign[7] * 2.0 ** 121
+    np.clip(c["mod"], -0.875, 0.875, out=c["mod"])  # gate x stays finite (gate, scale and shift are views)
+    c["x"] = _round(x, bf16)
+    assert np.isfinite(c["x"]).all()
+    h, dh, y, dy = _want(c, 3, 1e-6)
+    _, got = _call(q, c, bf16, bf16, 3, 1e-6)
+    err = np.abs(_np(got) - y)
+    tol = dy + (2.0 ** -8 if bf16 else U) * (np.abs(y) + dy) + 2.0 ** -147 + (2.0 ** -134 if bf16 else 0.0)
+    assert np.all(err <= tol), (float(np.max(err / tol)), np.argwhere(err > tol)[:4])
+    if not bf16:
+        for fmt in ("fp8", "fp4"):
+            _, codes, scales = _call(q, c, bf16, bf16, 3, 1e-6, fmt)
+            want = q.mx_quantize(got, fmt)
+            assert bool((codes == want[0]).all()) and bool((scales == want[1]).all())
+
+
 def test_rows_do_not_depend_on_the_batch(q):
     """Row r alone gives the bits that it has in a batch."""
     import torch
