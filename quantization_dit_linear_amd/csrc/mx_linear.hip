@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "mx_codec.h"
+#include "mx_stage.h"
 #include "oq_internal.h"
 
 namespace oq {
@@ -76,21 +77,12 @@ struct MxTile {
   static_assert(LDS * WGS <= 160 * 1024, "LDS of one CU");
 };
 
-// XOR swizzle of a row's 16-byte pieces in LDS (rows lie one after another).
-// A 16-byte LDS read serves lanes {0-3, 12-15, 20-23, 24-27} of 32 together,
-// then the others: of those, rows equal modulo 256 bytes differ in these bits.
-template <int RB>
-__device__ __forceinline__ int swizzle(int row) {
-  return RB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
-}
-
 typedef __attribute__((address_space(3))) void lds_void;
 
 // 64 lanes x 16 bytes from memory straight to LDS, lane after lane from `dst`
 // (uniform); lanes outside the buffer write zeros.
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint8_t *dst, uint32_t off,
-                                            uint32_t base) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)dst, 16, off, base, 0, 0);
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint8_t *dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)dst, 16, off, 0, 0, 0);
 }
 
 template <int N>
@@ -134,18 +126,17 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
   const int nbm = (M + TL::TM - 1) / TL::TM, nbn = (N + TL::TN - 1) / TL::TN;
   const int count = nbm * nbn;
 
-  // Loads of a stage: piece idx = tid + TH k of an operand, CA / CW pieces a
-  // row; the thread of LDS slot s of a row brings the row's piece s ^ swizzle.
-  constexpr int CA = RA / 16, CW = RW / 16;
-  constexpr int PA = TL::TM * CA, PW = TL::TN * CW;  // pieces
+  // Loads of a stage: piece idx = tid + TH k of an operand
+  using PieceA = MxPieces<RA, TH>;
+  using PieceW = MxPieces<RW, TH>;
+  constexpr int PA = TL::TM * PieceA::C, PW = TL::TN * PieceW::C;  // pieces
   constexpr int LA = PA / TH, LW = PW / TH, NL = LA + LW;
   // pieces requested in the last step of a stage, the others in the first of the
   // next (all of them in one burst: 3% slower)
   constexpr int LL = TL::STEPS == 4 ? NL / 2 : NL;
   constexpr int NST = TL::NST;
   static_assert(PA % TH == 0 && PW % TH == 0, "whole rounds of requests");
-  const int ra0 = tid / CA, ca0 = (tid % CA) ^ swizzle<RA>(ra0);
-  const int rw0 = tid / CW, cw0 = (tid % CW) ^ swizzle<RW>(rw0);
+  const int ba0 = PieceA::byte(tid), bw0 = PieceW::byte(tid);
   const int uw = __builtin_amdgcn_readfirstlane(wave);
   const int la0 = uw * 1024, lw0 = TL::AB + uw * 1024;
   // Fragments.  Of a stage's 2 STEPS blocks, step j multiplies blocks j and
@@ -154,15 +145,15 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
   // 2 j + 4 h + g.  Pieces differ in the bits of j and h alone, which the
   // swizzle leaves exclusive-or apart.
   const int arow = wm * 32 * IB + r, wrow = wn * 32 * JB + r;
-  const int fa0 = arow * RA + (((FA ? g : TL::STEPS * g) ^ swizzle<RA>(r)) << 4);
-  const int fw0 = TL::AB + wrow * RW + (((FW ? g : TL::STEPS * g) ^ swizzle<RW>(r)) << 4);
+  const int fa0 = arow * RA + (((FA ? g : TL::STEPS * g) ^ mx_swizzle<RA>(r)) << 4);
+  const int fw0 = TL::AB + wrow * RW + (((FW ? g : TL::STEPS * g) ^ mx_swizzle<RW>(r)) << 4);
   // the lane's scale bytes of a stage: blocks STEPS g .. STEPS g + STEPS - 1
   const int sp = TL::STEPS == 4 ? g * TL::SROWS * 4 : 2 * g;
   const int sa0 = TL::SC0 + 4 * arow + sp, sw0 = TL::SC0 + 4 * (TL::TM + wrow) + sp;
 
   struct Tile {
     int m0, n0, mr, nr;  // origin, rows and columns inside the matrix
-    __amdgpu_buffer_rsrc_t a, w;
+    __amdgpu_buffer_rsrc_t a[LA], w[LW];  // of each round of requests
   };
   // each XCD takes a contiguous run of the tile order; rows past the last lie
   // outside the buffers
@@ -173,24 +164,26 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
     Tile x;
     x.m0 = tm * TL::TM, x.n0 = tn * TL::TN;
     x.mr = M - x.m0 < TL::TM ? M - x.m0 : TL::TM, x.nr = N - x.n0 < TL::TN ? N - x.n0 : TL::TN;
-    x.a = __builtin_amdgcn_make_buffer_rsrc((void *)(A + (int64_t)x.m0 * rowA), 0, x.mr * rowA, 0x00027000);
-    x.w = __builtin_amdgcn_make_buffer_rsrc((void *)(W + (int64_t)x.n0 * rowW), 0, x.nr * rowW, 0x00027000);
+#pragma unroll
+    for (int k = 0; k < LA; k++)
+      x.a[k] = __builtin_amdgcn_make_buffer_rsrc(
+          (void *)(A + (int64_t)x.m0 * rowA + PieceA::base(rowA, k)), 0, PieceA::size(x.mr, rowA, k), 0x00027000);
+#pragma unroll
+    for (int k = 0; k < LW; k++)
+      x.w[k] = __builtin_amdgcn_make_buffer_rsrc(
+          (void *)(W + (int64_t)x.n0 * rowW + PieceW::base(rowW, k)), 0, PieceW::size(x.nr, rowW, k), 0x00027000);
     return x;
   };
   // piece k of stage t of a tile into LDS stage `buf`: activations first.
-  // Pieces past K and stages past the last are sent outside the buffers (the
-  // hardware's range check covers the uniform offset too).
-  const uint32_t offA = ra0 * rowA + ca0 * 16, offW = rw0 * rowW + cw0 * 16;
+  // Rows past the last, pieces past K and stages past the last lie outside the
+  // buffers.
+  const uint32_t offA = PieceA::row(tid) * rowA + ba0, offW = PieceW::row(tid) * rowW + bw0;
   auto load_piece = [&](const Tile &x, int t, int buf, int k) {
     uint8_t *b = lds + buf * TL::STAGE;
-    if (k < LA) {
-      const bool in = ca0 * 16 < rowA - t * RA;
-      load_to_lds(x.a, b + la0 + k * (16 * TH), in ? offA : 0x7ffffff0u, t * RA + k * (TH / CA) * rowA);
-    } else {
-      const bool in = cw0 * 16 < rowW - t * RW;
-      load_to_lds(x.w, b + lw0 + (k - LA) * (16 * TH), in ? offW : 0x7ffffff0u,
-                  t * RW + (k - LA) * (TH / CW) * rowW);
-    }
+    if (k < LA)
+      load_to_lds(x.a[k], b + la0 + k * (16 * TH), PieceA::offset(offA, ba0, rowA, t));
+    else
+      load_to_lds(x.w[k - LA], b + lw0 + (k - LA) * (16 * TH), PieceW::offset(offW, bw0, rowW, t));
   };
 
   for (int v = blockIdx.x; v < count; v += gridDim.x) {
