@@ -534,6 +534,8 @@ def add_rms_norm(x, residual=None, *, weight=None, gate=None, scale=None, shift=
         rows_per_mod = max(1, -(-rows // max(1, groups)))
     if mods and (rows_per_mod < 1 or -(-rows // rows_per_mod) > groups):
         raise ValueError(f"{rows} rows at {rows_per_mod} per group need more than {groups} groups")
+    if rows_per_mod > rows:  # one group: as a number that the C call's 64 bits hold
+        rows_per_mod = max(1, rows)
     if sum_out is not None and sum_out is not False:
         _shaped(sum_out, (rows, d), x.dtype, "sum_out")
     bits = 0

@@ -135,3 +135,32 @@ def test_one_tensor_as_weight_and_modulation():
     for name in ("gate", "scale", "shift"):
         with pytest.raises(ValueError, match="groups"):
             q.add_rms_norm(x, weight=w, rows_per_mod=1, **{name: w})
+
+
+class _Recorder:
+    """Stands for the library: keeps the arguments as the C side would see them."""
+
+    def __init__(self, monkeypatch):
+        self.args = []
+        monkeypatch.setattr(q, "lib", lambda: self)
+        monkeypatch.setattr(q, "_call_device", lambda *named: 0)
+        monkeypatch.setattr(q, "_raw_stream", lambda stream, dev: None)
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.args = [t(a).value for t, a in zip(q._SIGS[name][1], args)]
+            return q.OQ_OK
+        return call
+
+
+@pytest.mark.parametrize("per", [4, 5, 2 ** 31, 2 ** 63, 2 ** 64 + 1, 2 ** 65])
+def test_rows_per_mod_of_any_size(monkeypatch, per):
+    """One group covers every row, however large the number of rows it may
+    have: the library has to see no more than one (2^64 + 1 would arrive as 1,
+    and the rows behind the first would read past the group)."""
+    seen = _Recorder(monkeypatch)
+    p = torch.zeros((1, 64), dtype=torch.bfloat16)
+    q._torch()
+    q.add_rms_norm(torch.zeros((4, 64), dtype=torch.bfloat16), gate=p, rows_per_mod=per)
+    rows, rows_per_mod = seen.args[3], seen.args[11]
+    assert rows == 4 and rows_per_mod >= 4
