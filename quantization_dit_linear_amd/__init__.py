@@ -385,6 +385,12 @@ def _call_device(*named):
     return dev
 
 
+def _fits(size, what):
+    """Sizes that the C call takes as an int (ctypes would cut a larger one)."""
+    if size > 2147483647:
+        raise ValueError(f"{what} ({size}) must fit 32 bits")
+
+
 def _ptr(t, name):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -438,6 +444,7 @@ def _mx_pair(codes, scales, bits, codes_name, scales_name):
             raise ValueError(f"{n} must be two-dimensional, of dtype torch.uint8")
     rows, d = scales.shape
     d *= 32
+    _fits(d, codes_name + "'s row length")
     if codes.shape != (rows, d * bits // 8):
         _expect(codes, (rows, d * bits // 8), torch.uint8, codes_name)
     return rows, d
@@ -451,6 +458,7 @@ def mx_quantize(x, fmt, *, codes=None, scales=None, stream=None):
     if x.dim() != 2:
         raise ValueError("x must be [rows, d]")
     rows, d = x.shape
+    _fits(d, "x's row length")
     _check_mx_outputs(codes, scales, rows, d, bits)
     dev = _call_device((x, "x"), (codes, "codes"), (scales, "scales"))
     codes, scales = _mx_outputs(codes, scales, rows, d, bits, x, stream)
@@ -511,6 +519,7 @@ def add_rms_norm(x, residual=None, *, weight=None, gate=None, scale=None, shift=
     if x.dim() != 2:
         raise ValueError("x must be [rows, d]")
     rows, d = x.shape
+    _fits(d, "x's row length")
     if residual is not None:
         _shaped(residual, (rows, d), x.dtype, "residual")
     first, groups, stride, mods = None, 1, d, False
@@ -584,6 +593,9 @@ def rope(x, pos, axis_dims, *, theta=10000.0, half=False, inverse=False, out=Non
     axes = len(axis_dims)
     if not 1 <= axes <= 4:
         raise ValueError(f"axis_dims must name one to four axes (got {axes})")
+    if max(heads, hd, *axis_dims) > 2147483647 or min(axis_dims) < -2147483647:
+        for size, what in ((heads, "heads"), (hd, "head_dim"), *((abs(v), "axis_dims") for v in axis_dims)):
+            _fits(size, what)
     _shaped(pos, (tokens, axes), _torch().int32, "pos")
     if out is not None:
         _shaped(out, (tokens, heads, hd), x.dtype, "out")

@@ -164,3 +164,26 @@ def test_rows_per_mod_of_any_size(monkeypatch, per):
     q.add_rms_norm(torch.zeros((4, 64), dtype=torch.bfloat16), gate=p, rows_per_mod=per)
     rows, rows_per_mod = seen.args[3], seen.args[11]
     assert rows == 4 and rows_per_mod >= 4
+
+
+def test_sizes_beyond_32_bits_are_refused(monkeypatch):
+    """Sizes that the C calls take in 32 bits: a larger one is refused rather
+    than cut (2^32 + 64 columns would be taken for 64)."""
+    _Recorder(monkeypatch)
+    far = lambda *s, t=torch.bfloat16: torch.empty(s, dtype=t, device="meta")  # noqa: E731
+    u8, d, pos = torch.uint8, 2 ** 32 + 64, torch.zeros((1, 1), dtype=torch.int32)
+    q._torch()
+    cases = [
+        (lambda: q.mx_quantize(far(1, d), "fp4"), "x"),
+        (lambda: q.mx_dequantize(far(1, d, t=u8), far(1, d // 32, t=u8), "fp8"), "codes"),
+        (lambda: q.mx_linear(far(1, d, t=u8), far(1, d // 32, t=u8), "fp8", far(1, d, t=u8),
+                             far(1, d // 32, t=u8), "fp8"), "codes"),
+        (lambda: q.add_rms_norm(far(1, d)), "x"),
+        (lambda: q.rope(far(1, d, 64), pos, [64]), "heads"),
+        (lambda: q.rope(far(1, 1, d), pos, [64]), "head_dim"),
+        (lambda: q.rope(far(1, 1, 64), pos, [d]), "axis_dims"),
+        (lambda: q.rope(far(1, 1, 64), pos, [64 - 2 ** 32]), "axis_dims"),
+    ]
+    for call, what in cases:
+        with pytest.raises(ValueError, match=what + ".*32 bits"):
+            call()
