@@ -122,6 +122,56 @@ def test_slices_of_a_fused_projection(q, half, bf16):
     assert torch.equal(q.rope(one, pos, axes, half=half)[:, 2], want[:, 0])
 
 
+def _tokens_a_workgroup(tokens, heads, hd, turned):
+    """The launch's rule, to know that a case below runs what it is for."""
+    half, per = turned // 2, hd // 8
+    group = max(256 // half if half else 1, 1024 // (heads * per))
+    group = min(group, 1024 // half if half else 64)
+    return group if group >= 1 and tokens >= 1024 * group else 1
+
+
+@pytest.mark.parametrize("half", [False, True], ids=["pairs", "halves"])
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("tokens,heads,hd,axes,group",
+                         [(4099, 24, 128, [44, 42, 42], 4), (16387, 2, 128, [44, 42, 42], 16),
+                          (32771, 3, 64, [20, 22, 22], 32), (131075, 1, 16, [2, 4, 10], 128),
+                          (65543, 1, 80, [10, 0, 22], 64), (65539, 2, 64, [0, 0, 0], 64),
+                          (4099, 2, 512, [200, 156, 156], 4)])
+def test_several_tokens_a_workgroup(q, tokens, heads, hd, axes, group, bf16, half):
+    """Enough tokens that a workgroup takes several, the last one fewer; the
+    same inside a wider row, in place, with the elements around untouched."""
+    import torch
+    say("rope groups", tokens, heads, hd, axes, bf16, half)
+    assert _tokens_a_workgroup(tokens, heads, hd, sum(axes)) == group and tokens % group
+    x = _x((tokens, heads, hd), tokens + hd, bf16)
+    pos = np.random.default_rng(tokens).integers(-50, 4000, (tokens, len(axes))).astype(np.int32)
+    p, d = torch.from_numpy(pos).cuda(), to_device(wl.f32_to_bf16_bits(x) if bf16 else x)
+    got = q.rope(d, p, axes, half=half)
+    _check(_np(got), x, pos, axes, 10000.0, half, False, bf16)
+    wide = torch.full((tokens, heads * hd + 16), 3.0, dtype=d.dtype, device="cuda")
+    part = wide[:, 8:8 + heads * hd].unflatten(1, (heads, hd))
+    part.copy_(d)
+    q.rope(part, p, axes, half=half, out=part)
+    assert torch.equal(part, got)
+    assert bool((wide[:, :8] == 3).all()) and bool((wide[:, -8:] == 3).all())
+
+
+@pytest.mark.parametrize("half", [False, True], ids=["pairs", "halves"])
+def test_more_tokens_than_the_grid(q, half):
+    """2^20 workgroups of four tokens and more: some of them walk on."""
+    import torch
+    tokens = 4 * 2 ** 20 + 4099
+    say("rope walk", tokens, half)
+    assert _tokens_a_workgroup(tokens, 1, 512, 512) == 4
+    x = torch.randn((tokens, 1, 512), device="cuda", dtype=torch.bfloat16)
+    pos = torch.randint(-99, 9999, (tokens, 2), device="cuda", dtype=torch.int32)
+    parts = [slice(0, 9), slice(4 * 2 ** 20 - 7, 4 * 2 ** 20 + 9), slice(tokens - 9, tokens)]
+    want = [q.rope(x[s].clone(), pos[s].clone(), [256, 256], half=half) for s in parts]
+    q.rope(x, pos, [256, 256], half=half, out=x)
+    for s, w in zip(parts, want):
+        assert torch.equal(x[s], w)
+
+
 @pytest.mark.parametrize("half", [False, True])
 def test_inverse_is_the_gradient(q, half):
     """<g, rope(x + e d) - rope(x - e d)> / 2e = <rope^-1(g), d>: the map is
