@@ -218,6 +218,55 @@ def test_linear_nan_block_reaches_its_row_only(q, M, N, K, fa, fw):
     np.testing.assert_array_equal(y[:M - 1, 1:], clean[:M - 1, 1:])
 
 
+def _whole_numbers(rows, K, fmt, seed):
+    """Elements in {-1, 0, 1}, few of them not 0, under scales 1/2, 1 and 2:
+    codes, scale bytes and the values on the device."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    u = torch.rand((rows, K), device="cuda", generator=g)
+    v = (u > 0.96).float() - (u < 0.04).float()
+    e = torch.randint(-1, 2, (rows, K // 32), device="cuda", generator=g)
+    one, sign = (2, 8) if fmt == "fp4" else (0x38, 0x80)
+    c = (one * (v != 0) + sign * (v < 0)).to(torch.uint8)
+    c = c[:, 0::2] | (c[:, 1::2] << 4) if fmt == "fp4" else c
+    return c.contiguous(), (e + 127).to(torch.uint8), v * torch.exp2(e.float()).repeat_interleave(32, 1)
+
+
+@pytest.mark.parametrize("fa,fw", [("fp4", "fp4"), ("fp8", "fp4"), ("fp4", "fp8"), ("fp8", "fp8")])
+@pytest.mark.parametrize("M,N,K", [(5000, 5000, 544), (5000, 5003, 1056), (6000, 6000, 544), (5990, 6001, 2592),
+                                   (8200, 8200, 288)])
+def test_linear_over_many_tiles(q, M, N, K, fa, fw):
+    """More tiles than the card holds at once (256 tiles at 5000 and 8200, 128
+    tiles at 6000): workgroups walk to their next ones.  Sums of quarters below
+    64 fit bf16, and every step's products differ by 2^4 at most, which no
+    alignment drops, so every element is exact."""
+    import torch
+    say("mx linear many tiles", M, N, K, fa, fw)
+    ac, as_, a = _whole_numbers(M, K, fa, M + K)
+    wc, ws, w = _whole_numbers(N, K, fw, N + 3 * K)
+    want = a @ w.t()
+    assert torch.equal(want.bfloat16().float(), want)
+    for _ in range(2):
+        assert torch.equal(q.mx_linear(ac, as_, fa, wc, ws, fw).float(), want)
+
+
+@pytest.mark.parametrize("fa,fw", [("fp8", "fp4"), ("fp4", "fp8"), ("fp8", "fp8")])
+@pytest.mark.parametrize("M,N", [(20, 90), (600, 1000), (1500, 1600), (2900, 3000)])
+def test_linear_after_a_call_full_of_nan(q, M, N, fa, fw):
+    """K ends inside a stage: what lies behind it has to be zeros, not what the
+    call before left on the chip (here NaN in every e4m3 element)."""
+    import torch
+    say("mx linear after nan", M, N, fa, fw)
+    ac, as_, a = _whole_numbers(M, 160, fa, M)
+    wc, ws, w = _whole_numbers(N, 160, fw, N)
+    bad = lambda n, f: (torch.full((n, 1024 // (2 if f == "fp4" else 1)), 0x7f, device="cuda", dtype=torch.uint8),  # noqa: E731
+                        torch.full((n, 32), 127, device="cuda", dtype=torch.uint8))
+    ba, bw = bad(M, fa), bad(N, fw)
+    for _ in range(2):
+        assert bool(q.mx_linear(*ba, fa, *bw, fw).isnan().all())
+        assert torch.equal(q.mx_linear(ac, as_, fa, wc, ws, fw).float(), a @ w.t())
+
+
 def test_linear_writes_only_y(q):
     """Guard bytes around y stay as they were, at sizes that end inside a tile."""
     import torch
