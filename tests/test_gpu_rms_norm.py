@@ -287,6 +287,23 @@ def test_offsets_beyond_32_bits(q):
     assert bool((codes[:-5] == 0).all())
 
 
+@pytest.mark.parametrize("d,per", [(32, 4), (2080, 2), (5152, 1)])
+def test_more_rows_than_the_grid(q, d, per):
+    """2^20 workgroups of one, two or four rows and more: some of them walk on
+    to another row, also where a row's mean has overflowed."""
+    import torch
+    rows = per * 2 ** 20 + 1025
+    say("rms norm walk", rows, d)
+    x = torch.randn((rows, d), device="cuda", dtype=torch.bfloat16)
+    for k in (1, per * 2 ** 20 - 2, per * 2 ** 20 + 2, rows - 2):
+        x[k] *= 2.0 ** 120
+    parts = [slice(0, 9), slice(per * 2 ** 20 - 7, per * 2 ** 20 + 9), slice(rows - 9, rows)]
+    want = [q.add_rms_norm(x[s].clone(), sum_out=False)[1] for s in parts]
+    q.add_rms_norm(x, sum_out=False, out=x)
+    for s, w in zip(parts, want):
+        assert torch.equal(x[s], w) and bool((w.double().square().mean(1) - 1).abs().max() < 0.02)
+
+
 def test_empty(q):
     import torch
     h, y = q.add_rms_norm(torch.zeros((0, 64), device="cuda"))
