@@ -350,7 +350,7 @@ int oq_add_rms_norm(const void *x, const void *residual, int dtype, int64_t rows
  * The first R = sum(axis_dims) elements of each head are R/2 pairs, numbered
  * axis after axis; pair i of axis a turns by pos_a * theta^(-2 i / axis_dims[a]):
  *   (u, v) -> (u cos - v sin, u sin + v cos)
- * and the other head_dim - R elements are copied.  Angles are exact to 2^-32
+ * and the other head_dim - R elements are copied.  Angles are exact to 2^-30
  * of a turn at every int32 position.
  *   x, y: device, dtype; element e of head h of token t at t * token stride +
  *     h * head stride + e (strides in elements, multiples of 16 bytes, >= 0), so

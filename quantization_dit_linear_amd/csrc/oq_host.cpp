@@ -23,6 +23,7 @@
 
 #include "../../include/orbitquant.h"
 #include "oq_internal.h"
+#include "rope_rates.h"
 
 namespace {
 
@@ -996,23 +997,7 @@ int oq_rope(const void *x, int dtype, int64_t tokens, int heads, int head_dim, i
   a.inverse = (flags & OQ_ROPE_INVERSE) != 0;
   a.y = y;
   a.stream = (hipStream_t)stream;
-  // Turns per position of each pair, theta^(-2 i / size) / 2 pi <= 1 / 2 pi
-  // (theta >= 1), in units of 2^-64.  Exponentials for every 16th pair, a
-  // product a pair between: at most 16 roundings of 2^-64, below 2^-31 of a
-  // turn at any int32 position, for a small part of the exponentials' time.
-  int j = 0;
-  const long double log_theta = logl((long double)theta), unit64 = 0x1p64L / (2 * acosl(-1.0L));
-  for (int i = 0; i < axes; i++) {
-    if (axis_dims[i] == 0) continue;
-    const long double rate = log_theta / axis_dims[i], ratio = expl(-2 * rate);
-    long double f = unit64;
-    for (int k = 0; k < axis_dims[i]; k += 2, j++) {
-      if (k % 32 == 0) f = expl(-k * rate) * unit64;
-      a.freq[j] = (uint64_t)(int64_t)(f + 0.5L);
-      a.axis[j] = (uint8_t)i;
-      f *= ratio;
-    }
-  }
+  oq::rope_rates(theta, axes, axis_dims, a.freq, a.axis);
   hipError_t e = oq::launch_rope(a);
   return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
 }
