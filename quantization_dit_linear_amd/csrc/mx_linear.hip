@@ -70,8 +70,7 @@ struct MxTile {
   static constexpr int SROWS = TM + TN;
   static constexpr int SBUF = 4 * SROWS * 4;     // scales of 16 blocks: 4 planes of one word a row
   static constexpr int SPG = 512 / KS;           // stages that one such group lasts
-  static constexpr int EROWS = 32;               // output rows a wave stages at once
-  static constexpr int EPI = EROWS * 64 * JB;
+  static constexpr int EPI = 32 * 64 * JB;       // a wave's 32 output rows on their way out
   static constexpr int SC0 = NST * STAGE, LDS = SC0 + 2 * SBUF;
   static_assert(2 * WN * EPI <= SC0, "the output goes through the stages' LDS");
   static_assert(LDS * WGS <= 160 * 1024, "LDS of one CU");
@@ -349,51 +348,46 @@ __global__ __launch_bounds__(TL::THREADS, TL::WGS *TL::THREADS / 256) void mx_ti
     }
     wait_and_sync<0>();  // the requests past the last stage are done, every buffer is free
 
-    // Epilogue: EROWS output rows of the wave's block at a time through the
+    // Epilogue: 32 output rows of the wave's block at a time through the
     // wave's own LDS region (16-byte pieces XOR-swizzled by the row), out as
     // whole rows in 16-byte pieces.  Lane (r, g) holds row r, columns
-    // 32 j + 8 q + 4 g + (0..3); half of the lanes have a row of the pass.
+    // 32 j + 8 q + 4 g + (0..3).
     uint8_t *reg = lds + wave * TL::EPI;
-    constexpr int PPR = 4 * JB, ER = TL::EROWS;  // pieces per row
+    constexpr int PPR = 4 * JB;  // pieces per row
     int lane_ = lane;  // opaque: keeps the addresses below out of the K loop's registers
     asm volatile("" : "+v"(lane_));
-    const int er = lane_ & (ER - 1), eg = lane_ >> 5, c = lane_ % PPR;
+    const int er = lane_ & 31, eg = lane_ >> 5, c = lane_ % PPR;
     const int mw = m0 + wm * 32 * IB, n = n0 + wn * 32 * JB + 8 * c;
 #pragma unroll
     for (int i = 0; i < IB; i++) {
 #pragma unroll
-      for (int half = 0; half < 32 / ER; half++) {
-        if (ER == 32 || ((lane_ >> 4) & 1) == half) {
+      for (int j = 0; j < JB; j++)
 #pragma unroll
-          for (int j = 0; j < JB; j++)
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-              const bf16x2 p0 = {(__bf16)acc[j][i][4 * q], (__bf16)acc[j][i][4 * q + 1]};
-              const bf16x2 p1 = {(__bf16)acc[j][i][4 * q + 2], (__bf16)acc[j][i][4 * q + 3]};
-              *(u32x2 *)(reg + er * (64 * JB) + (((4 * j + q) ^ (er & (PPR - 1))) << 4) + 8 * eg) =
-                  u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
-            }
+        for (int q = 0; q < 4; q++) {
+          const bf16x2 p0 = {(__bf16)acc[j][i][4 * q], (__bf16)acc[j][i][4 * q + 1]};
+          const bf16x2 p1 = {(__bf16)acc[j][i][4 * q + 2], (__bf16)acc[j][i][4 * q + 3]};
+          *(u32x2 *)(reg + er * (64 * JB) + (((4 * j + q) ^ (er & (PPR - 1))) << 4) + 8 * eg) =
+              u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
         }
-        __builtin_amdgcn_wave_barrier();  // LDS works in order within a wave
-        const int m1 = mw + 32 * i + ER * half;
+      __builtin_amdgcn_wave_barrier();  // LDS works in order within a wave
+      const int m1 = mw + 32 * i;
 #pragma unroll
-        for (int k = 0; k < (ER * PPR + 63) / 64; k++) {
-          const int rr = lane_ / PPR + k * (64 / PPR);
-          const u32x4 o = *(const u32x4 *)(reg + rr * (64 * JB) + ((c ^ (rr & (PPR - 1))) << 4));
-          uint16_t *yp = Y + (int64_t)(m1 + rr) * N + n;
-          if (m1 + rr >= M || n >= N) continue;
-          if (n + 8 <= N) {
-            __builtin_nontemporal_store(o, (u32x4_y *)yp);
-          } else {
+      for (int k = 0; k < (32 * PPR + 63) / 64; k++) {
+        const int rr = lane_ / PPR + k * (64 / PPR);
+        const u32x4 o = *(const u32x4 *)(reg + rr * (64 * JB) + ((c ^ (rr & (PPR - 1))) << 4));
+        uint16_t *yp = Y + (int64_t)(m1 + rr) * N + n;
+        if (m1 + rr >= M || n >= N) continue;
+        if (n + 8 <= N) {
+          __builtin_nontemporal_store(o, (u32x4_y *)yp);
+        } else {
 #pragma unroll 1
-            for (int e = 0; e < 8; e++) {
-              const uint32_t d = e & 4 ? (e & 2 ? o[3] : o[2]) : e & 2 ? o[1] : o[0];
-              if (n + e < N) yp[e] = (uint16_t)(d >> (16 * (e & 1)));
-            }
+          for (int e = 0; e < 8; e++) {
+            const uint32_t d = e & 4 ? (e & 2 ? o[3] : o[2]) : e & 2 ? o[1] : o[0];
+            if (n + e < N) yp[e] = (uint16_t)(d >> (16 * (e & 1)));
           }
         }
-        __builtin_amdgcn_wave_barrier();
       }
+      __builtin_amdgcn_wave_barrier();
     }
   }
 }
@@ -451,7 +445,6 @@ __global__ __launch_bounds__(512) void mx_rows_kernel(
 #pragma unroll
     for (int i = 0; i < MB; i++) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const uint8_t *as = As + (int64_t)m0 * nb, *ws = Ws + (int64_t)n0 * nb;
-#pragma unroll 2
   for (int c = wave; c < C; c += WAVES) {
     Frag<FW> w[NB][2];
     Frag<FA> a[MB][2];
