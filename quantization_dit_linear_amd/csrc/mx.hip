@@ -9,10 +9,12 @@
 // by a power of two is exact, so the codes are a function of the input
 // alone; there is no accumulated error to bound.
 //
-// Memory bound: one pass, 16 bytes of bf16 a lane.  13824 x 5120 bf16 to e2m1
-// 32.7 us (5.5 TB/s), back to bf16 35.5 us (5.0 TB/s); 32760 x 5120 bf16 to e4m3
-// 89 us (5.7 TB/s), back 88 us (5.7 TB/s): the rate of a large copy (5.3 TB/s)
-// and above.  The smallest calls are a launch (2.6 us).
+// Memory bound: one pass, 16 bytes of bf16 a lane.  Measured beside a large
+// copy's 5.3 TB/s: 13824 x 5120 bf16 to e2m1 36 us (5.0 TB/s), fp32 to e2m1 66 us
+// (4.9), e2m1 to bf16 26 us (the codes come from the Infinity Cache); 32760 x
+// 5120 bf16 to e4m3 83 to 105 us by what ran before it (6.1 to 4.8), fp32 to
+// e4m3 180 us (4.7), e4m3 to bf16 83 us (6.1), to fp32 205 us (4.1).  The
+// smallest calls are a launch (1.8 to 2.8 us).
 #include <hip/hip_runtime.h>
 
 #include "mx_codec.h"

@@ -22,16 +22,16 @@
 // products.  Few rows: no tile has enough of them to share, the weights are
 // streamed once, K split over the waves of a workgroup.
 //
-// Measured (one MI355X): 32760 x 15360 x 5120, e2m1 both: 1.24-1.30 ms, 4.0-4.2
-// PFLOP/s; 32760 x 5120 x 13824, e4m3 x e2m1: 1.68 ms, 2.75 PFLOP/s; e4m3 both:
-// 1.82 ms, 2.55 PFLOP/s.  The matrix instructions alone, on random registers,
+// Measured (one MI355X): 32760 x 15360 x 5120, e2m1 both: 1.22-1.29 ms, 4.0-4.2
+// PFLOP/s; e2m1 x e4m3: 1.87-1.91 ms, 2.7 PFLOP/s; e4m3 both: 2.03-2.18 ms, 2.4-2.5
+// PFLOP/s; 32760 x 5120 x 13824, e4m3 x e2m1: 1.68 ms, 2.76 PFLOP/s.  The matrix instructions alone, on random registers,
 // keep 6.6, 4.3 and 3.9 PFLOP/s on this card: power, not issue, is what bounds
 // them (about 1.8 GHz under this load; the matrix cores are busy 57% of the
 // time), and the requests for the next stage, drained at each barrier, take
-// most of the rest (without them 1.04 ms).  At the first of those sizes four
+// most of the rest (without them 1.04 ms); a quarter of them are for scales.  At the first of those sizes four
 // waves of 128 x 128 took 1.26 ms, stages of 128 elements (64-byte pieces) with
 // four of them in LDS 1.38, 256 x 128 tiles with three stages 1.51, 128 tiles
-// 1.63.  2 x 30720 x 5120: 16.4 us, 5.1 TB/s of weights, the rate of a large
+// 1.63.  2 x 30720 x 5120: 16.5 us, 5.1 TB/s of weights, the rate of a large
 // copy.
 #include <hip/hip_runtime.h>
 

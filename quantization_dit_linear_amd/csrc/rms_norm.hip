@@ -16,9 +16,10 @@
 // slower (32760 x 5120: 280 against 255 us), the parameters come from the L2.
 // Stores are non-temporal (30000 x 512: 24 against 20 us).
 //
-// Measured: 32760 x 5120 bf16 228 us (5.9 TB/s; a large copy 5.3), with gate
-// and modulation 246 us (5.4), into e4m3 242 us (4.9); fp32 4111 x 1536 23 us
-// (4.3).  One row of 5120: 4.9 us, one wait for memory after another.
+// Measured: 32760 x 5120 bf16 230 us (5.8 TB/s; a large copy 5.3), with gate
+// and modulation 249 us (5.4), that into e4m3 259 us (4.6), into e2m1 245 us
+// (4.5); 9216 x 12288 184 us (4.9); fp32 4111 x 1536 22.4 us (4.5).  One row of
+// 5120: 4.8 us, one wait for memory after another.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -12,9 +12,9 @@
 // and sines serve all its heads, so a workgroup computes them once into LDS
 // (for several tokens, so that every thread has a pair to work on) and then
 // streams the heads.  Measured: 32760 tokens x 80 heads x 128 bf16, strided
-// input, 255 us (5.2 TB/s; each thread computing its own: 443 us); 24 heads of
-// 64: 35 us (5.7 TB/s); two heads of 128: 19 us (3.2 TB/s, the table's
-// arithmetic); one token 3.8 us.
+// input, 257 us (5.2 TB/s; each thread computing its own: 443 us); half-split 251
+// us; 40 heads of fp32 259 us; 24 heads of 64: 35 us (5.7 TB/s); two heads of
+// 128: 12.7 us (2.6 TB/s, the table's arithmetic); one token 3.9 us.
 #include <hip/hip_runtime.h>
 
 #include "mx_codec.h"
@@ -137,8 +137,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int tok_group, in
 
 hipError_t launch_rope(const RopeArgs &a) {
   // as many tokens a workgroup as give its threads a pair and four items
-  // each; one, and a slice of the heads, where tokens are too few to fill the
-  // card
+  // each, if that leaves 1024 workgroups (four a CU); else one token, and a
+  // slice of the heads where the tokens alone are still fewer than that
   const int half = a.turned / 2, per = a.head_dim / 8, most = half > 0 ? kPairs / half : 64;
   const int64_t items = 1024 / ((int64_t)a.heads * per);
   int group = half > 0 ? 256 / half : 1;
