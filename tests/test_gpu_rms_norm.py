@@ -140,6 +140,13 @@ def test_gate_and_modulation(q, rows, d, groups, bf16, pbf16, fmt):
     _check(q, rows, d, bf16, pbf16, fmt, groups=groups, gate=True, mod=True)
 
 
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("rows,d,groups", [(1, 64, 1), (7, 160, 3), (10, 5120, 2), (3, 12288, 2), (515, 512, 5)])
+def test_gate_and_modulation_into_four_bits(q, rows, d, groups, bf16):
+    say("rms norm mod fp4", rows, d, groups, bf16)
+    _check(q, rows, d, bf16, bf16, "fp4", groups=groups, gate=True, mod=True)
+
+
 @pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("weight", [False, True])
 @pytest.mark.parametrize("gate,mod", [(False, False), (True, False), (False, True)])
