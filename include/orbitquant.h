@@ -97,6 +97,9 @@ extern "C" {
 #define OQ_ROPE_INVERSE (1u << 1) /* turn by the opposite angle: undoes the embedding, and is the
                                      gradient of it (the turn is orthogonal) */
 
+/* attention flags */
+#define OQ_ATTN_CAUSAL (1u << 0) /* a query sees no token behind its own position */
+
 /* Text for a status code.  Never NULL; the string is static. */
 const char *oq_strerror(int status);
 
@@ -369,6 +372,132 @@ int oq_add_rms_norm(const void *x, const void *residual, int dtype, int64_t rows
 int oq_rope(const void *x, int dtype, int64_t tokens, int heads, int head_dim, int64_t x_token,
             int64_t x_head, const int32_t *pos, int axes, const int *axis_dims, double theta,
             uint32_t flags, void *y, int64_t y_token, int64_t y_head, void *stream);
+
+/* ---- the cached-attention path: projection -> heads -> cache -> attention ----
+ *
+ * What a block with a key/value cache runs for its new tokens (one token a
+ * step, a chunk of a streamed video, a prompt that every denoising step reads
+ * again): the projection of few rows by 4-bit weights with group scales, the
+ * norm and embedding of the query and key heads, the new keys and values into a
+ * 4-bit cache, and attention over it.  Conventions as above.
+ *
+ * The cache: `pages` pages of `page_size` tokens, for keys and for values
+ *   codes  [pages][kv_heads][page_size][head_dim / 2]
+ *   scales [pages][kv_heads][page_size][head_dim / 32]
+ * a head's row as an OQ_MX_FP4 row (so oq_mx_dequantize reads a cache back).  A
+ * token's slot is page * page_size + its offset in the page.
+ * head_dim: a multiple of 32, 32 <= head_dim <= 256; kv_heads up to 65535;
+ * page_size >= 1; codes and scales 16-byte aligned. */
+
+/* INT4 weights with a scale for every `group` consecutive coordinates of a row:
+ *   zeros NULL: scale = max |w| / 7, nibble = rint(w / scale) + 8
+ *   zeros:      scale = hi / 15 - lo / 15 with hi = max(w, 0), lo = min(w, 0),
+ *               zero = rint(-lo / scale), nibble = rint(w / scale) + zero in [0, 15]
+ * in fp32 (IEEE division, ties to even), with the scale already rounded to
+ * scale_dtype; a scale of 0 gives the nibble that stands for 0 (8, or zero = 0).
+ *   W: device, fp32 or bf16 [n_out][d_in] (4-byte aligned)
+ *   q4: device [n_out][d_in / 2] (16-byte aligned), the even coordinate in the
+ *       low nibble; scales, zeros: device, scale_dtype [n_out][d_in / group]
+ *       (4-byte aligned)
+ * group a multiple of 32 that divides d_in; d_in <= 16384 (else
+ * OQ_EUNSUPPORTED).  No two arrays may share a byte.  n_out = 0 no-op.
+ * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
+int oq_rtn4_group_prepare_weights(const void *W, int dtype, int64_t n_out, int d_in, int group,
+                                  uint8_t *q4, void *scales, void *zeros, int scale_dtype,
+                                  void *stream);
+
+/* The projection with those weights (any nibbles, scales and zeros):
+ *   y[m][n] = bf16( sum_g scale_ng sum_{k in g} x_mk (nibble_nk - zero_ng) )
+ * zero = 8 where zeros is NULL; fp32 accumulation, one bf16 rounding, no bias.
+ *   x: device fp32 or bf16 [M][K] (16-byte aligned); y: bf16 [M][N], apart from
+ *   the inputs
+ * Sized for few rows.  M = 0 or N = 0 no-op.
+ * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
+int oq_rtn4_group_linear(const void *x, int dtype, int64_t M, const uint8_t *q4,
+                         const void *scales, const void *zeros, int scale_dtype, int group,
+                         int64_t N, int K, uint16_t *y, void *stream);
+
+/* RMS norm of every query and key head with the rotary embedding (as oq_rope,
+ * its axes, angles and pairs) in the same pass:
+ *   n = x / sqrt(mean(x^2) + eps) * weight, over the head's elements
+ *   (u, v) -> (u cos - v sin, u sin + v cos) for the turned pairs of n
+ * fp32 arithmetic, one rounding to dtype.
+ *   q, k, q_out, k_out: device, dtype, strided as oq_rope's x and y: each may
+ *     be its own input (in place), no output may otherwise meet an input or the
+ *     other output.  k and k_out NULL with k_heads 0: queries alone
+ *   q_weight, k_weight: device, param_dtype [head_dim], 16-byte aligned, or NULL
+ *   eps: finite, at least the smallest normal fp32 number
+ *   pos: device int32 [tokens][axes]; flags: OQ_ROPE_HALF
+ * Limits as oq_rope's; heads up to 2^24 together.  tokens = 0 is a no-op.
+ * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
+int oq_qk_norm_rope(const void *q, int q_heads, int64_t q_token, int64_t q_head, const void *k,
+                    int k_heads, int64_t k_token, int64_t k_head, int dtype, int64_t tokens,
+                    int head_dim, const void *q_weight, const void *k_weight, int param_dtype,
+                    float eps, const int32_t *pos, int axes, const int *axis_dims, double theta,
+                    uint32_t flags, void *q_out, int64_t q_out_token, int64_t q_out_head,
+                    void *k_out, int64_t k_out_token, int64_t k_out_head, void *stream);
+
+/* Write the keys and values of tokens into the cache, quantized as
+ * oq_mx_quantize does.
+ *   k, v: device, dtype [tokens][kv_heads][head_dim], any strides that are
+ *     multiples of 16 bytes and >= 0, 16-byte aligned
+ *   slots: device int64 [tokens]; a token whose slot is negative or past the
+ *     cache is not written.  Two tokens may not share a slot (its contents are
+ *     then unspecified)
+ * The other slots keep their bytes.  tokens up to 2^30; tokens = 0 no-op.
+ * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
+int oq_mx_kv_write(const void *k, const void *v, int dtype, int64_t tokens, int64_t k_token,
+                   int64_t k_head, int64_t v_token, int64_t v_head, const int64_t *slots,
+                   uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes, uint8_t *v_scales,
+                   int64_t pages, int kv_heads, int page_size, int head_dim, void *stream);
+
+/* Bytes of workspace that oq_mx_kv_attention takes for these sizes (0: none; -1: a
+ * size that the call refuses). */
+int64_t oq_mx_kv_attention_workspace(int64_t q_tokens, int q_heads, int kv_heads, int head_dim,
+                                     int64_t batch, int page_size, int64_t table_pages);
+
+/* Attention of new queries over the cached keys and values of their sequences:
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q k_j)
+ * over the tokens j that the query sees; query head h reads key head
+ * h / (q_heads / kv_heads).
+ *   q, out: device, dtype [q_tokens][q_heads][head_dim], strided as oq_rope's x
+ *     and y, apart from each other
+ *   batch sequences; q_starts: device int32 [batch + 1], sequence b's queries
+ *     are the tokens [q_starts[b], q_starts[b + 1]); the outputs of tokens behind
+ *     the last sequence are left as they were.  NULL: the tokens are split
+ *     evenly (q_tokens a multiple of batch)
+ *   lengths: device int32 [batch], tokens in the cache (counting the new ones);
+ *     taken as 0 below 0 and as table_pages * page_size above that
+ *   table: device int32 [batch][table_pages], the pages of each sequence; a
+ *     token whose page number is not in [0, pages) reads as NaN.  NULL: sequence
+ *     b's tokens are page b alone (table_pages = 1, pages >= batch)
+ *   With n queries and length L, query i stands at position L - n + i.  It sees
+ *     every token, with OQ_ATTN_CAUSAL those up to its position, and with
+ *     window > 0 (which needs OQ_ATTN_CAUSAL) of these the last `window`.  A
+ *     query that sees none gets zeros (and lse -infinity)
+ *   lse: device fp32 [q_tokens][q_heads], ln sum_j p_j; may be NULL
+ *   scale: finite
+ *   workspace: device, 16-byte aligned, at least oq_mx_kv_attention_workspace
+ *     bytes, not shared with other work in flight; its contents before and after
+ *     do not matter
+ * fp32 statistics and sums.  bf16 queries: the products' operands are the bf16
+ * values (the cache's are exact in bf16) and weights p rounded to bf16; fp32
+ * queries keep fp32 accuracy.  Scores must be finite in fp32; a row with a NaN
+ * among its query or the keys or values it sees is NaN, tokens that it does not
+ * see do not reach it.  Scale bytes 253 to 255 read as NaN here (the writer
+ * makes none but 255), and values below 2^-126 may count as 0.
+ * A call gives the same bits every time; the order of a row's sums is chosen by
+ * the sizes.  q_tokens * q_heads / kv_heads up to 2^28, batch up to 2^20,
+ * table_pages * page_size up to 2^30.  q_tokens = 0 or batch = 0 no-op.
+ * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
+int oq_mx_kv_attention(const void *q, int dtype, int64_t q_tokens, int q_heads, int64_t q_token,
+                       int64_t q_head, const uint8_t *k_codes, const uint8_t *k_scales,
+                       const uint8_t *v_codes, const uint8_t *v_scales, int64_t pages,
+                       int kv_heads, int page_size, int head_dim, int64_t batch,
+                       const int32_t *lengths, const int32_t *q_starts, const int32_t *table,
+                       int64_t table_pages, float scale, uint32_t flags, int window, void *out,
+                       int64_t out_token, int64_t out_head, float *lse, void *workspace,
+                       int64_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

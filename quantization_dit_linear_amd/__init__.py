@@ -18,8 +18,14 @@ Functions mirror the C entry points:
 * :func:`mx_linear`       -> ``oq_mx_linear``
 * :func:`add_rms_norm`    -> ``oq_add_rms_norm``
 * :func:`rope`            -> ``oq_rope``
+* :func:`rtn4_group_prepare_weights`, :func:`rtn4_group_linear` -> ``oq_rtn4_group_*``
+* :func:`qk_norm_rope`    -> ``oq_qk_norm_rope``
+* :func:`mx_kv_write`, :func:`mx_kv_attention` -> ``oq_mx_kv_write``, ``oq_mx_kv_attention``
+  (:func:`mx_kv_cache` allocates a cache for them)
 """
+import collections
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -33,6 +39,7 @@ OQ_ROT_NO_SIGNS, OQ_OUT_F32_ROTATED, OQ_OUT_BF16_DEQUANT, OQ_ROT_INPUT_PERMUTED 
 OQ_CODEBOOK_SPHERE = 16
 OQ_MX_FP4, OQ_MX_FP8 = 4, 8
 OQ_ROPE_HALF, OQ_ROPE_INVERSE = 1, 2
+OQ_ATTN_CAUSAL = 1
 
 # every symbol the header declares, with (restype, argtypes)
 _P = ctypes.c_void_p
@@ -76,6 +83,31 @@ _SIGS = {
                                ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int, _P,
                                ctypes.c_double, ctypes.c_uint32, _P, ctypes.c_int64,
                                ctypes.c_int64, _P]),
+    "oq_rtn4_group_prepare_weights": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int,
+                                                     ctypes.c_int, _P, _P, _P, ctypes.c_int, _P]),
+    "oq_rtn4_group_linear": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, _P, _P, _P,
+                                            ctypes.c_int, ctypes.c_int, ctypes.c_int64,
+                                            ctypes.c_int, _P, _P]),
+    "oq_qk_norm_rope": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, _P,
+                                       ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
+                                       ctypes.c_int64, ctypes.c_int, _P, _P, ctypes.c_int,
+                                       ctypes.c_float, _P, ctypes.c_int, _P, ctypes.c_double,
+                                       ctypes.c_uint32, _P, ctypes.c_int64, ctypes.c_int64, _P,
+                                       ctypes.c_int64, ctypes.c_int64, _P]),
+    "oq_mx_kv_write": (ctypes.c_int, [_P, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
+                                      ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P, _P,
+                                      _P, _P, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                      ctypes.c_int, _P]),
+    "oq_mx_kv_attention_workspace": (ctypes.c_int64, [ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                                      ctypes.c_int, ctypes.c_int64, ctypes.c_int,
+                                                      ctypes.c_int64]),
+    "oq_mx_kv_attention": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int,
+                                          ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P,
+                                          ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                          ctypes.c_int64, _P, _P, _P, ctypes.c_int64,
+                                          ctypes.c_float, ctypes.c_uint32, ctypes.c_int, _P,
+                                          ctypes.c_int64, ctypes.c_int64, _P, _P, ctypes.c_int64,
+                                          _P]),
     "oq_diag_mfma_f16": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, _P]),
 }
 
@@ -609,6 +641,245 @@ def rope(x, pos, axis_dims, *, theta=10000.0, half=False, inverse=False, out=Non
                        _raw_stream(stream, dev))
     _check(rc, "oq_rope")
     return out
+
+
+# ---------------------------------------------- the cached-attention path --
+
+KVCache = collections.namedtuple("KVCache", "k_codes k_scales v_codes v_scales")
+
+
+def _group_arrays(q4, scales, zeros, K):
+    """(N, group) of 4-bit group weights, whose shapes must agree with K."""
+    torch = _torch()
+    for t, n in ((q4, "q4"), (scales, "scales")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+        if t.dim() != 2:
+            raise ValueError(f"{n} must be two-dimensional")
+    N, groups = scales.shape
+    if q4.shape != (N, K // 2) or q4.dtype is not torch.uint8:
+        _expect(q4, (N, K // 2), torch.uint8, "q4")
+    if groups < 1 or K % groups:
+        raise ValueError(f"scales has {groups} groups for {K} columns")
+    if zeros is not None:
+        _shaped(zeros, (N, groups), scales.dtype, "zeros")
+    return N, K // groups
+
+
+def rtn4_group_prepare_weights(W, group, *, zeros=False, scale_dtype=None, stream=None):
+    """INT4 weights of W [N, K] (bfloat16 or float32) with a scale for every
+    `group` columns: (uint8 [N, K/2], scales [N, K/group]), and with zeros=True
+    zero points of the same shape as a third.  scale_dtype: bfloat16 (default)
+    or float32."""
+    torch = _torch()
+    if W.dim() != 2:
+        raise ValueError("W must be [N, K]")
+    N, K = W.shape
+    _fits(K, "W's row length")
+    if group < 1 or K % group:
+        raise ValueError(f"group ({group}) must divide W's row length ({K})")
+    dev = _call_device((W, "W"))
+    scale_dtype = scale_dtype or torch.bfloat16
+    q4 = _empty((N, K // 2), torch.uint8, W, stream)
+    scales = _empty((N, K // group), scale_dtype, W, stream)
+    zero = _empty((N, K // group), scale_dtype, W, stream) if zeros else None
+    rc = lib().oq_rtn4_group_prepare_weights(_ptr(W, "W"), _element(W), N, K, group, q4.data_ptr(),
+                                             scales.data_ptr(), zero.data_ptr() if zeros else None,
+                                             _element(scales), _raw_stream(stream, dev))
+    _check(rc, "oq_rtn4_group_prepare_weights")
+    return (q4, scales, zero) if zeros else (q4, scales)
+
+
+def rtn4_group_linear(x, q4, scales, zeros=None, *, out=None, stream=None):
+    """bf16 y [M, N] = sum_g scales[n, g] sum_{k in g} x[m, k] (nibble[n, k] - zeros[n, g])
+    for few rows x [M, K] (bfloat16 or float32); q4 uint8 [N, K/2], scales and
+    zeros [N, K/group] of one type, bfloat16 or float32 (no zeros: 8)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    _fits(K, "x's row length")
+    N, group = _group_arrays(q4, scales, zeros, K)
+    if out is not None:
+        _shaped(out, (M, N), _T.bfloat16, "out")
+    dev = _call_device((x, "x"), (q4, "q4"), (scales, "scales"), (zeros, "zeros"), (out, "out"))
+    if out is None:
+        out = _empty((M, N), _T.bfloat16, x, stream)
+    rc = lib().oq_rtn4_group_linear(_ptr(x, "x"), _element(x), M, _ptr(q4, "q4"),
+                                    _ptr(scales, "scales"),
+                                    None if zeros is None else _ptr(zeros, "zeros"),
+                                    _element(scales), group, N, K, _ptr(out, "out"),
+                                    _raw_stream(stream, dev))
+    _check(rc, "oq_rtn4_group_linear")
+    return out
+
+
+def qk_norm_rope(q, k, pos, axis_dims, *, q_weight=None, k_weight=None, eps=1e-6, theta=10000.0,
+                 half=False, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q [tokens, q_heads, head_dim] and k [tokens,
+    k_heads, head_dim] (or None) with weights [head_dim] (or None), and the rotary
+    embedding at pos int32 [tokens, axes] as :func:`rope` has it, in one pass:
+    (q_out, k_out).  Strides as in rope: the slices of a fused projection's output
+    are taken as they lie; q_out may be q and k_out k (in place)."""
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q and k must be [tokens, heads, head_dim]")
+    tokens, q_heads, hd = q.shape
+    axes = len(axis_dims)
+    if not 1 <= axes <= 4:
+        raise ValueError(f"axis_dims must name one to four axes (got {axes})")
+    k_heads = 0
+    if k is not None:
+        k_heads = k.shape[1]
+        _shaped(k, (tokens, k_heads, hd), q.dtype, "k")
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need a k")
+    if max(q_heads, k_heads, hd, *axis_dims) > 2147483647 or min(axis_dims) < -2147483647:
+        for size, what in ((q_heads, "heads"), (k_heads, "heads"), (hd, "head_dim"),
+                           *((abs(v), "axis_dims") for v in axis_dims)):
+            _fits(size, what)
+    _shaped(pos, (tokens, axes), _torch().int32, "pos")
+    first = q_weight if q_weight is not None else k_weight
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _shaped(w, (hd,), first.dtype, n)
+    for t, x, n in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if t is not None:
+            _shaped(t, x.shape, x.dtype, n)
+    dev = _call_device((q, "q"), (k, "k"), (pos, "pos"), (q_weight, "q_weight"),
+                       (k_weight, "k_weight"), (q_out, "q_out"), (k_out, "k_out"))
+    if q_out is None:
+        q_out = _empty((tokens, q_heads, hd), q.dtype, q, stream)
+    if k is not None and k_out is None:
+        k_out = _empty((tokens, k_heads, hd), q.dtype, q, stream)
+    ks = (None, 0, 0, 0) if k is None else (_strided_ptr(k, "k"), k_heads, k.stride(0), k.stride(1))
+    ko = (None, 0, 0) if k is None else (_strided_ptr(k_out, "k_out"), k_out.stride(0), k_out.stride(1))
+    rc = lib().oq_qk_norm_rope(
+        _strided_ptr(q, "q"), q_heads, q.stride(0), q.stride(1), *ks, _element(q), tokens, hd,
+        None if q_weight is None else _ptr(q_weight, "q_weight"),
+        None if k_weight is None else _ptr(k_weight, "k_weight"),
+        OQ_F32 if first is None else _element(first), eps, _ptr(pos, "pos"), axes,
+        _C_INTS[axes](*axis_dims), theta, OQ_ROPE_HALF if half else 0, _strided_ptr(q_out, "q_out"),
+        q_out.stride(0), q_out.stride(1), *ko, _raw_stream(stream, dev))
+    _check(rc, "oq_qk_norm_rope")
+    return q_out, k_out
+
+
+def mx_kv_cache(pages, kv_heads, page_size, head_dim, *, device="cuda"):
+    """An empty (zero) 4-bit key/value cache: k_codes, k_scales, v_codes, v_scales,
+    uint8 [pages, kv_heads, page_size, head_dim / 2 and head_dim / 32]."""
+    torch = _torch()
+    if head_dim % 32:
+        raise ValueError(f"head_dim ({head_dim}) must be a multiple of 32")
+    shape = (pages, kv_heads, page_size)
+    return KVCache(*(torch.zeros((*shape, head_dim // w), dtype=torch.uint8, device=device)
+                     for w in (2, 32, 2, 32)))
+
+
+def _cache_shape(cache):
+    """(pages, kv_heads, page_size, head_dim) of a cache, whose arrays must agree."""
+    torch = _torch()
+    kc, ks, vc, vs = cache
+    if not isinstance(ks, torch.Tensor):
+        raise TypeError("cache must hold four torch.Tensors")
+    if ks.dim() != 4:
+        raise ValueError("the cache's arrays must be [pages, kv_heads, page_size, bytes]")
+    shape, nb = ks.shape[:3], ks.shape[3]
+    codes, scales = (*shape, 16 * nb), (*shape, nb)
+    for t, want, n in ((kc, codes, "k_codes"), (ks, scales, "k_scales"), (vc, codes, "v_codes"),
+                       (vs, scales, "v_scales")):
+        _shaped(t, want, torch.uint8, n)
+    if max(shape[1], shape[2], 32 * nb) > 2147483647:
+        for size, what in ((shape[1], "kv_heads"), (shape[2], "page_size"), (32 * nb, "head_dim")):
+            _fits(size, what)
+    return (*shape, 32 * nb)
+
+
+def mx_kv_write(k, v, slots, cache, *, stream=None):
+    """Quantize k and v [tokens, kv_heads, head_dim] (bfloat16 or float32, strided
+    as in rope) into the cache's slots int64 [tokens]: slot = page * page_size +
+    offset; a token with a negative slot, or one past the cache, is not written."""
+    pages, heads, page, hd = _cache_shape(cache)
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens, kv_heads, head_dim]")
+    tokens = k.shape[0]
+    _shaped(k, (tokens, heads, hd), k.dtype, "k")
+    _shaped(v, (tokens, heads, hd), k.dtype, "v")
+    _shaped(slots, (tokens,), _T.int64, "slots")
+    dev = _call_device((k, "k"), (v, "v"), (slots, "slots"), (cache[0], "k_codes"),
+                       (cache[1], "k_scales"), (cache[2], "v_codes"), (cache[3], "v_scales"))
+    rc = lib().oq_mx_kv_write(
+        _strided_ptr(k, "k"), _strided_ptr(v, "v"), _element(k), tokens, k.stride(0), k.stride(1),
+        v.stride(0), v.stride(1), _ptr(slots, "slots"), _ptr(cache[0], "k_codes"),
+        _ptr(cache[1], "k_scales"), _ptr(cache[2], "v_codes"), _ptr(cache[3], "v_scales"), pages,
+        heads, page, hd, _raw_stream(stream, dev))
+    _check(rc, "oq_mx_kv_write")
+
+
+def mx_kv_attention(q, cache, lengths, *, table=None, q_starts=None, scale=None, causal=False,
+                    window=0, out=None, lse=False, stream=None):
+    """Attention of q [tokens, q_heads, head_dim] (bfloat16 or float32, strided as
+    in rope) over the cached keys and values of each query's sequence.
+
+    lengths: int32 [batch], tokens that a sequence has in the cache (the new ones
+    among them); table: int32 [batch, pages a sequence], or None where sequence b
+    is page b; q_starts: int32 [batch + 1], sequence b's queries are
+    q[q_starts[b]:q_starts[b + 1]], or None where every sequence has as many.
+    Query i of n stands at position length - n + i; causal: it sees no later
+    token, with window > 0 only the last `window`.  A query that sees none gets
+    zeros.  scale: 1 / sqrt(head_dim) by default.  Returns out, or with lse=True
+    (or an fp32 tensor [tokens, q_heads] for it) (out, lse): the logarithm of each
+    row's sum of exponentials.  Rows behind the last sequence keep what out and
+    lse hold."""
+    pages, kv_heads, page, hd = _cache_shape(cache)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, q_heads, head_dim]")
+    tokens, q_heads, qd = q.shape
+    if qd != hd or kv_heads < 1 or q_heads % kv_heads:
+        raise ValueError(f"q has {q_heads} heads of {qd}, the cache {kv_heads} of {hd}")
+    _fits(q_heads, "q's heads")
+    _fits(abs(window), "window")
+    if not isinstance(lengths, _T.Tensor):
+        raise TypeError("lengths must be a torch.Tensor")
+    batch = lengths.numel()
+    _shaped(lengths, (batch,), _T.int32, "lengths")
+    width = 1
+    if table is not None:
+        width = table.shape[-1]
+        _shaped(table, (batch, width), _T.int32, "table")
+    elif pages < batch:
+        raise ValueError(f"{batch} sequences without a table need as many pages (got {pages})")
+    if q_starts is not None:
+        _shaped(q_starts, (batch + 1,), _T.int32, "q_starts")
+    elif batch and tokens % batch:
+        raise ValueError(f"{tokens} tokens do not split evenly over {batch} sequences: pass q_starts")
+    if out is not None:
+        _shaped(out, (tokens, q_heads, hd), q.dtype, "out")
+    want_lse = lse is not None and lse is not False
+    if want_lse and lse is not True:
+        _shaped(lse, (tokens, q_heads), _T.float32, "lse")
+    dev = _call_device((q, "q"), (cache[0], "k_codes"), (cache[1], "k_scales"),
+                       (cache[2], "v_codes"), (cache[3], "v_scales"), (lengths, "lengths"),
+                       (table, "table"), (q_starts, "q_starts"), (out, "out"),
+                       (lse if want_lse and lse is not True else None, "lse"))
+    if out is None:
+        out = _empty((tokens, q_heads, hd), q.dtype, q, stream)
+    if lse is True:
+        lse = _empty((tokens, q_heads), _T.float32, q, stream)
+    L = lib()
+    need = L.oq_mx_kv_attention_workspace(tokens, q_heads, kv_heads, hd, batch, page, width)
+    # of this call alone: the allocator hands it out again behind the call, in the stream's order
+    space = _empty((need,), _T.uint8, q, stream) if need > 0 else None
+    rc = L.oq_mx_kv_attention(
+        _strided_ptr(q, "q"), _element(q), tokens, q_heads, q.stride(0), q.stride(1),
+        _ptr(cache[0], "k_codes"), _ptr(cache[1], "k_scales"), _ptr(cache[2], "v_codes"),
+        _ptr(cache[3], "v_scales"), pages, kv_heads, page, hd, batch, _ptr(lengths, "lengths"),
+        None if q_starts is None else _ptr(q_starts, "q_starts"),
+        None if table is None else _ptr(table, "table"), width,
+        1.0 / math.sqrt(hd) if scale is None else scale, OQ_ATTN_CAUSAL if causal else 0, window,
+        _strided_ptr(out, "out"), out.stride(0), out.stride(1),
+        _ptr(lse, "lse") if want_lse else None, None if space is None else space.data_ptr(),
+        max(need, 0), _raw_stream(stream, dev))
+    _check(rc, "oq_mx_kv_attention")
+    return (out, lse) if want_lse else out
 
 
 def permute_rows(src, seed, *, out=None, stream=None):

@@ -583,7 +583,7 @@ const char *oq_strerror(int status) {
   switch (status) {
     case OQ_OK: return "success";
     case OQ_EINVAL: return "invalid argument (null or misaligned pointer, bad size, dtype or flag)";
-    case OQ_EUNSUPPORTED: return "unsupported configuration (d must be a multiple of 32 in [32, 16384], and the linear's K a multiple of 64; bits in {2,3,4,8}; 8 bits on both sides of a linear; the sphere codebook at 1-4 and 8 bits; the MX calls at up to 2^30 rows; the rotary embedding at head_dim a multiple of 8 up to 512, up to 4 axes, a multiple of 16 turned elements in halves)";
+    case OQ_EUNSUPPORTED: return "unsupported configuration (d must be a multiple of 32 in [32, 16384], and the linear's K a multiple of 64; bits in {2,3,4,8}; 8 bits on both sides of a linear; the sphere codebook at 1-4 and 8 bits; the MX calls at up to 2^30 rows; the rotary embedding at head_dim a multiple of 8 up to 512, up to 4 axes, a multiple of 16 turned elements in halves; group scales for a multiple of 32 coordinates; a cache's head_dim a multiple of 32 up to 256)";
     case OQ_ENOMEM: return "out of device memory for the rotation plan";
     case OQ_EDEVICE: return "HIP runtime or kernel launch failure";
     default: return "unknown status";
@@ -999,6 +999,292 @@ int oq_rope(const void *x, int dtype, int64_t tokens, int heads, int head_dim, i
   a.stream = (hipStream_t)stream;
   oq::rope_rates(theta, axes, axis_dims, a.freq, a.axis);
   hipError_t e = oq::launch_rope(a);
+  return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
+}
+
+// ---------------------------------------------- the cached-attention path --
+
+namespace {
+
+bool is_dtype(int dtype) { return dtype == OQ_F32 || dtype == OQ_BF16; }
+
+struct Span {
+  const void *p;
+  int64_t bytes;
+};
+
+bool meets(const Span &a, const Span &b) { return a.p && b.p && overlaps(a.p, a.bytes, b.p, b.bytes); }
+
+// A strided [tokens][heads][head_dim] array: its span, or bytes = -1 where a
+// stride or the address does not fit.  `write`: its elements need addresses of
+// their own (each head whole, heads inside tokens or tokens inside heads).
+Span heads_span(const void *p, int64_t tokens, int64_t &token, int heads, int64_t &head, int head_dim,
+                int size, bool write) {
+  if (!p || token < 0 || head < 0) return {p, -1};
+  if (tokens == 1) token = 0;  // the stride of a single one is not used
+  if (heads == 1) head = 0;
+  const int unit = 16 / size;
+  if (!aligned(p, 16) || token % unit || head % unit) return {p, -1};
+  if (write) {
+    const bool by_token = (heads == 1 || head >= head_dim) &&
+                          (tokens == 1 || (__int128)(heads - 1) * head + head_dim <= token);
+    const bool by_head = (tokens == 1 || token >= head_dim) &&
+                         (heads == 1 || (__int128)(tokens - 1) * token + head_dim <= head);
+    if (!by_token && !by_head) return {p, -1};
+  }
+  return {p, span_bytes(tokens, token, heads, head, head_dim, size)};
+}
+
+int check_group(int64_t N, int K, int group, int scale_dtype) {
+  if (N < 0 || K <= 0 || group <= 0 || !is_dtype(scale_dtype)) return OQ_EINVAL;
+  if (K % group != 0) return OQ_EINVAL;
+  if (group % 32 != 0 || K > 16384 || N > kMaxRows) return OQ_EUNSUPPORTED;
+  return OQ_OK;
+}
+
+// the sizes of a cache, and its four arrays where they are given
+int check_cache_shape(int64_t pages, int kv_heads, int page_size, int head_dim) {
+  if (pages < 0 || kv_heads <= 0 || page_size <= 0 || head_dim <= 0) return OQ_EINVAL;
+  if (head_dim % oq::kMxBlock != 0 || head_dim > oq::kKvMaxHeadDim || kv_heads > oq::kKvMaxHeads)
+    return OQ_EUNSUPPORTED;
+  const __int128 n = (__int128)pages * kv_heads * page_size;
+  return n > ((int64_t)1 << 48) ? OQ_EUNSUPPORTED : OQ_OK;
+}
+
+bool cache_spans(const oq::KvCache &c, Span out[4]) {
+  const int64_t rows = c.pages * c.heads * c.page;
+  out[0] = {c.k_codes, rows * (c.head_dim / 2)};
+  out[1] = {c.k_scales, rows * (c.head_dim / oq::kMxBlock)};
+  out[2] = {c.v_codes, rows * (c.head_dim / 2)};
+  out[3] = {c.v_scales, rows * (c.head_dim / oq::kMxBlock)};
+  for (int i = 0; i < 4; i++)
+    if (!out[i].p || !aligned(out[i].p, 16)) return false;
+  return true;
+}
+
+// the sizes that decide an attention call's grid and workspace
+int check_attention_shape(int64_t q_tokens, int q_heads, int kv_heads, int head_dim, int64_t batch,
+                          int page_size, int64_t table_pages) {
+  if (q_tokens < 0 || batch < 0 || table_pages < 1 || q_heads <= 0) return OQ_EINVAL;
+  const int rc = check_cache_shape(0, kv_heads, page_size, head_dim);
+  if (rc != OQ_OK) return rc;
+  if (q_heads % kv_heads != 0) return OQ_EINVAL;
+  if (batch > oq::kKvMaxBatch || (__int128)table_pages * page_size > oq::kKvMaxLength ||
+      q_tokens > oq::kKvMaxRows || q_tokens * (q_heads / kv_heads) > oq::kKvMaxRows)
+    return OQ_EUNSUPPORTED;
+  return OQ_OK;
+}
+
+}  // namespace
+
+int oq_rtn4_group_prepare_weights(const void *W, int dtype, int64_t n_out, int d_in, int group,
+                                  uint8_t *q4, void *scales, void *zeros, int scale_dtype,
+                                  void *stream) {
+  if (!is_dtype(dtype)) return OQ_EINVAL;
+  const int rc = check_group(n_out, d_in, group, scale_dtype);
+  if (rc != OQ_OK) return rc;
+  if (n_out == 0) return OQ_OK;
+  if (!W || !q4 || !scales) return OQ_EINVAL;
+  if (!aligned(W, 4) || !aligned(q4, 16) || !aligned(scales, 4) || !aligned(zeros, 4)) return OQ_EINVAL;
+  const int64_t sb = n_out * (d_in / group) * elem_bytes(scale_dtype);
+  const Span s[] = {{W, n_out * d_in * elem_bytes(dtype)}, {q4, n_out * d_in / 2}, {scales, sb}, {zeros, sb}};
+  for (int i = 0; i < 4; i++)
+    for (int j = i + 1; j < 4; j++)
+      if (meets(s[i], s[j])) return OQ_EINVAL;
+  hipError_t e = oq::launch_rtn4_group_prepare(W, dtype, n_out, d_in, group, q4, scales, zeros,
+                                               scale_dtype, (hipStream_t)stream);
+  return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
+}
+
+int oq_rtn4_group_linear(const void *x, int dtype, int64_t M, const uint8_t *q4,
+                         const void *scales, const void *zeros, int scale_dtype, int group,
+                         int64_t N, int K, uint16_t *y, void *stream) {
+  if (M < 0 || !is_dtype(dtype)) return OQ_EINVAL;
+  const int rc = check_group(N, K, group, scale_dtype);
+  if (rc != OQ_OK) return rc;
+  if (M > kMaxRows) return OQ_EUNSUPPORTED;
+  if (M == 0 || N == 0) return OQ_OK;
+  if (!x || !q4 || !scales || !y) return OQ_EINVAL;
+  if (!aligned(x, 16) || !aligned(q4, 16) || !aligned(scales, 4) || !aligned(zeros, 4) || !aligned(y, 2))
+    return OQ_EINVAL;
+  const int64_t sb = N * (K / group) * elem_bytes(scale_dtype);
+  const Span out = {y, M * N * 2};
+  for (const Span &in : {Span{x, M * K * elem_bytes(dtype)}, Span{q4, N * K / 2}, Span{scales, sb}, Span{zeros, sb}})
+    if (meets(out, in)) return OQ_EINVAL;
+  const oq::Rtn4GroupArgs a{x, dtype, M, q4, scales, zeros, scale_dtype, group, N, K, y,
+                            (hipStream_t)stream};
+  hipError_t e = oq::launch_rtn4_group_linear(a);
+  return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
+}
+
+int oq_qk_norm_rope(const void *q, int q_heads, int64_t q_token, int64_t q_head, const void *k,
+                    int k_heads, int64_t k_token, int64_t k_head, int dtype, int64_t tokens,
+                    int head_dim, const void *q_weight, const void *k_weight, int param_dtype,
+                    float eps, const int32_t *pos, int axes, const int *axis_dims, double theta,
+                    uint32_t flags, void *q_out, int64_t q_out_token, int64_t q_out_head,
+                    void *k_out, int64_t k_out_token, int64_t k_out_head, void *stream) {
+  if (!is_dtype(dtype) || !is_dtype(param_dtype) || (flags & ~OQ_ROPE_HALF)) return OQ_EINVAL;
+  if (!(eps >= std::numeric_limits<float>::min()) || !std::isfinite(eps)) return OQ_EINVAL;
+  if (tokens < 0 || q_heads < 0 || k_heads < 0 || head_dim <= 0 || axes < 1 || !axis_dims) return OQ_EINVAL;
+  if (!(theta >= 1.0) || !std::isfinite(theta)) return OQ_EINVAL;
+  if (head_dim % 8 != 0 || head_dim > oq::kRopeMaxHeadDim || axes > oq::kRopeMaxAxes)
+    return OQ_EUNSUPPORTED;
+  int64_t turned = 0;
+  for (int i = 0; i < axes; i++) {
+    if (axis_dims[i] < 0 || axis_dims[i] % 2 != 0) return OQ_EINVAL;
+    turned += axis_dims[i];
+  }
+  if (turned > head_dim) return OQ_EINVAL;
+  const bool half = (flags & OQ_ROPE_HALF) != 0;
+  if (half && turned % 16 != 0) return OQ_EUNSUPPORTED;
+  if (tokens > kMaxRows || (int64_t)q_heads + k_heads > 1 << 24) return OQ_EUNSUPPORTED;
+  if (tokens == 0 || (q_heads == 0 && k_heads == 0)) return OQ_OK;
+  if (!pos || !aligned(pos, 4) || !aligned(q_weight, 16) || !aligned(k_weight, 16)) return OQ_EINVAL;
+  const int size = elem_bytes(dtype);
+  oq::QkNormRopeArgs a{};
+  a.side[0] = {q, q_out, q_weight, q_token, q_head, q_out_token, q_out_head, q_heads};
+  a.side[1] = {k, k_out, k_weight, k_token, k_head, k_out_token, k_out_head, k_heads};
+  Span in[2] = {}, out[2] = {};
+  bool in_place[2] = {};
+  for (int i = 0; i < 2; i++) {
+    auto &s = a.side[i];
+    if (s.heads == 0) continue;
+    in[i] = heads_span(s.x, tokens, s.x_token, s.heads, s.x_head, head_dim, size, false);
+    out[i] = heads_span(s.y, tokens, s.y_token, s.heads, s.y_head, head_dim, size, true);
+    if (in[i].bytes < 0 || out[i].bytes < 0) return OQ_EINVAL;
+    in_place[i] = s.x == s.y && s.x_token == s.y_token && s.x_head == s.y_head;
+  }
+  const int64_t wb = (int64_t)head_dim * elem_bytes(param_dtype);
+  // Queries and keys are slices of one projection more often than not: their
+  // spans interleave without meeting, and so do two outputs.
+  const auto apart = [&](const Span &s, int64_t s_token, int64_t s_head, int s_heads, const Span &t,
+                         int64_t t_token, int64_t t_head, int t_heads) {
+    if (!meets(s, t)) return true;
+    const int64_t d = ((const char *)t.p - (const char *)s.p) / size;
+    if (s_token != t_token) return false;
+    // heads by turns, [tokens][heads][2 or more][head_dim]: apart within a head's stride
+    if (s_head == t_head && s_head > 0 && s_token % s_head == 0) {
+      const int64_t r = (d % s_head + s_head) % s_head;
+      if (r >= head_dim && r + head_dim <= s_head) return true;
+    }
+    if (s_token == 0) return false;
+    // the same token stride: a token's heads of one beside the other's, neither
+    // past the stride
+    const __int128 sw = (__int128)(s_heads - 1) * s_head + head_dim, tw = (__int128)(t_heads - 1) * t_head + head_dim;
+    return d >= 0 ? sw <= d && d + tw <= s_token : tw <= -d && -d + sw <= s_token;
+  };
+  for (int i = 0; i < 2; i++) {
+    if (!out[i].p) continue;
+    const auto &o = a.side[i];
+    for (int j = 0; j < 2; j++) {
+      const auto &s = a.side[j];
+      if (in[j].p && !(i == j && in_place[i]) &&
+          !apart(out[i], o.y_token, o.y_head, o.heads, in[j], s.x_token, s.x_head, s.heads))
+        return OQ_EINVAL;
+    }
+    for (const Span &p : {Span{pos, tokens * axes * 4}, Span{q_weight, wb}, Span{k_weight, wb}})
+      if (meets(out[i], p)) return OQ_EINVAL;
+  }
+  if (out[0].p && out[1].p &&
+      !apart(out[0], a.side[0].y_token, a.side[0].y_head, q_heads, out[1], a.side[1].y_token,
+             a.side[1].y_head, k_heads))
+    return OQ_EINVAL;
+  a.dtype = dtype;
+  a.param_dtype = param_dtype;
+  a.tokens = tokens;
+  a.head_dim = head_dim;
+  a.turned = (int)turned;
+  a.eps = eps;
+  a.pos = pos;
+  a.axes = axes;
+  a.half = half;
+  a.stream = (hipStream_t)stream;
+  oq::rope_rates(theta, axes, axis_dims, a.freq, a.axis);
+  hipError_t e = oq::launch_qk_norm_rope(a);
+  return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
+}
+
+int oq_mx_kv_write(const void *k, const void *v, int dtype, int64_t tokens, int64_t k_token,
+                   int64_t k_head, int64_t v_token, int64_t v_head, const int64_t *slots,
+                   uint8_t *k_codes, uint8_t *k_scales, uint8_t *v_codes, uint8_t *v_scales,
+                   int64_t pages, int kv_heads, int page_size, int head_dim, void *stream) {
+  if (!is_dtype(dtype) || tokens < 0) return OQ_EINVAL;
+  const int rc = check_cache_shape(pages, kv_heads, page_size, head_dim);
+  if (rc != OQ_OK) return rc;
+  if (tokens > kMaxRows) return OQ_EUNSUPPORTED;
+  if (tokens == 0 || pages == 0) return OQ_OK;
+  const oq::KvCache c{k_codes, k_scales, v_codes, v_scales, pages, kv_heads, page_size, head_dim};
+  Span cache[4];
+  if (!cache_spans(c, cache) || !slots || !aligned(slots, 8)) return OQ_EINVAL;
+  const int size = elem_bytes(dtype);
+  const Span ks = heads_span(k, tokens, k_token, kv_heads, k_head, head_dim, size, false);
+  const Span vs = heads_span(v, tokens, v_token, kv_heads, v_head, head_dim, size, false);
+  if (ks.bytes < 0 || vs.bytes < 0) return OQ_EINVAL;
+  const Span ss = {slots, tokens * 8};
+  for (int i = 0; i < 4; i++) {
+    if (meets(cache[i], ks) || meets(cache[i], vs) || meets(cache[i], ss)) return OQ_EINVAL;
+    for (int j = i + 1; j < 4; j++)
+      if (meets(cache[i], cache[j])) return OQ_EINVAL;
+  }
+  const oq::KvWriteArgs a{k, v, dtype, tokens, k_token, k_head, v_token, v_head, slots, c,
+                          (hipStream_t)stream};
+  hipError_t e = oq::launch_kv_write(a);
+  return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
+}
+
+int64_t oq_mx_kv_attention_workspace(int64_t q_tokens, int q_heads, int kv_heads, int head_dim,
+                                     int64_t batch, int page_size, int64_t table_pages) {
+  if (check_attention_shape(q_tokens, q_heads, kv_heads, head_dim, batch, page_size, table_pages) != OQ_OK)
+    return -1;
+  if (q_tokens == 0 || batch == 0) return 0;
+  return oq::kv_attention_workspace(q_tokens, q_heads, kv_heads, head_dim, batch, table_pages * page_size);
+}
+
+int oq_mx_kv_attention(const void *q, int dtype, int64_t q_tokens, int q_heads, int64_t q_token,
+                       int64_t q_head, const uint8_t *k_codes, const uint8_t *k_scales,
+                       const uint8_t *v_codes, const uint8_t *v_scales, int64_t pages,
+                       int kv_heads, int page_size, int head_dim, int64_t batch,
+                       const int32_t *lengths, const int32_t *q_starts, const int32_t *table,
+                       int64_t table_pages, float scale, uint32_t flags, int window, void *out,
+                       int64_t out_token, int64_t out_head, float *lse, void *workspace,
+                       int64_t workspace_bytes, void *stream) {
+  if (!is_dtype(dtype) || (flags & ~OQ_ATTN_CAUSAL) || !std::isfinite(scale)) return OQ_EINVAL;
+  const bool causal = (flags & OQ_ATTN_CAUSAL) != 0;
+  if (window < 0 || (window > 0 && !causal)) return OQ_EINVAL;
+  int rc = check_attention_shape(q_tokens, q_heads, kv_heads, head_dim, batch, page_size, table_pages);
+  if (rc != OQ_OK) return rc;
+  rc = check_cache_shape(pages, kv_heads, page_size, head_dim);
+  if (rc != OQ_OK) return rc;
+  if (q_tokens == 0 || batch == 0) return OQ_OK;
+  if (!q_starts && q_tokens % batch != 0) return OQ_EINVAL;
+  if (!table && (table_pages != 1 || pages < batch)) return OQ_EINVAL;
+  if (pages == 0) return OQ_EINVAL;
+  const oq::KvCache c{(uint8_t *)k_codes, (uint8_t *)k_scales, (uint8_t *)v_codes, (uint8_t *)v_scales,
+                      pages, kv_heads, page_size, head_dim};
+  Span cache[4];
+  if (!cache_spans(c, cache) || !lengths || !aligned(lengths, 4) || !aligned(q_starts, 4) ||
+      !aligned(table, 4) || !aligned(lse, 4) || !aligned(workspace, 16))
+    return OQ_EINVAL;
+  const int64_t need = oq::kv_attention_workspace(q_tokens, q_heads, kv_heads, head_dim, batch,
+                                                  table_pages * page_size);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return OQ_EINVAL;
+  const int size = elem_bytes(dtype);
+  const Span qs = heads_span(q, q_tokens, q_token, q_heads, q_head, head_dim, size, false);
+  const Span os = heads_span(out, q_tokens, out_token, q_heads, out_head, head_dim, size, true);
+  if (qs.bytes < 0 || os.bytes < 0) return OQ_EINVAL;
+  const Span ins[] = {qs, cache[0], cache[1], cache[2], cache[3], {lengths, batch * 4},
+                      {q_starts, (batch + 1) * 4}, {table, batch * table_pages * 4}};
+  const Span outs[] = {os, {lse, q_tokens * q_heads * 4}, {need > 0 ? workspace : nullptr, need}};
+  for (int i = 0; i < 3; i++) {
+    for (const Span &s : ins)
+      if (meets(outs[i], s)) return OQ_EINVAL;
+    for (int j = i + 1; j < 3; j++)
+      if (meets(outs[i], outs[j])) return OQ_EINVAL;
+  }
+  const oq::KvAttentionArgs a{q, dtype, q_tokens, q_token, q_head, q_heads, c, (int)batch, lengths,
+                              q_starts, table, (int)table_pages, scale, causal, window, out,
+                              out_token, out_head, lse, workspace, (hipStream_t)stream};
+  hipError_t e = oq::launch_kv_attention(a);
   return e == hipSuccess ? OQ_OK : OQ_EDEVICE;
 }
 

@@ -202,4 +202,85 @@ struct RopeArgs {
 };
 hipError_t launch_rope(const RopeArgs &a);
 
+// INT4 weights with group scales and, where zeros is not null, zero points
+hipError_t launch_rtn4_group_prepare(const void *W, int dtype, int64_t rows, int d, int group,
+                                     uint8_t *q4, void *scales, void *zeros, int scale_dtype,
+                                     hipStream_t stream);
+struct Rtn4GroupArgs {
+  const void *x;
+  int dtype;
+  int64_t M;
+  const uint8_t *q4;
+  const void *scales, *zeros;  // zeros may be null
+  int scale_dtype, group;
+  int64_t N;
+  int K;
+  uint16_t *y;
+  hipStream_t stream;
+};
+hipError_t launch_rtn4_group_linear(const Rtn4GroupArgs &a);
+
+struct QkNormRopeArgs {
+  struct Side {  // queries or keys
+    const void *x;
+    void *y;
+    const void *weight;  // may be null
+    int64_t x_token, x_head, y_token, y_head;
+    int heads;
+  } side[2];
+  int dtype, param_dtype;
+  int64_t tokens;
+  int head_dim, turned;
+  float eps;
+  const int32_t *pos;
+  int axes;
+  bool half;
+  hipStream_t stream;
+  uint64_t freq[kRopeMaxHeadDim / 2];
+  uint8_t axis[kRopeMaxHeadDim / 2];
+};
+hipError_t launch_qk_norm_rope(const QkNormRopeArgs &a);
+
+// The 4-bit key/value cache: [pages][heads][page][head_dim / 2] codes and
+// [pages][heads][page][head_dim / 32] scale bytes.
+constexpr int kKvMaxHeadDim = 256, kKvMaxHeads = 65535;
+constexpr int64_t kKvMaxRows = (int64_t)1 << 28, kKvMaxBatch = (int64_t)1 << 20,
+                  kKvMaxLength = (int64_t)1 << 30;
+struct KvCache {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  int64_t pages;
+  int heads, page, head_dim;
+};
+struct KvWriteArgs {
+  const void *k, *v;
+  int dtype;
+  int64_t tokens, k_token, k_head, v_token, v_head;
+  const int64_t *slots;
+  KvCache cache;
+  hipStream_t stream;
+};
+hipError_t launch_kv_write(const KvWriteArgs &a);
+
+struct KvAttentionArgs {
+  const void *q;
+  int dtype;
+  int64_t q_tokens, q_token, q_head;
+  int q_heads;
+  KvCache cache;
+  int batch;
+  const int32_t *lengths, *q_starts, *table;  // q_starts and table may be null
+  int table_pages;
+  float scale;
+  bool causal;
+  int window;
+  void *out;
+  int64_t out_token, out_head;
+  float *lse;  // may be null
+  void *workspace;
+  hipStream_t stream;
+};
+int64_t kv_attention_workspace(int64_t q_tokens, int q_heads, int kv_heads, int head_dim,
+                               int64_t batch, int64_t capacity);
+hipError_t launch_kv_attention(const KvAttentionArgs &a);
+
 }  // namespace oq

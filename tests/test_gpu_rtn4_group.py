@@ -1,0 +1,160 @@
+"""INT4 weights with group scales on the GPU against plain forms.
+
+The projection's tolerance, u = 2^-24: every order of summing K products is off
+by at most K u of the sum of magnitudes S = sum |s| |x| (|nibble - 8| + |8 - z|)
+(an implementation may take the zero point apart from the nibbles), the scale,
+the zero point and a split of x by 8 u more; then half a step of bf16.  A
+row's error over all outputs also has to be what that last rounding gives."""
+import numpy as np
+import pytest
+
+from tests import kv_ref as ref
+from tests.gpu_util import bf16_to_np, host, say, to_device
+import workloads as wl
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q():
+    import torch
+    import quantization_dit_linear_amd as q
+    assert torch.cuda.is_available()
+    q.lib()
+    return q
+
+
+def _np(t):
+    import torch
+    return bf16_to_np(t) if t.dtype == torch.bfloat16 else host(t).astype(np.float64)
+
+
+def _dev(a, bf16):
+    return to_device(wl.f32_to_bf16_bits(a) if bf16 else a.astype(np.float32))
+
+
+def _weights(rng, N, K, group, zeros, scale_bf16):
+    q4 = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+    s = (0.01 * np.exp(rng.standard_normal((N, K // group)))).astype(np.float32)
+    z = rng.uniform(0, 15, s.shape).astype(np.float32) if zeros else None
+    s, z = (None if a is None else _dev(a, scale_bf16) for a in (s, z))
+    return q4, s, z
+
+
+def _check(y, x, q4, s, z, group):
+    w, mag = ref.group_weights(q4, _np(s), None if z is None else _np(z), group)
+    want, e = x @ w.T, (np.abs(x) @ mag.T) * (x.shape[1] + 8) * ref.U
+    tol = e + 2.0 ** -8 * (np.abs(want) + e)
+    assert np.all(np.abs(y - want) <= tol), float(np.max(np.abs(y - want) / np.maximum(tol, 1e-300)))
+    assert np.linalg.norm(y - want) <= 2.0 ** -8 * np.linalg.norm(want) + np.linalg.norm(e)
+
+
+SHAPES = [(1, 1, 32, 32), (1, 16, 64, 64), (1, 17, 96, 32), (2, 100, 1024, 128), (3, 5, 480, 96),
+          (4, 257, 512, 512), (5, 33, 2048, 64), (8, 64, 256, 128), (9, 31, 160, 160), (16, 129, 1536, 64),
+          (17, 48, 640, 128), (31, 130, 320, 32), (33, 15, 224, 224), (64, 66, 512, 64), (65, 16, 128, 32),
+          (130, 40, 384, 128), (1, 515, 5120, 128), (2, 20, 16384, 16384), (7, 9, 16384, 64)]
+
+
+@pytest.mark.parametrize("zeros", [False, True], ids=["sym", "zeros"])
+@pytest.mark.parametrize("scale_bf16", [False, True], ids=["s32", "s16"])
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("M,N,K,group", SHAPES)
+def test_linear(q, M, N, K, group, bf16, scale_bf16, zeros):
+    say("rtn4 group linear", M, N, K, group, bf16, scale_bf16, zeros)
+    rng = np.random.default_rng([M, N, K, group])
+    x = rng.standard_normal((M, K)).astype(np.float32)
+    x[:, rng.integers(0, K, max(1, K // 100))] *= 100.0
+    q4, s, z = _weights(rng, N, K, group, zeros, scale_bf16)
+    xd = _dev(x, bf16)
+    y = q.rtn4_group_linear(xd, to_device(q4), s, z)
+    _check(_np(y), _np(xd), q4, s, z, group)
+
+
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("M", [1, 12, 40])
+def test_wide_ranges(q, M, bf16):
+    """Activations from 2^-60 to 2^60 side by side, groups of zeros, subnormals
+    and the largest numbers: the sums keep what an fp32 sum keeps."""
+    say("rtn4 group ranges", M, bf16)
+    rng, N, K = np.random.default_rng(M), 48, 256
+    x = (rng.standard_normal((M, K)) * 2.0 ** rng.integers(-60, 60, (M, K))).astype(np.float32)
+    x[:, 32:64] = 0
+    x[0, 64:96] = 2.0 ** -140
+    x[-1, 96:128] = rng.standard_normal(32) * 2.0 ** 100
+    q4, s, _ = _weights(rng, N, K, 32, False, False)
+    xd = _dev(x, bf16)
+    y = q.rtn4_group_linear(xd, to_device(q4), s)
+    _check(_np(y), _np(xd), q4, s, None, 32)
+
+
+@pytest.mark.parametrize("M", [1, 3, 20])
+def test_not_finite(q, M):
+    """A row with a NaN or an infinity does not reach the others."""
+    import torch
+    say("rtn4 group not finite", M)
+    rng, N, K = np.random.default_rng(M), 33, 128
+    x = rng.standard_normal((M + 2, K)).astype(np.float32)
+    x[0, 5], x[M + 1, 77] = np.nan, np.inf
+    q4, s, _ = _weights(rng, N, K, 64, False, True)
+    xd = _dev(x, True)
+    y = q.rtn4_group_linear(xd, to_device(q4), s)
+    assert torch.isnan(y[0]).all() and not torch.isfinite(y[-1]).any()
+    _check(_np(y)[1:-1], _np(xd)[1:-1], q4, s, None, 64)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("scale_bf16", [False, True], ids=["s32", "s16"])
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("N,K,group", [(1, 32, 32), (7, 192, 96), (33, 512, 64), (5, 1024, 1024), (64, 256, 32)])
+def test_prepare(q, N, K, group, bf16, scale_bf16, zeros):
+    """Bit for bit the definition's fp32 operations (numpy's are IEEE's)."""
+    import torch
+    say("rtn4 group prepare", N, K, group, bf16, scale_bf16, zeros)
+    rng = np.random.default_rng([N, K, group])
+    W = rng.standard_normal((N, K)).astype(np.float32)
+    W[0, :32] = 0
+    W[-1] = np.abs(W[-1])
+    if bf16:
+        W = wl.bf16_bits_to_f32(wl.f32_to_bf16_bits(W))
+    got = q.rtn4_group_prepare_weights(_dev(W, bf16), group, zeros=zeros,
+                                       scale_dtype=torch.bfloat16 if scale_bf16 else torch.float32)
+    g = W.reshape(N, -1, group)
+    hi, lo = np.maximum(g.max(-1), 0), np.minimum(g.min(-1), 0)
+    s = hi / np.float32(15) - lo / np.float32(15) if zeros else np.abs(g).max(-1) / np.float32(7)
+    if scale_bf16:
+        s = wl.bf16_bits_to_f32(wl.f32_to_bf16_bits(s))
+    div = np.where(s > 0, s, np.float32(1))
+    z = np.where(s > 0, np.clip(np.rint(-lo / div), 0, 15), 0) if zeros else np.full_like(s, 8)
+    n = np.clip(np.where(s[..., None] > 0, np.rint(g / div[..., None]), 0) + z[..., None], 0, 15)
+    n = n.astype(np.uint8).reshape(N, K)
+    np.testing.assert_array_equal(host(got[0]), n[:, 0::2] | (n[:, 1::2] << 4))
+    np.testing.assert_array_equal(_np(got[1]), s.astype(np.float64))
+    if zeros:
+        np.testing.assert_array_equal(_np(got[2]), z.astype(np.float64))
+    x = rng.standard_normal((3, K)).astype(np.float32)
+    y = q.rtn4_group_linear(_dev(x, False), *got)
+    _check(_np(y), x.astype(np.float64), host(got[0]), got[1], got[2] if zeros else None, group)
+
+
+def test_graph_and_stream(q):
+    """Captured once and replayed over changing inputs, and on another stream."""
+    import torch
+    say("rtn4 group graph")
+    rng, M, N, K = np.random.default_rng(0), 3, 200, 1024
+    q4, s, z = _weights(rng, N, K, 128, True, True)
+    q4d, x = to_device(q4), torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    q.rtn4_group_linear(x, q4d, s, z, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.rtn4_group_linear(x, q4d, s, z, out=out)
+    for i in range(3):
+        x.copy_(torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32)))
+        g.replay()
+        assert torch.equal(out, q.rtn4_group_linear(x, q4d, s, z))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = q.rtn4_group_linear(x, q4d, s, z, stream=side)
+    side.synchronize()
+    assert torch.equal(out, y)
