@@ -487,7 +487,7 @@ int64_t oq_mx_kv_attention_workspace(int64_t q_tokens, int q_heads, int kv_heads
  * see do not reach it.  Scale bytes 253 to 255 read as NaN here (the writer
  * makes none but 255), and values below 2^-126 may count as 0.
  * A call gives the same bits every time; the order of a row's sums is chosen by
- * the sizes.  q_tokens * q_heads / kv_heads up to 2^28, batch up to 2^20,
+ * the sizes.  q_tokens * q_heads / kv_heads up to 2^27, batch up to 2^20,
  * table_pages * page_size up to 2^30.  q_tokens = 0 or batch = 0 no-op.
  * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
 int oq_mx_kv_attention(const void *q, int dtype, int64_t q_tokens, int q_heads, int64_t q_token,

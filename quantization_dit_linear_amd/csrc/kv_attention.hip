@@ -1,136 +1,101 @@
-// kv_attention.hip -- attention of new queries over the 4-bit key/value cache.
+// kv_attention.hip -- attention of new queries over the 4-bit key/value cache:
+// which kernel takes a call, in how many parts, and the join of the parts.
 //
-//   out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q k_j - m),  lse = m + ln sum_j p_j
-// in one pass over the tokens with a running maximum m.
+//   out = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c q k_j - m),  lse = (m + log2 sum_j p_j) ln 2
+// with c = scale log2 e and m the running maximum of a row's c q k_j.
 #include <hip/hip_runtime.h>
 
-#include "kv_cache.h"
-#include "mx_codec.h"
-#include "oq_internal.h"
+#include <algorithm>
+#include <limits>
+
+#include "kv_attention.h"
 
 namespace oq {
 namespace {
 
-constexpr float kInf = __builtin_huge_valf();
-
-// A scale byte as attention reads it: 253 and more are NaN.
-__device__ __forceinline__ float kv_scale(uint32_t s) { return mx_scale(s >= 253 ? 255 : s); }
-
-__device__ __forceinline__ float fp4(uint32_t nibble) {
-  return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(nibble, 1.0f, 0)[0];
+// A row's parts, in their order: four elements a thread.
+template <class T>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvLaunch p) {
+  const KvAttentionArgs &a = p.a;
+  const KvTile t = find_tile(p, blockIdx.x);
+  if (t.b < 0) return;
+  const int hd = a.cache.head_dim, q4 = hd / 4;
+  const int64_t total = a.q_tokens * a.q_heads;
+  const int rows = t.rows - t.row0 < p.rows ? t.rows - t.row0 : p.rows;
+  for (int e = threadIdx.x; e < rows * q4; e += 256) {
+    uint32_t i, h;
+    const int r = e / q4, d = 4 * (e - r * q4);
+    p.share.split((uint32_t)(t.row0 + r), i, h);
+    const int64_t tok = t.start + (int64_t)i, head = (int64_t)blockIdx.y * p.share.d + h;
+    const int64_t row = tok * a.q_heads + head;
+    float top = -kInf, sum = 0.f;
+    for (int s = 0; s < p.splits; s++) top = fmaxf(top, p.part_ml[s * total + row][0]);
+    const float base = top == -kInf ? 0.f : top;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < p.splits; s++) {
+      const f32x2 ml = p.part_ml[s * total + row];
+      if (ml[1] == 0.f) continue;  // a part that saw nothing left no sum
+      const float f = __builtin_amdgcn_exp2f(ml[0] - base);
+      sum += ml[1] * f;
+      v += *(const f32x4 *)(p.part + (s * total + row) * hd + d) * f;
+    }
+    if (sum == 0.f) v = f32x4{0.f, 0.f, 0.f, 0.f};
+    else v *= 1.f / sum;
+    store4((T *)a.out + tok * a.out_token + head * a.out_head + d, v);
+    if (a.lse && d == 0) a.lse[row] = lse_of(top, sum);
+  }
 }
 
-// One wave a query head: 64 tokens a step, a token a lane for the scores, an
-// element a lane for the sum.
-template <class T>
-__global__ __launch_bounds__(64) void kv_attention_kernel(KvAttentionArgs a, FastDiv page) {
-  __shared__ float qs[kKvMaxHeadDim], ps[64];
-  __shared__ int64_t rows[64];
-  const KvCache &c = a.cache;
-  const int lane = threadIdx.x, hd = c.head_dim, nb = hd / 32, share = a.q_heads / c.heads;
-  const int64_t cap = (int64_t)a.table_pages * c.page;
-  for (int64_t r = blockIdx.x; r < a.q_tokens * a.q_heads; r += gridDim.x) {
-    const int64_t tok = r / a.q_heads;
-    const int h = (int)(r - tok * a.q_heads), kh = h / share;
-    // the sequence: the last whose start is not behind the token
-    int b, i, n;
-    if (a.q_starts) {
-      int lo = 0, hi = a.batch;
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (a.q_starts[mid] <= tok) lo = mid + 1;
-        else hi = mid;
-      }
-      b = lo - 1;
-      if (b < 0 || tok >= a.q_starts[b + 1]) continue;
-      i = (int)(tok - a.q_starts[b]), n = a.q_starts[b + 1] - a.q_starts[b];
-    } else {
-      n = (int)(a.q_tokens / a.batch);
-      b = (int)(tok / n), i = (int)(tok - (int64_t)b * n);
-    }
-    int64_t len = a.lengths[b];
-    len = len < 0 ? 0 : len > cap ? cap : len;
-    const int64_t at = len - n + i;
-    int64_t hi = a.causal && at + 1 < len ? at + 1 : len, lo = a.window && at + 1 > a.window ? at + 1 - a.window : 0;
-    const T *q = (const T *)a.q + tok * a.q_token + h * a.q_head;
-    __syncthreads();
-    for (int e = lane; e < hd; e += 64) {
-      if constexpr (sizeof(T) == 2) qs[e] = __builtin_bit_cast(float, (uint32_t)q[e] << 16);
-      else qs[e] = q[e];
-    }
-    float m = -kInf, l = 0.f, acc[kKvMaxHeadDim / 64] = {};
-    for (int64_t t0 = lo; t0 < hi; t0 += 64) {
-      __syncthreads();
-      const int64_t t = t0 + lane;
-      float s = -kInf;
-      if (t < hi) {
-        uint32_t p, off;
-        page.split((uint32_t)t, p, off);
-        const int64_t pg = a.table ? a.table[(int64_t)b * a.table_pages + p] : b;
-        const bool bad = pg < 0 || pg >= c.pages;
-        const int64_t row = ((bad ? 0 : pg) * c.heads + kh) * c.page + off;
-        rows[lane] = row;
-        s = bad ? __builtin_nanf("") : 0.f;
-        for (int k = 0; k < nb; k++) {
-          float u = 0.f;
-          for (int e = 0; e < 16; e++) {
-            const uint32_t w = c.k_codes[row * (hd / 2) + 16 * k + e];
-            u = fmaf(qs[32 * k + 2 * e], fp4(w & 15), u);
-            u = fmaf(qs[32 * k + 2 * e + 1], fp4(w >> 4), u);
-          }
-          s = fmaf(u, kv_scale(c.k_scales[row * nb + k]), s);
-        }
-        s *= a.scale;
-      }
-      float top = s;
-      for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-      top = fmaxf(m, top);
-      const float base = top == -kInf ? 0.f : top, old = expf(m - base);
-      const float p = t < hi ? expf(s - base) : 0.f;
-      m = top;
-      float sum = p;
-      for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-      l = fmaf(l, old, sum);
-      ps[lane] = p;
-      __syncthreads();
-      for (int x = 0; x < kKvMaxHeadDim / 64; x++) {
-        const int e = lane + 64 * x;
-        if (e >= hd) break;
-        float o = acc[x] * old;
-        for (int j = 0; j < 64 && t0 + j < hi; j++) {
-          const uint32_t w = c.v_codes[rows[j] * (hd / 2) + e / 2];
-          o = fmaf(ps[j], fp4(w >> (4 * (e & 1)) & 15) * kv_scale(c.v_scales[rows[j] * nb + e / 32]), o);
-        }
-        acc[x] = o;
-      }
-    }
-    T *out = (T *)a.out + tok * a.out_token + h * a.out_head;
-    for (int x = 0; x < kKvMaxHeadDim / 64; x++) {
-      const int e = lane + 64 * x;
-      if (e >= hd) break;
-      const float o = l == 0.f ? 0.f : acc[x] / l;
-      if constexpr (sizeof(T) == 2) out[e] = __builtin_bit_cast(uint16_t, (__bf16)o);
-      else out[e] = o;
-    }
-    if (a.lse && lane == 0) a.lse[r] = l == 0.f ? -kInf : m + logf(l);
-  }
+// The launch that the sizes decide: rows of a tile, tiles, parts.
+struct Plan {
+  int rows, splits;
+  int64_t tiles;
+};
+
+Plan plan(int dtype, int64_t q_tokens, int q_heads, int kv_heads, int head_dim, int64_t batch, int64_t capacity) {
+  const int64_t share = q_heads / kv_heads, per = q_tokens * share / batch;  // rows of a sequence, on average
+  Plan r;
+  r.rows = dtype == 0 || per <= 16 ? 16 : 32;
+  // every sequence may end inside a tile
+  r.tiles = (q_tokens * share + r.rows - 1) / r.rows + batch;
+  const int64_t groups = ((per + r.rows - 1) / r.rows) * batch * kv_heads;
+  // parts of at least 256 tokens, until four workgroups a CU are there
+  int64_t s = (1024 + groups - 1) / std::max<int64_t>(1, groups);
+  s = std::min({s, (capacity + 255) / 256, (int64_t)128});
+  r.splits = (int)std::max<int64_t>(1, s);
+  return r;
 }
 
 }  // namespace
 
 int64_t kv_attention_workspace(int64_t q_tokens, int q_heads, int kv_heads, int head_dim,
                                int64_t batch, int64_t capacity) {
-  return 0;
+  int64_t most = 0;  // for either type
+  for (int dtype = 0; dtype < 2; dtype++) {
+    const Plan r = plan(dtype, q_tokens, q_heads, kv_heads, head_dim, batch, capacity);
+    if (r.splits > 1) most = std::max(most, (int64_t)r.splits * q_tokens * q_heads * (head_dim + 2) * 4);
+  }
+  return most;
 }
 
 hipError_t launch_kv_attention(const KvAttentionArgs &a) {
-  const int64_t rows = a.q_tokens * a.q_heads;
-  const dim3 grid((unsigned)(rows < (1 << 20) ? rows : 1 << 20));
-  const FastDiv page((uint32_t)a.cache.page);
-  if (a.dtype == 0)
-    hipLaunchKernelGGL((kv_attention_kernel<float>), grid, dim3(64), 0, a.stream, a, page);
-  else
-    hipLaunchKernelGGL((kv_attention_kernel<uint16_t>), grid, dim3(64), 0, a.stream, a, page);
+  const Plan r = plan(a.dtype, a.q_tokens, a.q_heads, a.cache.heads, a.cache.head_dim, a.batch,
+                      (int64_t)a.table_pages * a.cache.page);
+  const int64_t share = a.q_heads / a.cache.heads, n = a.q_starts ? 0 : a.q_tokens / a.batch;
+  const int64_t each = std::max<int64_t>(1, (n * share + r.rows - 1) / r.rows);
+  const int64_t tiles = a.q_starts ? r.tiles : each * a.batch, total = a.q_tokens * a.q_heads;
+  KvLaunch p{a, FastDiv((uint32_t)a.cache.page), FastDiv((uint32_t)share), FastDiv((uint32_t)each), r.rows,
+             r.splits, fabsf(a.scale) * 1.4426950408889634f, nullptr, nullptr};
+  // hidden tokens are scores of -infinity, which a factor of 0 would make NaN: the
+  // smallest number instead, by which every finite score is as good as 0
+  if (p.log2_scale == 0.f) p.log2_scale = std::numeric_limits<float>::denorm_min();
+  p.part = (float *)a.workspace;
+  p.part_ml = (f32x2 *)(p.part + r.splits * total * a.cache.head_dim);
+  hipError_t e = launch_kv_rows(p, tiles);
+  if (e != hipSuccess || r.splits == 1) return e;
+  const dim3 grid((unsigned)tiles, (unsigned)a.cache.heads);
+  if (a.dtype == 0) hipLaunchKernelGGL((kv_join_kernel<float>), grid, dim3(256), 0, a.stream, p);
+  else hipLaunchKernelGGL((kv_join_kernel<uint16_t>), grid, dim3(256), 0, a.stream, p);
   return hipGetLastError();
 }
 

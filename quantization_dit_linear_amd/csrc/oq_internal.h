@@ -244,7 +244,7 @@ hipError_t launch_qk_norm_rope(const QkNormRopeArgs &a);
 // The 4-bit key/value cache: [pages][heads][page][head_dim / 2] codes and
 // [pages][heads][page][head_dim / 32] scale bytes.
 constexpr int kKvMaxHeadDim = 256, kKvMaxHeads = 65535;
-constexpr int64_t kKvMaxRows = (int64_t)1 << 28, kKvMaxBatch = (int64_t)1 << 20,
+constexpr int64_t kKvMaxRows = (int64_t)1 << 27, kKvMaxBatch = (int64_t)1 << 20,
                   kKvMaxLength = (int64_t)1 << 30;
 struct KvCache {
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;

@@ -111,7 +111,7 @@ def test_kv_attention():
                     dict(out=C + 0x1000000), dict(lse=F), dict(lse=A + 16), dict(lse=D), dict(out=E + 16),
                     dict(qt=1 << 60)),
              (dict(hd=48), dict(hd=288), dict(kh=65536, qh=65536), dict(batch=(1 << 20) + 1), dict(width=1 << 27),
-              dict(tokens=(1 << 28) + 1), dict(tokens=1 << 28)))
+              dict(tokens=(1 << 27) + 1), dict(tokens=1 << 27)))
     for kw in (dict(tokens=0), dict(batch=0), dict(tokens=0, q=None, out=None, kc=None)):
         assert call(**kw) == q.OQ_OK
 
@@ -119,12 +119,12 @@ def test_kv_attention():
 def test_kv_attention_workspace():
     size = q.lib().oq_mx_kv_attention_workspace
     for args in ((1, 4, 3, 64, 1, 16, 1), (1, 4, 2, 48, 1, 16, 1), (-1, 4, 2, 64, 1, 16, 1), (1, 4, 2, 64, 1, 0, 1),
-                 (1, 4, 2, 64, 1, 16, 0), (1, 4, 2, 64, 1, 16, 1 << 27), (1 << 28, 4, 2, 64, 1, 16, 1)):
+                 (1, 4, 2, 64, 1, 16, 0), (1, 4, 2, 64, 1, 16, 1 << 27), (1 << 27, 4, 2, 64, 1, 16, 1)):
         assert size(*args) == -1, args
     for args in ((0, 4, 2, 64, 1, 16, 1), (4, 4, 2, 64, 0, 16, 1)):
         assert size(*args) == 0, args
     for args in ((1, 1, 1, 32, 1, 1, 1), (1, 40, 8, 128, 1, 64, 512), (64, 32, 8, 128, 64, 64, 128),
-                 (1560, 40, 40, 128, 1, 1560, 21), (1 << 26, 4, 1, 256, 1 << 20, 1 << 10, 1 << 20)):
+                 (1560, 40, 40, 128, 1, 1560, 21), (1 << 25, 4, 1, 256, 1 << 20, 1 << 10, 1 << 20)):
         assert 0 <= size(*args) <= 1 << 31, args
 
 
