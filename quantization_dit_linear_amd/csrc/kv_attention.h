@@ -14,17 +14,21 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
 
-// One launch: tiles of `rows` (query, head of the group) rows of a sequence, in
-// the order of the sequences, times the key heads, times `splits` parts of the
-// tokens.  With more than one part every row leaves its sum, maximum and sum of
-// weights in the workspace, and the join adds the parts up in their order.
+// One launch.  A group is a tile of `rows` (query, head of the group) rows of a
+// sequence with one key head; its units are steps of `step` tokens, and `extra` in
+// front that stand for the time a group takes besides.
+// workers = 0: a wave a group.  Otherwise `workers` waves share all units evenly:
+// each takes the next of the order (sequence, key head, tile, step), and where
+// that cuts a group, its parts go to the workspace, to be joined in their order.
 struct KvLaunch {
   KvAttentionArgs a;
-  FastDiv page, share, tiles;  // tiles: of a sequence, where all have as many queries
-  int rows, splits;
-  float log2_scale;            // |scale| log2 e; a negative scale turns the queries
-  float *part;                 // [splits][q_tokens][q_heads][head_dim]
-  f32x2 *part_ml;              // [splits][q_tokens][q_heads]: maximum (log2), sum
+  FastDiv page, share, tiles;  // share: heads of a key head; tiles: of a sequence, where all have as many queries
+  int rows, step, extra;
+  int count, workers, least;  // count: tiles (at most); least: units of a worker
+  float log2_scale;           // |scale| log2 e; a negative scale turns the queries
+  float *part;     // [2 workers][rows][head_dim]: a worker's first part, then its last
+  f32x2 *part_ml;  // [2 workers][rows]: maximum (log2), sum of weights
+  int2 *parts;     // [tiles][heads]: a group's first part, and their number
 };
 
 // The rows of one tile.
@@ -39,52 +43,64 @@ struct KvTile {
 
 __device__ __forceinline__ int clamped(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
+// Sequence b's queries and length.
+__device__ __forceinline__ KvTile sequence(const KvLaunch &p, int b) {
+  const KvAttentionArgs &a = p.a;
+  KvTile t;
+  t.b = b, t.row0 = 0;
+  if (a.q_starts) {
+    const int most = (int)a.q_tokens;
+    t.start = clamped(a.q_starts[b], 0, most);
+    t.n = clamped(a.q_starts[b + 1], t.start, most) - t.start;
+  } else {
+    t.n = (int)(a.q_tokens / a.batch);
+    t.start = b * t.n;
+  }
+  t.rows = t.n * (int)p.share.d;
+  t.length = clamped(a.lengths[b], 0, a.table_pages * a.cache.page);
+  return t;
+}
+
+// The inclusive sum over the lanes up to this one.
+__device__ __forceinline__ int prefix_sum(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int off = 1; off < 64; off *= 2) {
+    const int o = __shfl_up(v, off);
+    if (lane >= off) v += o;
+  }
+  return v;
+}
+
+__device__ __forceinline__ KvTile from_lane(KvTile t, int l) {
+  return {__builtin_amdgcn_readlane(t.b, l), __builtin_amdgcn_readlane(t.row0, l), __builtin_amdgcn_readlane(t.rows, l),
+          __builtin_amdgcn_readlane(t.start, l), __builtin_amdgcn_readlane(t.n, l), __builtin_amdgcn_readlane(t.length, l)};
+}
+
 // Tile x of the launch.  Sequences of their own lengths: 64 of them at a time, a
 // prefix sum of their tiles over the wave's lanes (every wave for itself).
 __device__ __forceinline__ KvTile find_tile(const KvLaunch &p, int x) {
-  const KvAttentionArgs &a = p.a;
-  KvTile t{-1, 0, 0, 0, 0, 0};
-  int tile = 0;
-  if (!a.q_starts) {
+  const int lane = threadIdx.x & 63;
+  if (!p.a.q_starts) {
     uint32_t b, r;
     p.tiles.split((uint32_t)x, b, r);
-    t.b = (int)b, tile = (int)r;
-    t.n = (int)(a.q_tokens / a.batch);
-    t.start = t.b * t.n;
-  } else {
-    const int lane = threadIdx.x & 63, share = (int)p.share.d, most = (int)a.q_tokens;
-    int before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 64) {
-      const int b = b0 + lane;
-      int s = 0, n = 0;
-      if (b < a.batch) {
-        s = clamped(a.q_starts[b], 0, most);
-        n = clamped(a.q_starts[b + 1], s, most) - s;
-      }
-      const int tiles = (n * share + p.rows - 1) / p.rows;
-      int sum = tiles;
-#pragma unroll
-      for (int off = 1; off < 64; off *= 2) {
-        const int o = __shfl_up(sum, off);
-        if (lane >= off) sum += o;
-      }
-      const uint64_t past = __ballot(before + sum > x);
-      if (past) {
-        const int l = __builtin_ctzll(past);
-        t.b = b0 + l;
-        t.start = __builtin_amdgcn_readlane(s, l);
-        t.n = __builtin_amdgcn_readlane(n, l);
-        tile = x - before - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(tiles, l));
-        break;
-      }
-      before += __builtin_amdgcn_readlane(sum, 63);
-    }
-    if (t.b < 0) return t;
+    KvTile t = sequence(p, (int)b);
+    t.row0 = (int)r * p.rows;
+    return t;
   }
-  t.row0 = tile * p.rows;
-  t.rows = t.n * (int)p.share.d;
-  t.length = clamped(a.lengths[t.b], 0, a.table_pages * a.cache.page);
-  return t;
+  for (int b0 = 0, before = 0; b0 < p.a.batch; b0 += 64) {
+    KvTile t{-1, 0, 0, 0, 0, 0};
+    if (b0 + lane < p.a.batch) t = sequence(p, b0 + lane);
+    const int tiles = (t.rows + p.rows - 1) / p.rows, sum = before + prefix_sum(tiles);
+    const uint64_t past = __ballot(sum > x);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      t.row0 = (x - sum + tiles) * p.rows;
+      return from_lane(t, l);
+    }
+    before = __builtin_amdgcn_readlane(sum, 63);
+  }
+  return {-1, 0, 0, 0, 0, 0};
 }
 
 // The tokens [lo, hi) that query i of a tile's sequence sees.
@@ -98,13 +114,60 @@ __device__ __forceinline__ void seen(const KvAttentionArgs &a, const KvTile &t, 
   }
 }
 
-// The cache row of token t (of its key head) in sequence b; -1 if its page is not there.
-__device__ __forceinline__ int64_t cache_row(const KvLaunch &p, int b, int kh, int t) {
-  uint32_t pg, off;
-  p.page.split((uint32_t)t, pg, off);
-  const int64_t page = p.a.table ? p.a.table[(int64_t)b * p.a.table_pages + pg] : b;
-  if (page < 0 || page >= p.a.cache.pages) return -1;
-  return (page * p.a.cache.heads + kh) * p.a.cache.page + off;
+// A sequence in the order of the units: every (key head, tile) of it has `units`,
+// the last of them steps of the cache from step `first`.
+struct KvUnits {
+  KvTile t;
+  int before, tiles_before;  // units and tiles of the sequences before
+  int tiles, units, first;
+  __device__ int all(int heads) const { return heads * tiles * units; }
+};
+
+__device__ __forceinline__ KvUnits units_of(const KvLaunch &p, int b) {
+  KvUnits u{{-1, 0, 0, 0, 0, 0}, 0, 0, 0, 0, 0};
+  if (b >= p.a.batch) return u;
+  u.t = sequence(p, b);
+  if (u.t.n == 0) return u;
+  u.tiles = (u.t.rows + p.rows - 1) / p.rows;
+  int lo, hi, unused;
+  seen(p.a, u.t, 0, lo, unused);
+  seen(p.a, u.t, u.t.n - 1, unused, hi);
+  u.first = lo / p.step;
+  u.units = (hi + p.step - 1) / p.step - u.first;
+  u.units = p.extra + (u.units < 0 ? 0 : u.units);  // (rows that see nothing are written too)
+  return u;
+}
+
+// All units, and a worker's part of them.
+__device__ __forceinline__ int share_of(const KvLaunch &p, int &total) {
+  const int lane = threadIdx.x & 63;
+  total = 0;
+  for (int b0 = 0; b0 < p.a.batch; b0 += 64)
+    total += __builtin_amdgcn_readlane(prefix_sum(units_of(p, b0 + lane).all(p.a.cache.heads)), 63);
+  const int share = (total + p.workers - 1) / p.workers;
+  return share < p.least ? p.least : share;
+}
+
+// The sequence that unit x belongs to (x below the total).
+__device__ __forceinline__ KvUnits find_units(const KvLaunch &p, int x) {
+  const int lane = threadIdx.x & 63;
+  for (int b0 = 0, before = 0, tiles = 0; b0 < p.a.batch; b0 += 64) {
+    const KvUnits u = units_of(p, b0 + lane);
+    const int all = u.all(p.a.cache.heads), sum = before + prefix_sum(all), tsum = tiles + prefix_sum(u.tiles);
+    const uint64_t past = __ballot(sum > x);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      return {from_lane(u.t, l),
+              __builtin_amdgcn_readlane(sum - all, l),
+              __builtin_amdgcn_readlane(tsum - u.tiles, l),
+              __builtin_amdgcn_readlane(u.tiles, l),
+              __builtin_amdgcn_readlane(u.units, l),
+              __builtin_amdgcn_readlane(u.first, l)};
+    }
+    before = __builtin_amdgcn_readlane(sum, 63);
+    tiles = __builtin_amdgcn_readlane(tsum, 63);
+  }
+  return {{-1, 0, 0, 0, 0, 0}, 0, 0, 0, 0, 0};
 }
 
 // Eight e2m1 codes of one block as bf16: exact at every scale.
@@ -117,9 +180,11 @@ __device__ __forceinline__ bf16x8 fp4x8(uint32_t w, float scale) {
   return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// A scale byte as attention reads it: 253 and more are NaN.
+// Scale bytes that attention reads as NaN: the writer's 255, and those whose
+// blocks could pass bf16's range.  255 as an exponent makes the conversion's
+// results NaN; 0 its results subnormal or zero.
 __device__ __forceinline__ bool kv_nan(uint32_t s) { return s >= 253; }
-__device__ __forceinline__ float kv_scale(uint32_t s) { return mx_scale(kv_nan(s) ? 255 : s); }
+__device__ __forceinline__ float kv_scale(uint32_t s) { return __uint_as_float(s << 23); }
 
 // Eight fp32 values as bf16 in NQ parts whose sum they are: one, rounded to
 // nearest, or three, which hold all 24 bits.
@@ -167,6 +232,8 @@ __device__ __forceinline__ void store4(T *p, f32x4 v) {
 
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -kInf : (m + log2f(l)) * kLn2; }
 
-hipError_t launch_kv_rows(const KvLaunch &p, int64_t tiles);
+// tokens a step of the rows kernel
+constexpr int kv_rows_step(int head_dim) { return head_dim <= 128 ? 64 : 32; }
+hipError_t launch_kv_rows(const KvLaunch &p);
 
 }  // namespace oq
