@@ -17,14 +17,17 @@ constexpr float kLn2 = 0.6931471805599453f;
 // One launch.  A group is a tile of `rows` (query, head of the group) rows of a
 // sequence with one key head; its units are steps of `step` tokens, and `extra` in
 // front that stand for the time a group takes besides.
-// workers = 0: a wave a group.  Otherwise `workers` waves share all units evenly:
-// each takes the next of the order (sequence, key head, tile, step), and where
-// that cuts a group, its parts go to the workspace, to be joined in their order.
+// workers = 0: a wave a group.  Otherwise `workers` waves (team: workgroups, whose
+// waves take the steps by turns) share all units evenly: each takes the next of the
+// order (sequence, key head, tile, step), and where that cuts a group, its parts go
+// to the workspace, to be joined in their order.
 struct KvLaunch {
   KvAttentionArgs a;
   FastDiv page, share, tiles;  // share: heads of a key head; tiles: of a sequence, where all have as many queries
   int rows, step, extra;
   int count, workers, least;  // count: tiles (at most); least: units of a worker
+  int each;                   // queries of a sequence, where all have as many
+  bool team;
   float log2_scale;           // |scale| log2 e; a negative scale turns the queries
   float *part;     // [2 workers][rows][head_dim]: a worker's first part, then its last
   f32x2 *part_ml;  // [2 workers][rows]: maximum (log2), sum of weights
@@ -53,7 +56,7 @@ __device__ __forceinline__ KvTile sequence(const KvLaunch &p, int b) {
     t.start = clamped(a.q_starts[b], 0, most);
     t.n = clamped(a.q_starts[b + 1], t.start, most) - t.start;
   } else {
-    t.n = (int)(a.q_tokens / a.batch);
+    t.n = p.each;
     t.start = b * t.n;
   }
   t.rows = t.n * (int)p.share.d;
@@ -61,15 +64,24 @@ __device__ __forceinline__ KvTile sequence(const KvLaunch &p, int b) {
   return t;
 }
 
-// The inclusive sum over the lanes up to this one.
+// The inclusive sum over the lanes up to this one: within rows of 16 lanes, then
+// each row's last lane into the rows behind it.
 __device__ __forceinline__ int prefix_sum(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int off = 1; off < 64; off *= 2) {
-    const int o = __shfl_up(v, off);
-    if (lane >= off) v += o;
-  }
+#define OQ_STEP(CTRL, ROWS) v += __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false)
+  OQ_STEP(0x111, 0xf);  // the lane before
+  OQ_STEP(0x112, 0xf);
+  OQ_STEP(0x114, 0xf);
+  OQ_STEP(0x118, 0xf);
+  OQ_STEP(0x142, 0xa);  // lane 15 of the row before, into rows 1 and 3
+  OQ_STEP(0x143, 0xc);  // lane 31 into rows 2 and 3
+#undef OQ_STEP
   return v;
+}
+
+// The same, known to be the same in all lanes.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ KvTile uniform(KvTile t) {
+  return {uniform(t.b), uniform(t.row0), uniform(t.rows), uniform(t.start), uniform(t.n), uniform(t.length)};
 }
 
 __device__ __forceinline__ KvTile from_lane(KvTile t, int l) {
@@ -138,14 +150,17 @@ __device__ __forceinline__ KvUnits units_of(const KvLaunch &p, int b) {
   return u;
 }
 
-// All units, and a worker's part of them.
-__device__ __forceinline__ int share_of(const KvLaunch &p, int &total) {
-  const int lane = threadIdx.x & 63;
-  total = 0;
-  for (int b0 = 0; b0 < p.a.batch; b0 += 64)
-    total += __builtin_amdgcn_readlane(prefix_sum(units_of(p, b0 + lane).all(p.a.cache.heads)), 63);
-  const int share = (total + p.workers - 1) / p.workers;
-  return share < p.least ? p.least : share;
+// The sequence that unit x belongs to (none past the last), among the 64 from b0 on
+// of which the lanes hold one each, all its units and the prefix sums of these and of
+// the tiles.
+__device__ __forceinline__ KvUnits pick(const KvUnits &u, int all, int sum, int tsum, uint64_t past) {
+  const int l = __builtin_ctzll(past);
+  return {from_lane(u.t, l),
+          __builtin_amdgcn_readlane(sum - all, l),
+          __builtin_amdgcn_readlane(tsum - u.tiles, l),
+          __builtin_amdgcn_readlane(u.tiles, l),
+          __builtin_amdgcn_readlane(u.units, l),
+          __builtin_amdgcn_readlane(u.first, l)};
 }
 
 // The sequence that unit x belongs to (x below the total).
@@ -155,19 +170,32 @@ __device__ __forceinline__ KvUnits find_units(const KvLaunch &p, int x) {
     const KvUnits u = units_of(p, b0 + lane);
     const int all = u.all(p.a.cache.heads), sum = before + prefix_sum(all), tsum = tiles + prefix_sum(u.tiles);
     const uint64_t past = __ballot(sum > x);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      return {from_lane(u.t, l),
-              __builtin_amdgcn_readlane(sum - all, l),
-              __builtin_amdgcn_readlane(tsum - u.tiles, l),
-              __builtin_amdgcn_readlane(u.tiles, l),
-              __builtin_amdgcn_readlane(u.units, l),
-              __builtin_amdgcn_readlane(u.first, l)};
-    }
+    if (past) return pick(u, all, sum, tsum, past);
     before = __builtin_amdgcn_readlane(sum, 63);
     tiles = __builtin_amdgcn_readlane(tsum, 63);
   }
   return {{-1, 0, 0, 0, 0, 0}, 0, 0, 0, 0, 0};
+}
+
+// A worker's units [pos, end), `share` each, and the sequence of the first.
+__device__ __forceinline__ KvUnits first_units(const KvLaunch &p, int worker, int &share, int &pos, int &end) {
+  const int lane = threadIdx.x & 63;
+  int total = 0;
+  KvUnits u;
+  int all = 0, sum = 0;
+  for (int b0 = 0; b0 < p.a.batch; b0 += 64) {
+    u = units_of(p, b0 + lane);
+    all = u.all(p.a.cache.heads);
+    sum = prefix_sum(all);
+    total += __builtin_amdgcn_readlane(sum, 63);
+  }
+  share = (total + p.workers - 1) / p.workers;
+  if (share < p.least) share = p.least;
+  pos = worker * share;
+  end = pos + share < total ? pos + share : total;
+  if (pos >= end) return u;
+  if (p.a.batch > 64) return find_units(p, pos);
+  return pick(u, all, sum, prefix_sum(u.tiles), __ballot(sum > pos));
 }
 
 // Eight e2m1 codes of one block as bf16: exact at every scale.

@@ -7,71 +7,85 @@
 
 #include <algorithm>
 #include <limits>
-#include <stdlib.h>
 
 #include "kv_attention.h"
 
 namespace oq {
 namespace {
 
-// A group's parts, in their order.  A workgroup takes every gridDim.z-th row of a
-// group; 256 / (head_dim / 4) threads an element take every so many parts, eight
-// loads at a time, and their sums join in a fixed order.
-constexpr int kMaxWorkers = 2048;
-
-template <class T>
-__global__ __launch_bounds__(256) void kv_join_kernel(KvLaunch p) {
-  __shared__ __attribute__((aligned(16))) float sums[256 * 4];
-  __shared__ float weight[kMaxWorkers], part_sum[4], part_top[4];
+// A group's parts, in their order, a wave a row: 64 parts' maxima and sums of
+// weights a time, then their sums, as many side by side as the lanes hold, eight
+// loads a lane.  SPLIT: the waves of a workgroup share a row (parts are many where
+// groups are few), and the first of them adds up.
+template <class T, bool SPLIT>
+__global__ __launch_bounds__(SPLIT ? 1024 : 256) void kv_join_kernel(KvLaunch p) {
+  constexpr int kWaves = SPLIT ? 16 : 4;
+  __shared__ __attribute__((aligned(16))) float sums[kWaves][64 * 4];
+  __shared__ f32x2 waves[kWaves];
   const KvAttentionArgs &a = p.a;
-  const int tid = threadIdx.x, hd = a.cache.head_dim, q4 = hd / 4, groups = 256 / q4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hd = a.cache.head_dim, q4 = hd / 4, side = 64 / q4, g = lane / q4, d = 4 * (lane - g * q4);
+  const int2 which = p.parts[(int64_t)blockIdx.x * a.cache.heads + blockIdx.y];
   const KvTile t = find_tile(p, blockIdx.x);
   if (t.b < 0) return;
-  const int2 which = p.parts[(int64_t)blockIdx.x * a.cache.heads + blockIdx.y];
   const int first = which.x, parts = which.y;
   if (parts == 1) return;
   // part k: the last of its worker where the group starts there, else the first
   const auto slot = [&](int k) { return (int64_t)(k == 0 ? first : first - 1 + 2 * k) * p.rows; };
   const int rows = t.rows - t.row0 < p.rows ? t.rows - t.row0 : p.rows;
-  for (int r = blockIdx.z; r < rows; r += gridDim.z) {
-    __syncthreads();  // the row before is read
+  const int per = SPLIT ? (parts + kWaves - 1) / kWaves : parts;
+  const int k0 = SPLIT ? wave * per : 0, k1 = k0 + per < parts ? k0 + per : parts;
+  for (int r = SPLIT ? blockIdx.z : wave; r < rows; r += SPLIT ? gridDim.z : kWaves) {
     float top = -kInf, sum = 0.f;
-    for (int k = tid; k < parts; k += 256) top = fmaxf(top, p.part_ml[slot(k) + r][0]);
-    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-    if ((tid & 63) == 0) part_top[tid >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(part_top[0], part_top[1]), fmaxf(part_top[2], part_top[3]));
-    const float base = top == -kInf ? 0.f : top;
-    for (int k = tid; k < parts; k += 256) {
-      const f32x2 ml = p.part_ml[slot(k) + r];
-      const float w = __builtin_amdgcn_exp2f(ml[0] - base);
-      sum += ml[1] * w;
-      weight[k] = ml[1] == 0.f ? -1.f : w;  // a part that saw nothing left no sum: it is not read
-    }
-    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-    if ((tid & 63) == 0) part_sum[tid >> 6] = sum;
-    __syncthreads();
-    sum = part_sum[0] + part_sum[1] + part_sum[2] + part_sum[3];
-
-    const int g = tid / q4, d = 4 * (tid - g * q4);
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (g < groups) {
-      for (int k0 = g; k0 < parts; k0 += 8 * groups) {
+    for (int c0 = k0; c0 < k1; c0 += 64) {
+      const int k = c0 + lane, n = k1 - c0 < 64 ? k1 - c0 : 64;
+      f32x2 ml = {-kInf, 0.f};
+      if (k < k1) ml = p.part_ml[slot(k) + r];
+      float now = ml[0];
+      for (int off = 32; off > 0; off >>= 1) now = fmaxf(now, __shfl_xor(now, off));
+      now = fmaxf(now, top);
+      const float base = now == -kInf ? 0.f : now, old = __builtin_amdgcn_exp2f(top - base);
+      const float w = __builtin_amdgcn_exp2f(ml[0] - base);
+      top = now;
+      v *= old;
+      float s = ml[1] * w;
+      for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+      sum = sum * old + s;
+      const float keep = ml[1] == 0.f ? -1.f : w;  // a part that saw nothing left no sum: it is not read
+      for (int b0 = 0; b0 < n; b0 += 8 * side) {
         f32x4 x[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-          const int k = k0 + e * groups;
+          const int at = b0 + e * side + g;
+          const float f = __shfl(keep, at & 63);
           x[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-          if (k < parts && weight[k] != -1.f) x[e] = *(const f32x4 *)(p.part + (slot(k) + r) * hd + d) * weight[k];
+          if (g < side && at < n && f != -1.f) x[e] = *(const f32x4 *)(p.part + (slot(c0 + at) + r) * hd + d) * f;
         }
 #pragma unroll
         for (int e = 0; e < 8; e++) v += x[e];
       }
-      *(f32x4 *)(sums + 4 * tid) = v;
     }
-    __syncthreads();
-    if (g == 0) {
-      for (int k = 1; k < groups; k++) v += *(const f32x4 *)(sums + 4 * (tid + k * q4));
+    if (SPLIT) __syncthreads();  // the row before is read
+    *(f32x4 *)&sums[wave][4 * lane] = v;
+    if (lane == 0) waves[wave] = f32x2{top, sum};
+    if (SPLIT) __syncthreads();
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (SPLIT && wave != 0) continue;
+    if (lane < q4) {
+      v = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (SPLIT) {
+#pragma unroll
+        for (int w = 0; w < kWaves; w++) top = fmaxf(top, waves[w][0]);
+        sum = 0.f;
+      }
+      const float base = top == -kInf ? 0.f : top;
+      for (int w = SPLIT ? 0 : wave; w <= (SPLIT ? kWaves - 1 : wave); w++) {
+        const float f = SPLIT ? __builtin_amdgcn_exp2f(waves[w][0] - base) : 1.f;
+        if (SPLIT) sum += waves[w][1] * f;
+        for (int k = 0; k < side; k++) v += *(const f32x4 *)&sums[w][4 * (lane + k * q4)] * f;
+      }
       if (sum == 0.f) v = f32x4{0.f, 0.f, 0.f, 0.f};
       else v *= 1.f / sum;
       uint32_t i, h;
@@ -86,6 +100,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvLaunch p) {
 // The launch that the sizes decide.
 struct Plan {
   int rows, step, workers;
+  bool team;
   int64_t tiles;
   int64_t workspace(int kv_heads, int head_dim) const {
     return workers ? (int64_t)2 * workers * rows * (head_dim + 2) * 4 + tiles * kv_heads * 8 : 0;
@@ -93,16 +108,20 @@ struct Plan {
 };
 
 Plan plan(int dtype, int64_t q_tokens, int q_heads, int kv_heads, int head_dim, int64_t batch, int64_t capacity) {
-  const int64_t share = q_heads / kv_heads, per = q_tokens * share / batch;  // rows of a sequence, on average
+  const int64_t share = q_heads / kv_heads;
   Plan r;
-  r.rows = dtype == 0 || head_dim > 128 || per <= 16 ? 16 : 32;
+  r.rows = 16;
   r.step = kv_rows_step(head_dim);
   // every sequence may end inside a tile
   r.tiles = (q_tokens * share + r.rows - 1) / r.rows + batch;
-  const char *e2 = getenv("KV_WG"), *e3 = getenv("KV_MAX");
-  const int64_t most = e3 ? atoi(e3) : 1024;
+  // Even shares of the steps while the tiles are few enough to be counted by every
+  // wave: eight waves a CU, or two workgroups of them where the groups are so few that
+  // each is cut into many parts (fewer parts to join: one token over 32760 24.3
+  // against 26 us).
   const int64_t units = r.tiles * kv_heads * (capacity / r.step + 8);
-  r.workers = r.tiles <= most && units < (int64_t)1 << 30 ? (e2 ? atoi(e2) : 2048) : 0;
+  r.workers = r.tiles <= 1024 && units < (int64_t)1 << 30 ? 2048 : 0;
+  r.team = r.workers && r.tiles * kv_heads <= 128;
+  if (r.team) r.workers /= 4;
   return r;
 }
 
@@ -122,9 +141,8 @@ hipError_t launch_kv_attention(const KvAttentionArgs &a) {
   const int64_t share = a.q_heads / a.cache.heads, n = a.q_starts ? 0 : a.q_tokens / a.batch;
   const int64_t each = std::max<int64_t>(1, (n * share + r.rows - 1) / r.rows);
   const int64_t tiles = a.q_starts ? r.tiles : each * a.batch;
-  const char *e1 = getenv("KV_LEAST"), *e2 = getenv("KV_EXTRA");
   KvLaunch p{a, FastDiv((uint32_t)a.cache.page), FastDiv((uint32_t)share), FastDiv((uint32_t)each), r.rows,
-             r.step, e2 ? atoi(e2) : 2, (int)tiles, r.workers, e1 ? atoi(e1) : 2, fabsf(a.scale) * 1.4426950408889634f, nullptr, nullptr, nullptr};
+             r.step, 2, (int)tiles, r.workers, 2, (int)n, r.team, fabsf(a.scale) * 1.4426950408889634f, nullptr, nullptr, nullptr};
   // hidden tokens are scores of -infinity, which a factor of 0 would make NaN: the
   // smallest number instead, by which every finite score is as good as 0
   if (p.log2_scale == 0.f) p.log2_scale = std::numeric_limits<float>::denorm_min();
@@ -133,10 +151,15 @@ hipError_t launch_kv_attention(const KvAttentionArgs &a) {
   p.parts = (int2 *)(p.part_ml + (int64_t)2 * r.workers * r.rows);
   hipError_t e = launch_kv_rows(p);
   if (e != hipSuccess || !r.workers) return e;
-  // a workgroup a row where the groups are few
-  const dim3 grid((unsigned)tiles, (unsigned)a.cache.heads, tiles * a.cache.heads <= 128 ? r.rows : 1);
-  if (a.dtype == 0) hipLaunchKernelGGL((kv_join_kernel<float>), grid, dim3(256), 0, a.stream, p);
-  else hipLaunchKernelGGL((kv_join_kernel<uint16_t>), grid, dim3(256), 0, a.stream, p);
+  const bool few = tiles * a.cache.heads <= 128;
+  const dim3 grid((unsigned)tiles, (unsigned)a.cache.heads, few ? r.rows : 1);
+  if (a.dtype == 0) {
+    if (few) hipLaunchKernelGGL((kv_join_kernel<float, true>), grid, dim3(1024), 0, a.stream, p);
+    else hipLaunchKernelGGL((kv_join_kernel<float, false>), grid, dim3(256), 0, a.stream, p);
+  } else {
+    if (few) hipLaunchKernelGGL((kv_join_kernel<uint16_t, true>), grid, dim3(1024), 0, a.stream, p);
+    else hipLaunchKernelGGL((kv_join_kernel<uint16_t, false>), grid, dim3(256), 0, a.stream, p);
+  }
   return hipGetLastError();
 }
 
