@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "liborbitquant.so")
 SOURCES = ["oq_host.cpp", "rotate_quantize.hip", "rotate_quantize_fast.hip", "linear.hip",
            "adaln_rtn4.hip", "mx.hip", "mx_linear.hip", "rms_norm.hip", "rope.hip", "rtn4_group.hip",
-           "qk_norm_rope.hip", "kv_cache.hip", "kv_attention.hip", "kv_attention_rows.hip",
+           "qk_norm_rope.hip", "kv_cache.hip", "kv_attention.hip", "kv_attention_rows.hip", "kv_attention_tiles.hip",
            "diag.hip"]
 # per-source extra flags: the rotate kernel keeps its MFMA results in
 # ordinary VGPRs (no accumulation-register round trip per value)

@@ -35,7 +35,7 @@ __global__ __launch_bounds__(SPLIT ? 1024 : 256) void kv_join_kernel(KvLaunch p)
   const int rows = t.rows - t.row0 < p.rows ? t.rows - t.row0 : p.rows;
   const int per = SPLIT ? (parts + kWaves - 1) / kWaves : parts;
   const int k0 = SPLIT ? wave * per : 0, k1 = k0 + per < parts ? k0 + per : parts;
-  for (int r = SPLIT ? blockIdx.z : wave; r < rows; r += SPLIT ? gridDim.z : kWaves) {
+  for (int r = SPLIT ? blockIdx.z : blockIdx.z * kWaves + wave; r < rows; r += SPLIT ? gridDim.z : kWaves * gridDim.z) {
     float top = -kInf, sum = 0.f;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     for (int c0 = k0; c0 < k1; c0 += 64) {
@@ -97,10 +97,14 @@ __global__ __launch_bounds__(SPLIT ? 1024 : 256) void kv_join_kernel(KvLaunch p)
   }
 }
 
+#ifndef KV_WIDE
+#define KV_WIDE 32
+#endif
+
 // The launch that the sizes decide.
 struct Plan {
   int rows, step, workers;
-  bool team;
+  bool team, wide;  // wide: the tiles kernel
   int64_t tiles;
   int64_t workspace(int kv_heads, int head_dim) const {
     return workers ? (int64_t)2 * workers * rows * (head_dim + 2) * 4 + tiles * kv_heads * 8 : 0;
@@ -108,10 +112,11 @@ struct Plan {
 };
 
 Plan plan(int dtype, int64_t q_tokens, int q_heads, int kv_heads, int head_dim, int64_t batch, int64_t capacity) {
-  const int64_t share = q_heads / kv_heads;
+  const int64_t share = q_heads / kv_heads, per = q_tokens * share / batch;  // rows of a sequence, on average
   Plan r;
-  r.rows = 16;
-  r.step = kv_rows_step(head_dim);
+  r.wide = per > KV_WIDE;
+  r.rows = r.wide ? kv_tiles_rows(dtype, head_dim) : 16;
+  r.step = r.wide ? kKvTilesStep : kv_rows_step(head_dim);
   // every sequence may end inside a tile
   r.tiles = (q_tokens * share + r.rows - 1) / r.rows + batch;
   // Even shares of the steps while the tiles are few enough to be counted by every
@@ -122,6 +127,7 @@ Plan plan(int dtype, int64_t q_tokens, int q_heads, int kv_heads, int head_dim, 
   r.workers = r.tiles <= 1024 && units < (int64_t)1 << 30 ? 2048 : 0;
   r.team = r.workers && r.tiles * kv_heads <= 128;
   if (r.team) r.workers /= 4;
+  if (r.wide) r.team = false, r.workers = r.workers && r.tiles * kv_heads <= 1024 ? 256 : 0;
   return r;
 }
 
@@ -149,10 +155,10 @@ hipError_t launch_kv_attention(const KvAttentionArgs &a) {
   p.part = (float *)a.workspace;
   p.part_ml = (f32x2 *)(p.part + (int64_t)2 * r.workers * r.rows * a.cache.head_dim);
   p.parts = (int2 *)(p.part_ml + (int64_t)2 * r.workers * r.rows);
-  hipError_t e = launch_kv_rows(p);
+  hipError_t e = r.wide ? launch_kv_tiles(p) : launch_kv_rows(p);
   if (e != hipSuccess || !r.workers) return e;
-  const bool few = tiles * a.cache.heads <= 128;
-  const dim3 grid((unsigned)tiles, (unsigned)a.cache.heads, few ? r.rows : 1);
+  const bool few = tiles * a.cache.heads <= 128 && !r.wide;
+  const dim3 grid((unsigned)tiles, (unsigned)a.cache.heads, few ? r.rows : r.rows / 16);
   if (a.dtype == 0) {
     if (few) hipLaunchKernelGGL((kv_join_kernel<float, true>), grid, dim3(1024), 0, a.stream, p);
     else hipLaunchKernelGGL((kv_join_kernel<float, false>), grid, dim3(256), 0, a.stream, p);

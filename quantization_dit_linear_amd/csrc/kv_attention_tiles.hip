@@ -1,0 +1,362 @@
+// kv_attention_tiles.hip -- attention of many rows (chunks, prompts) over the
+// 4-bit cache.
+//
+// A workgroup takes a tile of rows, each of its four waves QT times 32 of them,
+// and walks over the tokens 64 a step.  The step's keys and values are converted
+// once for all waves, into LDS as bf16 (two buffers: the next step's are written
+// while this one's are read).  A wave computes
+//   S^T = K Q^T   and   O^T = V^T P^T
+// with 32x32x16 matrix instructions; the first leaves each lane eight tokens of its
+// row a time, in an order that the second takes as its operand, so the weights
+// never leave their lane.  V^T comes from LDS by transposed reads.  16-byte pieces
+// of a row are swizzled by the token, so that neither the operands' reads nor the
+// conversion's writes conflict.
+#include <hip/hip_runtime.h>
+
+#include "kv_attention.h"
+
+namespace oq {
+namespace {
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+constexpr int kTok = kKvTilesStep;
+
+// A token's row in LDS: 4 NB pieces of 16 bytes.  Rows repeat their banks every
+// 256 bytes, that is every 1, 2 or 4 tokens by NB modulo 4; the piece's number is
+// changed by the bits of the token that the row's place does not use, so that any
+// 16 tokens in line (16-byte reads of one piece) and any four (8-byte reads of four
+// pieces) meet all banks alike.
+template <int NB>
+__device__ __forceinline__ int swizzle(int tok) {
+  constexpr int HIGH = NB % 4 == 0 ? 2 : NB % 2 == 0 ? 1 : 0;
+  return ((tok & 3) >> (2 - HIGH) << 2) | (tok >> 2 & 3);
+}
+
+template <int NB, int QT, bool F32>
+__global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
+  using T = typename std::conditional<F32, float, uint16_t>::type;
+  constexpr int HD = 32 * NB, ROWB = 2 * HD, NQ = F32 ? 3 : 1, TASKS = (kTok * NB + 255) / 256;
+  __shared__ __attribute__((aligned(16))) char lds[2][2][kTok * ROWB];  // [buffer][keys, values]
+  __shared__ int nans[4];  // by step modulo 4: blocks of NaN among the values
+  const KvAttentionArgs &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
+  const int wave = uniform(tid >> 6);
+  int share = 0, pos = 0, end = 1;
+  KvUnits u;
+  if (p.workers) u = first_units(p, blockIdx.x, share, pos, end);
+  for (bool again = false; pos < end; again = true) {
+    // the group, and this workgroup's steps of it
+    KvTile t;
+    int kh, g0 = 0, g1 = 1 << 30, slot = -1;
+    if (p.workers) {
+      if (again) u = find_units(p, pos);
+      const int at = pos - u.before, g = at / u.units, skip = at - g * u.units;
+      const int len = u.units - skip < end - pos ? u.units - skip : end - pos;
+      t = u.t;
+      kh = g / u.tiles;
+      const int tile = g - kh * u.tiles;
+      t.row0 = tile * p.rows;
+      g1 = u.first + skip + len - p.extra;
+      g0 = skip > p.extra ? u.first + skip - p.extra : u.first;
+      if (len < u.units) slot = 2 * (int)blockIdx.x + (skip == 0);
+      if (skip == 0 && tid == 0)
+        p.parts[(int64_t)(u.tiles_before + tile) * a.cache.heads + kh] =
+            int2{slot, (pos + u.units - 1) / share - (int)blockIdx.x + 1};
+      pos += len;
+    } else {
+      t = find_tile(p, blockIdx.x);
+      kh = blockIdx.y;
+      pos = end;
+      if (t.b < 0) return;
+    }
+    t = uniform(t), kh = uniform(kh), g0 = uniform(g0), g1 = uniform(g1), slot = uniform(slot), pos = uniform(pos);
+    // what the tile as a whole sees, and what every row of it sees
+    int any_lo, any_hi, all_lo, all_hi;
+    const int row1 = t.row0 + p.rows < t.rows ? t.row0 + p.rows : t.rows;
+    seen(a, t, (int)p.share.div((uint32_t)t.row0), any_lo, all_hi);
+    seen(a, t, (int)p.share.div((uint32_t)(row1 - 1)), all_lo, any_hi);
+    const int step0 = any_lo / kTok > g0 ? any_lo / kTok : g0;
+    const int step1 = any_hi <= any_lo ? step0 : (any_hi + kTok - 1) / kTok < g1 ? (any_hi + kTok - 1) / kTok : g1;
+
+    // Conversion: task x of a step is block x % NB of token x / NB, for keys and
+    // values; a thread has TASKS of them.
+    const int last_tok = (kTok * step1 < any_hi ? kTok * step1 : any_hi) - 1;
+    const int32_t *table = a.table ? a.table + (int64_t)t.b * a.table_pages : a.lengths + t.b;
+    const uint32_t mask = a.table ? ~0u : 0u;
+    auto token = [&](int step, int i) {
+      const int x = tid + 256 * i, tok = kTok * step + (x < kTok * NB ? x / NB : kTok - 1);
+      return tok < last_tok ? tok : last_tok;
+    };
+    auto entry = [&](int step, int (&page)[TASKS]) {
+#pragma unroll
+      for (int i = 0; i < TASKS; i++) page[i] = table[p.page.div((uint32_t)token(step, i)) & mask];
+    };
+    struct Raw {
+      u32x4 k[TASKS], v[TASKS];
+      uint32_t ks[TASKS], vs[TASKS];
+      bool missing[TASKS];
+    };
+    const int64_t pages = a.cache.pages, heads = a.cache.heads;
+    auto load = [&](int step, const int (&page)[TASKS], Raw &raw) {
+#pragma unroll
+      for (int i = 0; i < TASKS; i++) {
+        uint32_t pg, off;
+        p.page.split((uint32_t)token(step, i), pg, off);
+        const int n = a.table ? page[i] : t.b;
+        raw.missing[i] = (uint32_t)n >= (uint64_t)pages;
+        const int64_t row = ((raw.missing[i] ? 0 : n) * heads + kh) * (int64_t)p.page.d + off;
+        const int64_t at = row * NB + (tid + 256 * i) % NB;
+        raw.k[i] = *(const u32x4 *)(a.cache.k_codes + 16 * at);
+        raw.ks[i] = a.cache.k_scales[at];
+        raw.v[i] = *(const u32x4 *)(a.cache.v_codes + 16 * at);
+        raw.vs[i] = a.cache.v_scales[at];
+      }
+    };
+    // Keys and values of a step into a buffer.  A thread's four pieces go out in an
+    // order of its own (its dwords are exchanged by two bits of the token), so that
+    // neighbours write to different banks.
+    auto convert = [&](int step, Raw &raw, int buffer) {
+#pragma unroll
+      for (int i = 0; i < TASKS; i++) {
+        const int x = tid + 256 * i, tok = x / NB, blk = x % NB, at = kTok * step + tok;
+        if (kTok * NB % 256 != 0 && x >= kTok * NB) continue;
+        if (at < any_lo || at >= any_hi || raw.missing[i]) raw.v[i] = u32x4{0, 0, 0, 0}, raw.vs[i] = 127;
+        if (kv_nan(raw.vs[i])) {  // put right behind the products
+          raw.v[i] = u32x4{0, 0, 0, 0}, raw.vs[i] = 127;
+          nans[step & 3] = 1;
+        }
+        if (kv_nan(raw.ks[i]) || raw.missing[i]) raw.ks[i] = 255;
+        const float ks = kv_scale(raw.ks[i]), vs = kv_scale(raw.vs[i]);
+        const int turn = tok & 3, sw = swizzle<NB>(tok);
+        auto turned = [&](u32x4 w) {
+          const bool b0 = turn & 1, b1 = turn & 2;
+          w = u32x4{b0 ? w[1] : w[0], b0 ? w[0] : w[1], b0 ? w[3] : w[2], b0 ? w[2] : w[3]};
+          return u32x4{b1 ? w[2] : w[0], b1 ? w[3] : w[1], b1 ? w[0] : w[2], b1 ? w[1] : w[3]};
+        };
+        const u32x4 k = turned(raw.k[i]), v = turned(raw.v[i]);
+        char *kr = &lds[buffer][0][tok * ROWB], *vr = &lds[buffer][1][tok * ROWB];
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          const int piece = (4 * blk + (c ^ turn)) ^ sw;
+          *(bf16x8 *)(kr + 16 * piece) = fp4x8(k[c], ks);
+          *(bf16x8 *)(vr + 16 * piece) = fp4x8(v[c], vs);
+        }
+      }
+    };
+
+    Raw raw;
+    int page[TASKS];
+    __syncthreads();  // the buffers and flags of the group before are read
+    if (tid < 4) nans[tid] = 0;
+    if (step0 < step1) {
+      int first[TASKS];
+      entry(step0, first);
+      entry(step0 + 1, page);
+      load(step0, first, raw);
+    }
+
+    // the rows of this lane's columns, their tokens and operands; columns behind the
+    // last row repeat it and see nothing
+    int lo[QT], hi[QT];
+    bf16x8 qf[QT][HD / 16][NQ];
+#pragma unroll
+    for (int x = 0; x < QT; x++) {
+      const int r = t.row0 + 32 * (QT * wave + x) + col;
+      uint32_t i, h;
+      p.share.split((uint32_t)(r < t.rows ? r : t.rows - 1), i, h);
+      seen(a, t, (int)i, lo[x], hi[x]);
+      if (r >= t.rows) lo[x] = hi[x] = 0;
+      const T *q = (const T *)a.q + (t.start + (int64_t)i) * a.q_token + ((int64_t)kh * p.share.d + h) * a.q_head;
+#pragma unroll
+      for (int s = 0; s < HD / 16; s++) {
+        float v[8];
+        load8(q + 16 * s + 8 * half, v);
+        if (a.scale < 0.f)
+#pragma unroll
+          for (int k = 0; k < 8; k++) v[k] = -v[k];
+        split8<NQ>(v, qf[x][s]);
+      }
+    }
+    f32x16 o[QT][NB];
+    float m[QT], l[QT];
+#pragma unroll
+    for (int x = 0; x < QT; x++) {
+      m[x] = -kInf, l[x] = 0.f;
+#pragma unroll
+      for (int d = 0; d < NB; d++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) o[x][d][e] = 0.f;
+    }
+    __syncthreads();  // the flags are clear
+    if (step0 < step1) {
+      convert(step0, raw, step0 & 1);
+      load(step0 + 1, page, raw);
+      entry(step0 + 2, page);
+    }
+
+    for (int step = step0; step < step1; step++) {
+      __syncthreads();  // this step's buffer is written, the other one read
+      const int buffer = step & 1;
+      if (step + 1 < step1) {
+        convert(step + 1, raw, buffer ^ 1);
+        load(step + 2, page, raw);
+        entry(step + 3, page);
+      }
+      if (tid == 0) nans[(step + 3) & 3] = 0;
+      const char *kb = lds[buffer][0], *vb = lds[buffer][1];
+#pragma unroll
+      for (int i = 0; i < 2; i++) {  // 32 tokens
+        f32x16 s[QT];
+#pragma unroll
+        for (int x = 0; x < QT; x++)
+#pragma unroll
+          for (int e = 0; e < 16; e++) s[x][e] = 0.f;
+        {
+          const int tok = 32 * i + col, sw = swizzle<NB>(tok);
+#pragma unroll
+          for (int c = 0; c < HD / 16; c++) {
+            const bf16x8 k = *(const bf16x8 *)(kb + tok * ROWB + 16 * ((2 * c + half) ^ sw));
+#pragma unroll
+            for (int x = 0; x < QT; x++)
+#pragma unroll
+              for (int n = NQ - 1; n >= 0; n--)  // small parts first
+                s[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[x][c][n], s[x], 0, 0, 0);
+          }
+        }
+        const int at = kTok * step + 32 * i;
+        bf16x8 pf[QT][2][NQ];
+#pragma unroll
+        for (int x = 0; x < QT; x++) {
+          // tokens that not every row sees: rare, and a loop, which stays a branch
+          int edges = uniform(at < all_lo || at + 32 > all_hi);
+          asm volatile("" : "+s"(edges));
+          for (; edges; edges = 0) {
+            const int a0 = lo[x] - at - 4 * half, a1 = hi[x] - at - 4 * half;
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+              const int tok = (e & 3) + 8 * (e >> 2);
+              if (tok < a0 || tok >= a1) s[x][e] = -kInf;
+            }
+          }
+          float top = s[x][0];
+#pragma unroll
+          for (int e = 1; e < 16; e++) top = fmaxf(top, s[x][e]);
+          const uint32_t tb = __float_as_uint(top);
+          const auto other = __builtin_amdgcn_permlane32_swap(tb, tb, false, false);
+          top = fmaxf(__uint_as_float(other[0]), __uint_as_float(other[1])) * p.log2_scale;
+          // the maximum follows only where weights could pass 2^8: they keep their
+          // relative accuracy up to there
+          if (__any(top > m[x] + 8.f)) {
+            top = fmaxf(m[x], top);
+            const float old = __builtin_amdgcn_exp2f(m[x] - (top == -kInf ? 0.f : top));
+            l[x] *= old;
+#pragma unroll
+            for (int d = 0; d < NB; d++) o[x][d] *= old;
+            m[x] = top;
+          }
+          // a row that sees nothing yet keeps -infinity; 0 stands for it here
+          const float base = m[x] == -kInf ? 0.f : m[x];
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 16; e++) {
+            v[e] = __builtin_amdgcn_exp2f(fmaf(s[x][e], p.log2_scale, -base));
+            l[x] += v[e];
+          }
+          split8<NQ>(v, pf[x][0]);
+          split8<NQ>(v + 8, pf[x][1]);
+        }
+        // transposed reads: lanes 4j .. 4j+3 of 16 name token j's 16 elements
+        const int j = (lane & 15) >> 2, c = lane & 3, which = lane >> 4 & 1;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int tok = 32 * i + 16 * h + 4 * half + j;
+#pragma unroll
+          for (int d = 0; d < NB; d++) {
+            const int piece = 4 * d + 2 * which + (c >> 1);
+            const i16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_i16x4 *)(vb + tok * ROWB + 16 * (piece ^ swizzle<NB>(tok)) + 8 * (c & 1)));
+            const i16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_i16x4 *)(vb + (tok + 8) * ROWB + 16 * (piece ^ swizzle<NB>(tok + 8)) + 8 * (c & 1)));
+            const bf16x8 vt = __builtin_bit_cast(bf16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int x = 0; x < QT; x++)
+#pragma unroll
+              for (int n = NQ - 1; n >= 0; n--)
+                o[x][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt, pf[x][h][n], o[x][d], 0, 0, 0);
+          }
+        }
+      }
+      if (uniform(nans[step & 3])) {
+        // blocks of NaN among the values: NaN for the rows that see their tokens
+        for (int tok = kTok * step; tok < kTok * step + kTok; tok++) {
+          if (tok < any_lo || tok >= any_hi) continue;
+          uint32_t pg, off;
+          p.page.split((uint32_t)tok, pg, off);
+          const int n = a.table ? table[pg] : t.b;
+          if ((uint32_t)n >= (uint64_t)pages) continue;
+          const int64_t row = (n * heads + kh) * (int64_t)p.page.d + off;
+#pragma unroll
+          for (int d = 0; d < NB; d++)
+            if (kv_nan(a.cache.v_scales[row * NB + d]))
+#pragma unroll
+              for (int x = 0; x < QT; x++)
+                if (tok >= lo[x] && tok < hi[x]) o[x][d] += __builtin_nanf("");
+        }
+      }
+    }
+
+#pragma unroll
+    for (int x = 0; x < QT; x++) {
+      const int r = t.row0 + 32 * (QT * wave + x) + col;
+      const uint32_t lb = __float_as_uint(l[x]);
+      const auto other = __builtin_amdgcn_permlane32_swap(lb, lb, false, false);
+      const float sum = __uint_as_float(other[0]) + __uint_as_float(other[1]);
+      if (r >= t.rows || r >= t.row0 + p.rows) continue;
+      uint32_t i, h;
+      p.share.split((uint32_t)r, i, h);
+      const int64_t tok = t.start + (int64_t)i, head = (int64_t)kh * p.share.d + h;
+      const int64_t at = (int64_t)slot * p.rows + (r - t.row0);
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int d = 0; d < NB; d++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          f32x4 v = {o[x][d][4 * e], o[x][d][4 * e + 1], o[x][d][4 * e + 2], o[x][d][4 * e + 3]};
+          const int el = 32 * d + 8 * e + 4 * half;
+          if (slot < 0)
+            store4((T *)a.out + tok * a.out_token + head * a.out_head + el,
+                   sum == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : v * inv);
+          else if (sum != 0.f)
+            *(f32x4 *)(p.part + at * HD + el) = v;
+        }
+      if (half == 0) {
+        if (slot >= 0) p.part_ml[at] = f32x2{m[x], sum};
+        else if (a.lse) a.lse[tok * a.q_heads + head] = lse_of(m[x], sum);
+      }
+    }
+  }
+}
+
+template <int NB>
+void launch(const KvLaunch &p, dim3 grid) {
+  if (p.a.dtype == 0) hipLaunchKernelGGL((kv_tiles_kernel<NB, 1, true>), grid, dim3(256), 0, p.a.stream, p);
+  else if constexpr (NB <= 4) hipLaunchKernelGGL((kv_tiles_kernel<NB, 2, false>), grid, dim3(256), 0, p.a.stream, p);
+  else hipLaunchKernelGGL((kv_tiles_kernel<NB, 1, false>), grid, dim3(256), 0, p.a.stream, p);
+}
+
+}  // namespace
+
+hipError_t launch_kv_tiles(const KvLaunch &p) {
+  const dim3 grid(p.workers ? (unsigned)p.workers : (unsigned)p.count, p.workers ? 1u : (unsigned)p.a.cache.heads);
+  switch (p.a.cache.head_dim / 32) {
+#define OQ_CASE(NB) \
+  case NB: launch<NB>(p, grid); break;
+    OQ_CASE(1) OQ_CASE(2) OQ_CASE(3) OQ_CASE(4) OQ_CASE(5) OQ_CASE(6) OQ_CASE(7) OQ_CASE(8)
+#undef OQ_CASE
+  }
+  return hipGetLastError();
+}
+
+}  // namespace oq
