@@ -264,7 +264,7 @@ __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -k
 constexpr int kv_rows_step(int head_dim) { return head_dim <= 128 ? 64 : 32; }
 hipError_t launch_kv_rows(const KvLaunch &p);
 // rows of a workgroup's tile and tokens a step of the tiles kernel
-constexpr int kv_tiles_rows(int dtype, int head_dim) { return dtype == 0 || head_dim > 128 ? 128 : 256; }
+constexpr int kv_tiles_rows(int dtype, int head_dim) { return head_dim > (dtype == 0 ? 64 : 128) ? 128 : 256; }
 constexpr int kKvTilesStep = 64;
 hipError_t launch_kv_tiles(const KvLaunch &p);
 

@@ -20,6 +20,8 @@ namespace {
 
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8;
+typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kTok = kKvTilesStep;
 
@@ -34,10 +36,22 @@ __device__ __forceinline__ int swizzle(int tok) {
   return ((tok & 3) >> (2 - HIGH) << 2) | (tok >> 2 & 3);
 }
 
-template <int NB, int QT, bool F32>
-__global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
+// Scores of tokens outside [a0, a1) (counted from the lane's first) to -infinity.
+// Rare: the empty asm keeps the compiler from doing it every time.
+__device__ __forceinline__ void hide(f32x16 &s, int a0, int a1) {
+#pragma unroll
+  for (int e = 0; e < 16; e++) {
+    const int tok = (e & 3) + 8 * (e >> 2);
+    float v = tok < a0 || tok >= a1 ? -kInf : s[e];
+    asm volatile("" : "+v"(v));
+    s[e] = v;
+  }
+}
+
+template <int NB, int WAVES, bool F32>
+__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void kv_tiles_kernel(KvLaunch p) {
   using T = typename std::conditional<F32, float, uint16_t>::type;
-  constexpr int HD = 32 * NB, ROWB = 2 * HD, NQ = F32 ? 3 : 1, TASKS = (kTok * NB + 255) / 256;
+  constexpr int HD = 32 * NB, ROWB = 2 * HD, NQ = F32 ? 3 : 1, TASKS = (2 * NB + WAVES - 1) / WAVES;
   __shared__ __attribute__((aligned(16))) char lds[2][2][kTok * ROWB];  // [buffer][keys, values]
   __shared__ int nans[4];  // by step modulo 4: blocks of NaN among the values
   const KvAttentionArgs &a = p.a;
@@ -80,13 +94,18 @@ __global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
     const int step0 = any_lo / kTok > g0 ? any_lo / kTok : g0;
     const int step1 = any_hi <= any_lo ? step0 : (any_hi + kTok - 1) / kTok < g1 ? (any_hi + kTok - 1) / kTok : g1;
 
-    // Conversion: task x of a step is block x % NB of token x / NB, for keys and
-    // values; a thread has TASKS of them.
+    // Conversion: task x of a step is block x % NB of token x / NB, first of the keys,
+    // then of the values; a thread has TASKS of them, a wave's all of one kind.
     const int last_tok = (kTok * step1 < any_hi ? kTok * step1 : any_hi) - 1;
     const int32_t *table = a.table ? a.table + (int64_t)t.b * a.table_pages : a.lengths + t.b;
     const uint32_t mask = a.table ? ~0u : 0u;
+    auto values = [&](int i) { return wave + WAVES * i >= NB; };
+    auto task = [&](int i) {
+      const int x = tid + 64 * WAVES * i;
+      return x < kTok * NB ? x : x < 2 * kTok * NB ? x - kTok * NB : kTok * NB - 1;
+    };
     auto token = [&](int step, int i) {
-      const int x = tid + 256 * i, tok = kTok * step + (x < kTok * NB ? x / NB : kTok - 1);
+      const int tok = kTok * step + task(i) / NB;
       return tok < last_tok ? tok : last_tok;
     };
     auto entry = [&](int step, int (&page)[TASKS]) {
@@ -94,8 +113,8 @@ __global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
       for (int i = 0; i < TASKS; i++) page[i] = table[p.page.div((uint32_t)token(step, i)) & mask];
     };
     struct Raw {
-      u32x4 k[TASKS], v[TASKS];
-      uint32_t ks[TASKS], vs[TASKS];
+      u32x4 c[TASKS];
+      uint32_t s[TASKS];
       bool missing[TASKS];
     };
     const int64_t pages = a.cache.pages, heads = a.cache.heads;
@@ -107,42 +126,36 @@ __global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
         const int n = a.table ? page[i] : t.b;
         raw.missing[i] = (uint32_t)n >= (uint64_t)pages;
         const int64_t row = ((raw.missing[i] ? 0 : n) * heads + kh) * (int64_t)p.page.d + off;
-        const int64_t at = row * NB + (tid + 256 * i) % NB;
-        raw.k[i] = *(const u32x4 *)(a.cache.k_codes + 16 * at);
-        raw.ks[i] = a.cache.k_scales[at];
-        raw.v[i] = *(const u32x4 *)(a.cache.v_codes + 16 * at);
-        raw.vs[i] = a.cache.v_scales[at];
+        const int64_t at = row * NB + task(i) % NB;
+        raw.c[i] = *(const u32x4 *)((values(i) ? a.cache.v_codes : a.cache.k_codes) + 16 * at);
+        raw.s[i] = (values(i) ? a.cache.v_scales : a.cache.k_scales)[at];
       }
     };
-    // Keys and values of a step into a buffer.  A thread's four pieces go out in an
+    // A step's keys and values into a buffer.  A thread's four pieces go out in an
     // order of its own (its dwords are exchanged by two bits of the token), so that
     // neighbours write to different banks.
     auto convert = [&](int step, Raw &raw, int buffer) {
 #pragma unroll
       for (int i = 0; i < TASKS; i++) {
-        const int x = tid + 256 * i, tok = x / NB, blk = x % NB, at = kTok * step + tok;
-        if (kTok * NB % 256 != 0 && x >= kTok * NB) continue;
-        if (at < any_lo || at >= any_hi || raw.missing[i]) raw.v[i] = u32x4{0, 0, 0, 0}, raw.vs[i] = 127;
-        if (kv_nan(raw.vs[i])) {  // put right behind the products
-          raw.v[i] = u32x4{0, 0, 0, 0}, raw.vs[i] = 127;
-          nans[step & 3] = 1;
+        if (wave + WAVES * i >= 2 * NB) break;
+        const int x = task(i), tok = x / NB, blk = x % NB, at = kTok * step + tok;
+        const bool nan = kv_nan(raw.s[i]);
+        if (values(i)) {
+          if (at < any_lo || at >= any_hi || raw.missing[i]) raw.c[i] = u32x4{0, 0, 0, 0}, raw.s[i] = 127;
+          else if (nan) raw.c[i] = u32x4{0, 0, 0, 0}, raw.s[i] = 127, nans[step & 3] = 1;  // put right behind the products
+        } else if (nan || raw.missing[i]) {
+          raw.s[i] = 255;
         }
-        if (kv_nan(raw.ks[i]) || raw.missing[i]) raw.ks[i] = 255;
-        const float ks = kv_scale(raw.ks[i]), vs = kv_scale(raw.vs[i]);
-        const int turn = tok & 3, sw = swizzle<NB>(tok);
-        auto turned = [&](u32x4 w) {
-          const bool b0 = turn & 1, b1 = turn & 2;
-          w = u32x4{b0 ? w[1] : w[0], b0 ? w[0] : w[1], b0 ? w[3] : w[2], b0 ? w[2] : w[3]};
-          return u32x4{b1 ? w[2] : w[0], b1 ? w[3] : w[1], b1 ? w[0] : w[2], b1 ? w[1] : w[3]};
-        };
-        const u32x4 k = turned(raw.k[i]), v = turned(raw.v[i]);
-        char *kr = &lds[buffer][0][tok * ROWB], *vr = &lds[buffer][1][tok * ROWB];
+        const float scale = kv_scale(raw.s[i]);
+        const bool b0 = tok & 1, b1 = tok & 2;
+        u32x4 w = raw.c[i];
+        w = u32x4{b0 ? w[1] : w[0], b0 ? w[0] : w[1], b0 ? w[3] : w[2], b0 ? w[2] : w[3]};
+        w = u32x4{b1 ? w[2] : w[0], b1 ? w[3] : w[1], b1 ? w[0] : w[2], b1 ? w[1] : w[3]};
+        char *row = &lds[buffer][values(i)][tok * ROWB];
+        const int sw = swizzle<NB>(tok);
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-          const int piece = (4 * blk + (c ^ turn)) ^ sw;
-          *(bf16x8 *)(kr + 16 * piece) = fp4x8(k[c], ks);
-          *(bf16x8 *)(vr + 16 * piece) = fp4x8(v[c], vs);
-        }
+        for (int c = 0; c < 4; c++)
+          *(bf16x8 *)(row + 16 * ((4 * blk + (c ^ (tok & 3))) ^ sw)) = fp4x8(w[c], scale);
       }
     };
 
@@ -157,17 +170,16 @@ __global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
       load(step0, first, raw);
     }
 
-    // the rows of this lane's columns, their tokens and operands; columns behind the
-    // last row repeat it and see nothing
-    int lo[QT], hi[QT];
-    bf16x8 qf[QT][HD / 16][NQ];
-#pragma unroll
-    for (int x = 0; x < QT; x++) {
-      const int r = t.row0 + 32 * (QT * wave + x) + col;
+    // the row of this lane's column, its tokens and operands; columns behind the last
+    // row repeat it and see nothing
+    int lo, hi;
+    bf16x8 qf[HD / 16][NQ];
+    {
+      const int r = t.row0 + 32 * wave + col;
       uint32_t i, h;
       p.share.split((uint32_t)(r < t.rows ? r : t.rows - 1), i, h);
-      seen(a, t, (int)i, lo[x], hi[x]);
-      if (r >= t.rows) lo[x] = hi[x] = 0;
+      seen(a, t, (int)i, lo, hi);
+      if (r >= t.rows) lo = hi = 0;
       const T *q = (const T *)a.q + (t.start + (int64_t)i) * a.q_token + ((int64_t)kh * p.share.d + h) * a.q_head;
 #pragma unroll
       for (int s = 0; s < HD / 16; s++) {
@@ -176,18 +188,33 @@ __global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
         if (a.scale < 0.f)
 #pragma unroll
           for (int k = 0; k < 8; k++) v[k] = -v[k];
-        split8<NQ>(v, qf[x][s]);
+        split8<NQ>(v, qf[s]);
       }
     }
-    f32x16 o[QT][NB];
-    float m[QT], l[QT];
+    f32x16 o[NB];
+    float m = -kInf, l = 0.f;
 #pragma unroll
-    for (int x = 0; x < QT; x++) {
-      m[x] = -kInf, l[x] = 0.f;
+    for (int d = 0; d < NB; d++)
 #pragma unroll
-      for (int d = 0; d < NB; d++)
+      for (int e = 0; e < 16; e++) o[d][e] = 0.f;
+    // LDS addresses of the operands' reads: of keys a row a lane, of values (transposed:
+    // lanes 4j .. 4j+3 of 16 name token j's 16 elements) rows j and j + 8 of 16.  They
+    // change from buffer to buffer with the step; 16 and 32 tokens on is an offset, as
+    // the swizzle is the same there.
+    constexpr uint32_t BUFFER = 2 * kTok * ROWB;
+    uint32_t k_at[HD / 16], v_at[NB][2];
+    {
+      const uint32_t base = (uint32_t)(uintptr_t)(lds_char *)&lds[0][0][0] + (step0 & 1) * BUFFER;
 #pragma unroll
-        for (int e = 0; e < 16; e++) o[x][d][e] = 0.f;
+      for (int c = 0; c < HD / 16; c++) k_at[c] = base + col * ROWB + 16 * ((2 * c + half) ^ swizzle<NB>(col));
+      const int c = lane & 3, which = lane >> 4 & 1;
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        const int tok = 4 * half + ((lane & 15) >> 2) + 8 * k;
+#pragma unroll
+        for (int d = 0; d < NB; d++)
+          v_at[d][k] = base + kTok * ROWB + tok * ROWB + 16 * ((4 * d + 2 * which + (c >> 1)) ^ swizzle<NB>(tok)) + 8 * (c & 1);
+      }
     }
     __syncthreads();  // the flags are clear
     if (step0 < step1) {
@@ -205,89 +232,67 @@ __global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
         entry(step + 3, page);
       }
       if (tid == 0) nans[(step + 3) & 3] = 0;
-      const char *kb = lds[buffer][0], *vb = lds[buffer][1];
+      const bool edge = kTok * step < all_lo || kTok * step + kTok > all_hi;
+      {
 #pragma unroll
-      for (int i = 0; i < 2; i++) {  // 32 tokens
-        f32x16 s[QT];
+        for (int i = 0; i < 2; i++) {  // 32 tokens
+          f32x16 s;
 #pragma unroll
-        for (int x = 0; x < QT; x++)
-#pragma unroll
-          for (int e = 0; e < 16; e++) s[x][e] = 0.f;
-        {
-          const int tok = 32 * i + col, sw = swizzle<NB>(tok);
+          for (int e = 0; e < 16; e++) s[e] = 0.f;
 #pragma unroll
           for (int c = 0; c < HD / 16; c++) {
-            const bf16x8 k = *(const bf16x8 *)(kb + tok * ROWB + 16 * ((2 * c + half) ^ sw));
+            const bf16x8 k = *(lds_bf16x8 *)(uintptr_t)(k_at[c] + 32 * i * ROWB);
 #pragma unroll
-            for (int x = 0; x < QT; x++)
-#pragma unroll
-              for (int n = NQ - 1; n >= 0; n--)  // small parts first
-                s[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[x][c][n], s[x], 0, 0, 0);
+            for (int n = NQ - 1; n >= 0; n--)  // small parts first
+              s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[c][n], s, 0, 0, 0);
           }
-        }
-        const int at = kTok * step + 32 * i;
-        bf16x8 pf[QT][2][NQ];
+          if (edge) hide(s, lo - (kTok * step + 32 * i + 4 * half), hi - (kTok * step + 32 * i + 4 * half));
+          float top = s[0];
 #pragma unroll
-        for (int x = 0; x < QT; x++) {
-          // tokens that not every row sees: rare, and a loop, which stays a branch
-          int edges = uniform(at < all_lo || at + 32 > all_hi);
-          asm volatile("" : "+s"(edges));
-          for (; edges; edges = 0) {
-            const int a0 = lo[x] - at - 4 * half, a1 = hi[x] - at - 4 * half;
-#pragma unroll
-            for (int e = 0; e < 16; e++) {
-              const int tok = (e & 3) + 8 * (e >> 2);
-              if (tok < a0 || tok >= a1) s[x][e] = -kInf;
-            }
-          }
-          float top = s[x][0];
-#pragma unroll
-          for (int e = 1; e < 16; e++) top = fmaxf(top, s[x][e]);
+          for (int e = 1; e < 16; e++) top = fmaxf(top, s[e]);
           const uint32_t tb = __float_as_uint(top);
           const auto other = __builtin_amdgcn_permlane32_swap(tb, tb, false, false);
           top = fmaxf(__uint_as_float(other[0]), __uint_as_float(other[1])) * p.log2_scale;
           // the maximum follows only where weights could pass 2^8: they keep their
           // relative accuracy up to there
-          if (__any(top > m[x] + 8.f)) {
-            top = fmaxf(m[x], top);
-            const float old = __builtin_amdgcn_exp2f(m[x] - (top == -kInf ? 0.f : top));
-            l[x] *= old;
+          if (__any(top > m + 8.f)) {
+            top = fmaxf(m, top);
+            const float old = __builtin_amdgcn_exp2f(m - (top == -kInf ? 0.f : top));
+            l *= old;
 #pragma unroll
-            for (int d = 0; d < NB; d++) o[x][d] *= old;
-            m[x] = top;
+            for (int d = 0; d < NB; d++) o[d] *= old;
+            m = top;
           }
           // a row that sees nothing yet keeps -infinity; 0 stands for it here
-          const float base = m[x] == -kInf ? 0.f : m[x];
+          const float base = m == -kInf ? 0.f : m;
           float v[16];
 #pragma unroll
           for (int e = 0; e < 16; e++) {
-            v[e] = __builtin_amdgcn_exp2f(fmaf(s[x][e], p.log2_scale, -base));
-            l[x] += v[e];
+            v[e] = __builtin_amdgcn_exp2f(fmaf(s[e], p.log2_scale, -base));
+            l += v[e];
           }
-          split8<NQ>(v, pf[x][0]);
-          split8<NQ>(v + 8, pf[x][1]);
-        }
-        // transposed reads: lanes 4j .. 4j+3 of 16 name token j's 16 elements
-        const int j = (lane & 15) >> 2, c = lane & 3, which = lane >> 4 & 1;
+          bf16x8 pf[2][NQ];
+          split8<NQ>(v, pf[0]);
+          split8<NQ>(v + 8, pf[1]);
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const int tok = 32 * i + 16 * h + 4 * half + j;
+          for (int h = 0; h < 2; h++) {
 #pragma unroll
-          for (int d = 0; d < NB; d++) {
-            const int piece = 4 * d + 2 * which + (c >> 1);
-            const i16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_i16x4 *)(vb + tok * ROWB + 16 * (piece ^ swizzle<NB>(tok)) + 8 * (c & 1)));
-            const i16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_i16x4 *)(vb + (tok + 8) * ROWB + 16 * (piece ^ swizzle<NB>(tok + 8)) + 8 * (c & 1)));
-            const bf16x8 vt = __builtin_bit_cast(bf16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-            for (int x = 0; x < QT; x++)
+            for (int d = 0; d < NB; d++) {
+              const uint32_t on = (32 * i + 16 * h) * ROWB;
+              const i16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(uintptr_t)(v_at[d][0] + on));
+              const i16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(uintptr_t)(v_at[d][1] + on));
+              const bf16x8 vt = __builtin_bit_cast(bf16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
               for (int n = NQ - 1; n >= 0; n--)
-                o[x][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt, pf[x][h][n], o[x][d], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt, pf[h][n], o[d], 0, 0, 0);
+            }
           }
         }
       }
+#pragma unroll
+      for (int c = 0; c < HD / 16; c++) k_at[c] += buffer ? -BUFFER : BUFFER;
+#pragma unroll
+      for (int d = 0; d < NB; d++) v_at[d][0] += buffer ? -BUFFER : BUFFER, v_at[d][1] += buffer ? -BUFFER : BUFFER;
       if (uniform(nans[step & 3])) {
         // blocks of NaN among the values: NaN for the rows that see their tokens
         for (int tok = kTok * step; tok < kTok * step + kTok; tok++) {
@@ -299,21 +304,17 @@ __global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
           const int64_t row = (n * heads + kh) * (int64_t)p.page.d + off;
 #pragma unroll
           for (int d = 0; d < NB; d++)
-            if (kv_nan(a.cache.v_scales[row * NB + d]))
-#pragma unroll
-              for (int x = 0; x < QT; x++)
-                if (tok >= lo[x] && tok < hi[x]) o[x][d] += __builtin_nanf("");
+            if (kv_nan(a.cache.v_scales[row * NB + d]) && tok >= lo && tok < hi)
+              o[d] += __builtin_nanf("");
         }
       }
     }
 
-#pragma unroll
-    for (int x = 0; x < QT; x++) {
-      const int r = t.row0 + 32 * (QT * wave + x) + col;
-      const uint32_t lb = __float_as_uint(l[x]);
-      const auto other = __builtin_amdgcn_permlane32_swap(lb, lb, false, false);
-      const float sum = __uint_as_float(other[0]) + __uint_as_float(other[1]);
-      if (r >= t.rows || r >= t.row0 + p.rows) continue;
+    const int r = t.row0 + 32 * wave + col;
+    const uint32_t lb = __float_as_uint(l);
+    const auto other = __builtin_amdgcn_permlane32_swap(lb, lb, false, false);
+    const float sum = __uint_as_float(other[0]) + __uint_as_float(other[1]);
+    if (r < t.rows) {
       uint32_t i, h;
       p.share.split((uint32_t)r, i, h);
       const int64_t tok = t.start + (int64_t)i, head = (int64_t)kh * p.share.d + h;
@@ -323,7 +324,7 @@ __global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
       for (int d = 0; d < NB; d++)
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          f32x4 v = {o[x][d][4 * e], o[x][d][4 * e + 1], o[x][d][4 * e + 2], o[x][d][4 * e + 3]};
+          f32x4 v = {o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
           const int el = 32 * d + 8 * e + 4 * half;
           if (slot < 0)
             store4((T *)a.out + tok * a.out_token + head * a.out_head + el,
@@ -332,8 +333,8 @@ __global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
             *(f32x4 *)(p.part + at * HD + el) = v;
         }
       if (half == 0) {
-        if (slot >= 0) p.part_ml[at] = f32x2{m[x], sum};
-        else if (a.lse) a.lse[tok * a.q_heads + head] = lse_of(m[x], sum);
+        if (slot >= 0) p.part_ml[at] = f32x2{m, sum};
+        else if (a.lse) a.lse[tok * a.q_heads + head] = lse_of(m, sum);
       }
     }
   }
@@ -341,9 +342,9 @@ __global__ __launch_bounds__(256, 1) void kv_tiles_kernel(KvLaunch p) {
 
 template <int NB>
 void launch(const KvLaunch &p, dim3 grid) {
-  if (p.a.dtype == 0) hipLaunchKernelGGL((kv_tiles_kernel<NB, 1, true>), grid, dim3(256), 0, p.a.stream, p);
-  else if constexpr (NB <= 4) hipLaunchKernelGGL((kv_tiles_kernel<NB, 2, false>), grid, dim3(256), 0, p.a.stream, p);
-  else hipLaunchKernelGGL((kv_tiles_kernel<NB, 1, false>), grid, dim3(256), 0, p.a.stream, p);
+  constexpr int W16 = kv_tiles_rows(1, 32 * NB) / 32, W32 = kv_tiles_rows(0, 32 * NB) / 32;
+  if (p.a.dtype == 1) hipLaunchKernelGGL((kv_tiles_kernel<NB, W16, false>), grid, dim3(64 * W16), 0, p.a.stream, p);
+  else hipLaunchKernelGGL((kv_tiles_kernel<NB, W32, true>), grid, dim3(64 * W32), 0, p.a.stream, p);
 }
 
 }  // namespace
