@@ -54,6 +54,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void kv_tiles_kernel(KvLaunc
   constexpr int HD = 32 * NB, ROWB = 2 * HD, NQ = F32 ? 3 : 1, TASKS = (2 * NB + WAVES - 1) / WAVES;
   __shared__ __attribute__((aligned(16))) char lds[2][2][kTok * ROWB];  // [buffer][keys, values]
   __shared__ int nans[4];  // by step modulo 4: blocks of NaN among the values
+  constexpr int AHEAD = NB == 1 ? 4 : 4;
   const KvAttentionArgs &a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
   const int wave = uniform(tid >> 6);
@@ -232,62 +233,91 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void kv_tiles_kernel(KvLaunc
         entry(step + 3, page);
       }
       if (tid == 0) nans[(step + 3) & 3] = 0;
-      const bool edge = kTok * step < all_lo || kTok * step + kTok > all_hi;
-      {
+      // Reads run AHEAD products ahead, in this order: left to itself the compiler waits
+      // for each.
+      f32x16 s[2];
 #pragma unroll
-        for (int i = 0; i < 2; i++) {  // 32 tokens
-          f32x16 s;
+      for (int i = 0; i < 2; i++)
 #pragma unroll
-          for (int e = 0; e < 16; e++) s[e] = 0.f;
+        for (int e = 0; e < 16; e++) s[i][e] = 0.f;
+      auto key = [&](int c) { return *(lds_bf16x8 *)(uintptr_t)(k_at[c % (HD / 16)] + c / (HD / 16) * 32 * ROWB); };
+      bf16x8 kf[AHEAD];
 #pragma unroll
-          for (int c = 0; c < HD / 16; c++) {
-            const bf16x8 k = *(lds_bf16x8 *)(uintptr_t)(k_at[c] + 32 * i * ROWB);
+      for (int c = 0; c < AHEAD; c++) kf[c] = key(c);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int n = NQ - 1; n >= 0; n--)  // small parts first
-              s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, qf[c][n], s, 0, 0, 0);
-          }
-          if (edge) hide(s, lo - (kTok * step + 32 * i + 4 * half), hi - (kTok * step + 32 * i + 4 * half));
-          float top = s[0];
+      for (int c = 0; c < HD / 8; c++) {
+        f32x16 &to = s[c / (HD / 16)];
 #pragma unroll
-          for (int e = 1; e < 16; e++) top = fmaxf(top, s[e]);
-          const uint32_t tb = __float_as_uint(top);
-          const auto other = __builtin_amdgcn_permlane32_swap(tb, tb, false, false);
-          top = fmaxf(__uint_as_float(other[0]), __uint_as_float(other[1])) * p.log2_scale;
-          // the maximum follows only where weights could pass 2^8: they keep their
-          // relative accuracy up to there
-          if (__any(top > m + 8.f)) {
-            top = fmaxf(m, top);
-            const float old = __builtin_amdgcn_exp2f(m - (top == -kInf ? 0.f : top));
-            l *= old;
+        for (int n = NQ - 1; n >= 0; n--)  // small parts first
+          to = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[c % AHEAD], qf[c % (HD / 16)][n], to, 0, 0, 0);
+        if (c + AHEAD < HD / 8) kf[c % AHEAD] = key(c + AHEAD);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // product x of the second: token 16 (x / NB), elements 32 (x % NB)
+      auto value = [&](int x) {
+        const uint32_t on = x / NB * 16 * ROWB;
+        const i16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(uintptr_t)(v_at[x % NB][0] + on));
+        const i16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(uintptr_t)(v_at[x % NB][1] + on));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+      };
+      bf16x8 vf[AHEAD];
 #pragma unroll
-            for (int d = 0; d < NB; d++) o[d] *= old;
-            m = top;
-          }
-          // a row that sees nothing yet keeps -infinity; 0 stands for it here
-          const float base = m == -kInf ? 0.f : m;
-          float v[16];
+      for (int c = 0; c < AHEAD; c++) vf[c] = value(c);
+      __builtin_amdgcn_sched_barrier(0);
+      if (kTok * step < all_lo || kTok * step + kTok > all_hi) {
+        const int first = kTok * step + 4 * half;
+        hide(s[0], lo - first, hi - first);
+        hide(s[1], lo - first - 32, hi - first - 32);
+      }
+      // (the instruction that keeps a NaN: a row with one is NaN, and it takes three)
+      float top = __builtin_elementwise_maximum(s[0][0], s[1][0]);
 #pragma unroll
-          for (int e = 0; e < 16; e++) {
-            v[e] = __builtin_amdgcn_exp2f(fmaf(s[e], p.log2_scale, -base));
-            l += v[e];
-          }
-          bf16x8 pf[2][NQ];
-          split8<NQ>(v, pf[0]);
-          split8<NQ>(v + 8, pf[1]);
+      for (int e = 1; e < 16; e++)
+        top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(top, s[0][e]), s[1][e]);
+      const uint32_t tb = __float_as_uint(top);
+      const auto other = __builtin_amdgcn_permlane32_swap(tb, tb, false, false);
+      top = fmaxf(__uint_as_float(other[0]), __uint_as_float(other[1])) * p.log2_scale;
+      // the maximum follows only where weights could pass 2^8: they keep their relative
+      // accuracy up to there
+      if (__any(top > m + 8.f)) {
+        top = fmaxf(m, top);
+        const float old = __builtin_amdgcn_exp2f(m - (top == -kInf ? 0.f : top));
+        l *= old;
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
+        for (int d = 0; d < NB; d++) o[d] *= old;
+        m = top;
+      }
+      // a row that sees nothing yet keeps -infinity; 0 stands for it here
+      const float base = m == -kInf ? 0.f : m;
+      // the second 32 tokens' weights between the first's products
+      float v[2][16];
+      bf16x8 pf[4][NQ];
+      auto weigh = [&](int i, int e) {
+        v[i][e] = __builtin_amdgcn_exp2f(fmaf(s[i][e], p.log2_scale, -base));
+        l += v[i][e];
+      };
 #pragma unroll
-            for (int d = 0; d < NB; d++) {
-              const uint32_t on = (32 * i + 16 * h) * ROWB;
-              const i16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(uintptr_t)(v_at[d][0] + on));
-              const i16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(uintptr_t)(v_at[d][1] + on));
-              const bf16x8 vt = __builtin_bit_cast(bf16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+      for (int e = 0; e < 16; e++) weigh(0, e);
+      split8<NQ>(v[0], pf[0]);
+      split8<NQ>(v[0] + 8, pf[1]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-              for (int n = NQ - 1; n >= 0; n--)
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vt, pf[h][n], o[d], 0, 0, 0);
-            }
+      for (int x = 0; x < 4 * NB; x++) {
+#pragma unroll
+        for (int n = NQ - 1; n >= 0; n--)
+          o[x % NB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[x % AHEAD], pf[x / NB][n], o[x % NB], 0, 0, 0);
+        if (x + AHEAD < 4 * NB) vf[x % AHEAD] = value(x + AHEAD);
+        if (x < 2 * NB) {
+          constexpr int EACH = (16 + 2 * NB - 1) / (2 * NB);
+#pragma unroll
+          for (int e = EACH * x; e < EACH * (x + 1) && e < 16; e++) weigh(1, e);
+          if (x == 2 * NB - 1) {
+            split8<NQ>(v[1], pf[2]);
+            split8<NQ>(v[1] + 8, pf[3]);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int c = 0; c < HD / 16; c++) k_at[c] += buffer ? -BUFFER : BUFFER;
