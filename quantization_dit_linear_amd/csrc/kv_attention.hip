@@ -97,6 +97,38 @@ __global__ __launch_bounds__(SPLIT ? 1024 : 256) void kv_join_kernel(KvLaunch p)
   }
 }
 
+// The same for tiles of many rows, whose parts are few: four elements a thread.
+template <class T>
+__global__ __launch_bounds__(256) void kv_join_wide_kernel(KvLaunch p) {
+  const KvAttentionArgs &a = p.a;
+  const int2 which = p.parts[(int64_t)blockIdx.x * a.cache.heads + blockIdx.y];
+  const KvTile t = find_tile(p, blockIdx.x);
+  if (t.b < 0) return;
+  const int first = which.x, parts = which.y, hd = a.cache.head_dim, q4 = hd / 4;
+  const int e = (int)blockIdx.z * 256 + (int)threadIdx.x, r = e / q4, d = 4 * (e - r * q4);
+  if (parts == 1 || r >= p.rows || t.row0 + r >= t.rows) return;
+  const auto slot = [&](int k) { return (int64_t)(k == 0 ? first : first - 1 + 2 * k) * p.rows + r; };
+  float top = -kInf, sum = 0.f;
+  for (int k = 0; k < parts; k++) top = fmaxf(top, p.part_ml[slot(k)][0]);
+  const float base = top == -kInf ? 0.f : top;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int k = 0; k < parts; k++) {
+    const f32x2 ml = p.part_ml[slot(k)];
+    if (ml[1] == 0.f) continue;  // a part that saw nothing left no sum
+    const float w = __builtin_amdgcn_exp2f(ml[0] - base);
+    sum += ml[1] * w;
+    v += *(const f32x4 *)(p.part + slot(k) * hd + d) * w;
+  }
+  if (sum == 0.f) v = f32x4{0.f, 0.f, 0.f, 0.f};
+  else v *= 1.f / sum;
+  uint32_t i, h;
+  p.share.split((uint32_t)(t.row0 + r), i, h);
+  const int64_t tok = t.start + (int64_t)i, head = (int64_t)blockIdx.y * p.share.d + h;
+  store4((T *)a.out + tok * a.out_token + head * a.out_head + d, v);
+  if (a.lse && d == 0) a.lse[tok * a.q_heads + head] = lse_of(top, sum);
+}
+
 #ifndef KV_WIDE
 #define KV_WIDE 32
 #endif
@@ -157,8 +189,15 @@ hipError_t launch_kv_attention(const KvAttentionArgs &a) {
   p.parts = (int2 *)(p.part_ml + (int64_t)2 * r.workers * r.rows);
   hipError_t e = r.wide ? launch_kv_tiles(p) : launch_kv_rows(p);
   if (e != hipSuccess || !r.workers) return e;
-  const bool few = tiles * a.cache.heads <= 128 && !r.wide;
-  const dim3 grid((unsigned)tiles, (unsigned)a.cache.heads, few ? r.rows : r.rows / 16);
+  if (r.wide) {
+    const dim3 grid((unsigned)tiles, (unsigned)a.cache.heads, (unsigned)(r.rows * a.cache.head_dim / 4 + 255) / 256);
+    if (a.dtype == 0) hipLaunchKernelGGL((kv_join_wide_kernel<float>), grid, dim3(256), 0, a.stream, p);
+    else hipLaunchKernelGGL((kv_join_wide_kernel<uint16_t>), grid, dim3(256), 0, a.stream, p);
+    return hipGetLastError();
+  }
+  // a workgroup a row where the groups are few
+  const bool few = tiles * a.cache.heads <= 128;
+  const dim3 grid((unsigned)tiles, (unsigned)a.cache.heads, few ? r.rows : 1);
   if (a.dtype == 0) {
     if (few) hipLaunchKernelGGL((kv_join_kernel<float, true>), grid, dim3(1024), 0, a.stream, p);
     else hipLaunchKernelGGL((kv_join_kernel<float, false>), grid, dim3(256), 0, a.stream, p);
