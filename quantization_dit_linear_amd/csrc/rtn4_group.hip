@@ -4,11 +4,16 @@
 //   y[m][n] = bf16( sum_g s_ng sum_{k in g} x_mk (nibble_nk - z_ng) )
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
+#include "kv_cache.h"
 #include "mx_codec.h"
 #include "oq_internal.h"
 
 namespace oq {
 namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ float load_in(const void *x, int dtype, int64_t i) {
   return dtype == 1 ? __builtin_bit_cast(float, (uint32_t)((const uint16_t *)x)[i] << 16) : ((const float *)x)[i];
@@ -59,27 +64,228 @@ __global__ __launch_bounds__(256) void rtn4_group_prepare_kernel(const void *__r
   }
 }
 
-// One wave an output row, 8 coordinates a lane and step; rows of x in turn.
-__global__ __launch_bounds__(256) void rtn4_group_linear_kernel(Rtn4GroupArgs a) {
-  const int lane = threadIdx.x & 63, words = a.K / 8, groups = a.K / a.group;
-  const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (n >= a.N) return;
-  for (int64_t m = 0; m < a.M; m++) {
-    float sum = 0.f;
-    for (int w = lane; w < words; w += 64) {
-      const int64_t g = n * groups + 8 * w / a.group;
-      const float z = a.zeros ? load_in(a.zeros, a.scale_dtype, g) : 8.f;
-      const uint32_t q = ((const uint32_t *)a.q4)[n * words + w];
-      float v[8], t = 0.f;
-      if (a.dtype == 1) load8((const uint16_t *)a.x + m * a.K + 8 * w, v);
-      else load8((const float *)a.x + m * a.K + 8 * w, v);
+constexpr int kWaves = 8;
+
+// 16 NT columns of y by 16 MT rows of x a workgroup, whose eight waves share K.  A
+// step is 128 coordinates.  Four lanes load 64 bytes of a weight row, and as many as
+// its 32 coordinates take a part of an activation row; through LDS of the wave's own
+// they come to the lanes that the products want.  G128: groups are whole steps.  XR:
+// the rows of x that there can be in a tile, 4 or 16; 4 are repeated.
+template <int MT, int NT, int XR, bool G128, bool F32>
+__global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4GroupArgs a, FastDiv per_group) {
+  constexpr int NQ = F32 ? 3 : 1, ES = F32 ? 4 : 2, XV = ES / 2;  // XV: 16-byte parts of 8 activations
+  constexpr int C = XR == 4 ? 16 : 4 * XV, R = 64 / C;            // a load of x: rows and parts of a row
+  constexpr int XD = XR == 4 ? 4 / XV : 1;                        // and the products that it serves
+  constexpr int XL = MT * XR / R;                                 // loads of XD products
+  constexpr int kSwap = 64 * (NT + XL), kPart = 4 * MT * (16 * NT + 4), kRegion = kSwap > kPart ? kSwap : kPart;
+  __shared__ u32x4 region[kWaves][kRegion];
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, kg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * NT, m0 = (int64_t)blockIdx.y * 16 * MT;
+  const int K = a.K, group = a.group, groups = K / group;
+  const int steps = (K + 127) / 128, per = (steps + kWaves - 1) / kWaves;
+  const int s0 = wave * per, s1 = s0 + per < steps ? s0 + per : steps;
+  const int end = s1 * 128 < K ? s1 * 128 : K;
+
+  // a uniform base and a lane's offset; rows behind the last are the last again:
+  // their results are not used
+  const char *const w_base = (const char *)a.q4 + n0 * (K / 2), *const x_base = (const char *)a.x + m0 * K * ES;
+  const bool s32 = a.scale_dtype == 0, symmetric = !a.zeros;
+  uint32_t row[NT], x_off[XL];
 #pragma unroll
-      for (int e = 0; e < 8; e++) t = fmaf(v[e], (float)(q >> (4 * e) & 15) - z, t);
-      sum = fmaf(load_in(a.scales, a.scale_dtype, g), t, sum);
-    }
-    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
-    if (lane == 0) a.y[m * a.N + n] = __builtin_bit_cast(uint16_t, (__bf16)sum);
+  for (int t = 0; t < NT; t++) {
+    const uint32_t last = (uint32_t)(a.N - 1 - n0 < 16 * NT ? a.N - 1 - n0 : 16 * NT - 1), r = 16 * t + lane / 4;
+    row[t] = r < last ? r : last;
   }
+#pragma unroll
+  for (int j = 0; j < XL; j++) {
+    const uint32_t last = (uint32_t)(a.M - 1 - m0 < 16 * MT ? a.M - 1 - m0 : 16 * MT - 1), r = R * j + lane / C;
+    x_off[j] = (r < last ? r : last) * K * ES;
+  }
+  u32x4 *const w_swap = region[wave], *const x_swap = w_swap + 64 * NT;
+  // places of 16 bytes, turned so that eight lanes that read meet no bank twice
+  const int w_put = lane / 4 * 4 + ((lane ^ lane / 16) & 3), w_get = col * 4 + ((kg ^ col / 4) & 3);
+  const auto x_place = [&](int r, int c) {
+    return r * C + (XR == 4 ? c ^ 4 * r : F32 ? c ^ 2 * (r / 2 & 3) : c ^ (r / 4 & 3));
+  };
+  const int x_row = XR == 4 ? col & 3 : col;
+
+  u32x4 w[NT], x[4 / XD][XL];
+  uint32_t sr[2][NT], zr[2][NT];  // scales and zeros of 16 rows x 4 groups, and of the next 4
+  // what lies behind K is read inside the row and not used
+  const auto load_w = [&](int s) {
+    const int last = (K - s * 128) / 2 - 16;
+    const uint32_t at = G128 || 16 * (lane & 3) < last ? 16 * (lane & 3) : last;
+#pragma unroll
+    for (int t = 0; t < NT; t++) w[t] = *(const u32x4 *)(w_base + s * 64 + (row[t] * (K / 2) + at));
+  };
+  const auto load_x = [&](int s, int d) {  // d: of 4 / XD
+    const int c = (s * 128 + 32 * XD * d) * ES + lane % C * 16, last = K * ES - 16;
+    const uint32_t at = G128 || c < last ? c : last;
+#pragma unroll
+    for (int j = 0; j < XL; j++) x[d][j] = *(const u32x4 *)(x_base + (x_off[j] + at));
+  };
+  const auto load_scales = [&](int quad, uint32_t (&sv)[NT], uint32_t (&zv)[NT]) {
+    const int g = 4 * quad + (lane & 3);
+    const int64_t at = n0 * groups + (g < groups ? g : groups - 1);
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+      if (s32) sv[t] = ((const uint32_t *)a.scales)[at + row[t] * groups];
+      else sv[t] = ((const uint16_t *)a.scales)[at + row[t] * groups];
+      if (symmetric) zv[t] = 0;
+      else if (s32) zv[t] = ((const uint32_t *)a.zeros)[at + row[t] * groups];
+      else zv[t] = ((const uint16_t *)a.zeros)[at + row[t] * groups];
+    }
+  };
+
+  f32x4 total[NT][MT], acc[NT][MT], sum[MT];
+#pragma unroll
+  for (int i = 0; i < MT; i++) {
+    sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < NT; t++) total[t][i] = acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  bf16x8 ones;
+#pragma unroll
+  for (int e = 0; e < 8; e++) ones[e] = (__bf16)1.f;
+
+  int g = 0, left = 0;  // the group, and the coordinates that it still holds
+  float scale[NT], off[NT];
+  const auto pick = [&] {
+    const int from = 4 * (4 * col + (g & 3));
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+      const uint32_t sv = __builtin_amdgcn_ds_bpermute(from, sr[0][t]), zv = __builtin_amdgcn_ds_bpermute(from, zr[0][t]);
+      scale[t] = __builtin_bit_cast(float, s32 ? sv : sv << 16);
+      off[t] = -16.f - (symmetric ? 8.f : __builtin_bit_cast(float, s32 ? zv : zv << 16));
+    }
+  };
+  if (s0 < s1) {
+    g = per_group.div(4 * s0), left = (g + 1) * group - s0 * 128;
+    load_scales(g / 4, sr[0], zr[0]);
+    load_w(s0);
+#pragma unroll
+    for (int d = 0; d < 4 / XD; d++) load_x(s0, d);
+    load_scales(g / 4 + 1, sr[1], zr[1]);
+    pick();
+  }
+  for (int s = s0; s < s1; s++) {
+    const int next = s + 1 < s1 ? s + 1 : s;
+    u32x4 q[NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) w_swap[64 * t + w_put] = w[t];
+#pragma unroll
+    for (int t = 0; t < NT; t++) q[t] = w_swap[64 * t + w_get];
+    load_w(next);
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+      const auto s02 = __builtin_amdgcn_permlane32_swap(q[t][0], q[t][2], false, false);
+      const auto s13 = __builtin_amdgcn_permlane32_swap(q[t][1], q[t][3], false, false);
+      const auto s01 = __builtin_amdgcn_permlane16_swap(s02[0], s13[0], false, false);
+      const auto s23 = __builtin_amdgcn_permlane16_swap(s02[1], s13[1], false, false);
+      q[t] = u32x4{s01[0], s01[1], s23[0], s23[1]};
+    }
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+      const int c = s * 128 + 32 * d;
+      if (!G128 && c >= end) break;
+      if (d % XD == 0) {
+#pragma unroll
+        for (int j = 0; j < XL; j++) x_swap[x_place(R * j + lane / C, lane % C)] = x[d / XD][j];
+        load_x(next, d / XD);
+      }
+      // the activations in the order of the weights' pairs: coordinates j and j + 4
+      bf16x8 xf[MT][NQ];
+#pragma unroll
+      for (int i = 0; i < MT; i++) {
+        u32x4 v[XV];
+#pragma unroll
+        for (int e = 0; e < XV; e++) v[e] = x_swap[16 * C * i + x_place(x_row, 4 * XV * (d % XD) + XV * kg + e)];
+        if constexpr (F32) {
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            float r = __builtin_bit_cast(f32x4, v[e & 1])[e / 2];
+#pragma unroll
+            for (int k = 0; k < NQ; k++) {
+              xf[i][k][e] = (__bf16)r;
+              if (k + 1 < NQ) r -= (float)xf[i][k][e];
+            }
+          }
+        } else {
+          const u32x4 p = {__builtin_amdgcn_perm(v[0][2], v[0][0], 0x05040100u), __builtin_amdgcn_perm(v[0][2], v[0][0], 0x07060302u),
+                           __builtin_amdgcn_perm(v[0][3], v[0][1], 0x05040100u), __builtin_amdgcn_perm(v[0][3], v[0][1], 0x07060302u)};
+          xf[i][0] = __builtin_bit_cast(bf16x8, p);
+        }
+#pragma unroll
+        for (int k = NQ - 1; k >= 0; k--)  // small parts first
+          sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i][k], ones, sum[i], 0, 0, 0);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        const uint32_t v = q[t][d];
+        const u32x4 p = {(v << 3 & 0x00780078u) | 0x41804180u, (v >> 1 & 0x00780078u) | 0x41804180u,
+                         (v >> 5 & 0x00780078u) | 0x41804180u, (v >> 9 & 0x00780078u) | 0x41804180u};
+        const bf16x8 wf = __builtin_bit_cast(bf16x8, p);
+#pragma unroll
+        for (int i = 0; i < MT; i++)
+#pragma unroll
+          for (int k = NQ - 1; k >= 0; k--)
+            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i][k], wf, acc[t][i], 0, 0, 0);
+      }
+      if constexpr (G128)
+        if (d < 3) continue;
+      left -= G128 ? 128 : 32;
+      if (left == 0 || c + 32 == end) {  // the group's end, or the wave's
+#pragma unroll
+        for (int i = 0; i < MT; i++) {
+#pragma unroll
+          for (int t = 0; t < NT; t++) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) total[t][i][e] = fmaf(scale[t], fmaf(off[t], sum[i][e], acc[t][i][e]), total[t][i][e]);
+            acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+          }
+          sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        g++, left = group;
+        if (g % 4 == 0) {
+#pragma unroll
+          for (int t = 0; t < NT; t++) sr[0][t] = sr[1][t], zr[0][t] = zr[1][t];
+          load_scales(g / 4 + 1, sr[1], zr[1]);
+        }
+        pick();
+      }
+    }
+  }
+
+  // the waves' sums, in their order
+  float *const part = (float *)region;
+  const auto at = [](int w, int m, int n) { return 4 * kRegion * w + (16 * NT + 4) * m + n; };
+#pragma unroll
+  for (int i = 0; i < MT; i++)
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) part[at(wave, 16 * i + 4 * kg + e, 16 * t + col)] = total[t][i][e];
+  __syncthreads();
+  const int rows_here = a.M - m0 < 16 * MT ? (int)(a.M - m0) : 16 * MT;
+  for (int e = tid; e < rows_here * 16 * NT; e += 64 * kWaves) {
+    const int m = e / (16 * NT), n = e % (16 * NT);
+    float y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; w++) y += part[at(w, m, n)];
+    if (n0 + n < a.N) a.y[(m0 + m) * a.N + n0 + n] = __builtin_bit_cast(uint16_t, (__bf16)y);
+  }
+}
+
+template <int MT, int NT, int XR>
+void launch_linear(const Rtn4GroupArgs &a) {
+  const dim3 grid((unsigned)((a.N + 16 * NT - 1) / (16 * NT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT))), block(64 * kWaves);
+  const FastDiv per_group((uint32_t)(a.group / 32));
+  const bool f = a.dtype == 0, g = a.group % 128 == 0;
+  if (g && f) hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, true, true>), grid, block, 0, a.stream, a, per_group);
+  else if (g) hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, true, false>), grid, block, 0, a.stream, a, per_group);
+  else if (f) hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, false, true>), grid, block, 0, a.stream, a, per_group);
+  else hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, false, false>), grid, block, 0, a.stream, a, per_group);
 }
 
 }  // namespace
@@ -94,7 +300,18 @@ hipError_t launch_rtn4_group_prepare(const void *W, int dtype, int64_t rows, int
 }
 
 hipError_t launch_rtn4_group_linear(const Rtn4GroupArgs &a) {
-  hipLaunchKernelGGL(rtn4_group_linear_kernel, dim3((unsigned)((a.N + 3) / 4)), dim3(256), 0, a.stream, a);
+  const bool narrow = a.N <= 16 * 1024;
+  if (a.M <= 4) {
+    if (narrow) launch_linear<1, 1, 4>(a);
+    else launch_linear<1, 2, 4>(a);
+  } else if (a.M <= 16) {
+    if (narrow) launch_linear<1, 1, 16>(a);
+    else launch_linear<1, 2, 16>(a);
+  } else if (a.dtype == 0) {
+    launch_linear<2, 2, 16>(a);
+  } else {
+    launch_linear<2, 4, 16>(a);
+  }
   return hipGetLastError();
 }
 
