@@ -66,17 +66,36 @@ __global__ __launch_bounds__(256) void rtn4_group_prepare_kernel(const void *__r
 
 constexpr int kWaves = 8;
 
-// 16 NT columns of y by 16 MT rows of x a workgroup, whose eight waves share K.  A
-// step is 128 coordinates.  Four lanes load 64 bytes of a weight row, and as many as
-// its 32 coordinates take a part of an activation row; through LDS of the wave's own
-// they come to the lanes that the products want.  G128: groups are whole steps.  XR:
-// the rows of x that there can be in a tile, 4 or 16; 4 are repeated.
+// A few rows read every weight once: bound by memory up to some 16 rows, beyond that
+// by the products and what prepares them.  A workgroup makes 16 NT columns of y for 16
+// MT rows of x, its eight waves share K, and LDS joins their sums in a fixed order: one
+// launch, 160 workgroups even where N is 5120.  A step is 128 coordinates.
+//
+// A nibble becomes the bf16 16 + nibble by one shift and one mask-or for two (its
+// four bits are the upper mantissa bits of 16..31), so the products are exact in the
+// matrix unit; a second product by ones gives sum x, and at a group's end
+//   total += scale (sum x (16 + nibble) + (-16 - zero) sum x)
+// in fp32.  fp32 activations are three exact bf16 parts, the small ones added first.
+//
+// The loads follow the rows in memory: four lanes take 64 bytes of a weight row, as
+// many as 32 coordinates need take a part of an activation row, one load brings 16
+// rows' scales of four groups.  LDS of the wave's own turns them to the lanes that the
+// products want.  Loaded straight to those lanes (each lane of a load in a row of its
+// own) the same kernel is held by address processing: 2 x 30720 x 5120 with zeros in 45
+// instead of 30 us, 16 rows of 30720 x 5120 in 45 instead of 24 us.
+//
+// 1 x 5120 x 5120: 7.8 us; 1 x 32768 x 16384: 58 us (4.6 TB/s); 2 x 30720 x 5120,
+// groups of 64 with zeros: 30 us; 29 fp32 rows x 13824 x 5120, groups of 32: 39 us.
+//
+// G128: groups are whole steps.  XR: the rows of x that there can be in a tile, 4 or
+// 16; 4 are repeated, which saves three of four loads.
 template <int MT, int NT, int XR, bool G128, bool F32>
 __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4GroupArgs a, FastDiv per_group) {
   constexpr int NQ = F32 ? 3 : 1, ES = F32 ? 4 : 2, XV = ES / 2;  // XV: 16-byte parts of 8 activations
   constexpr int C = XR == 4 ? 16 : 4 * XV, R = 64 / C;            // a load of x: rows and parts of a row
   constexpr int XD = XR == 4 ? 4 / XV : 1;                        // and the products that it serves
   constexpr int XL = MT * XR / R;                                 // loads of XD products
+  constexpr int XS = MT > 1 && F32 ? 2 : 4 / XD;                  // such sets of loads in flight
   constexpr int kSwap = 64 * (NT + XL), kPart = 4 * MT * (16 * NT + 4), kRegion = kSwap > kPart ? kSwap : kPart;
   __shared__ u32x4 region[kWaves][kRegion];
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, kg = lane >> 4;
@@ -110,7 +129,7 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
   };
   const int x_row = XR == 4 ? col & 3 : col;
 
-  u32x4 w[NT], x[4 / XD][XL];
+  u32x4 w[NT], x[XS][XL];
   uint32_t sr[2][NT], zr[2][NT];  // scales and zeros of 16 rows x 4 groups, and of the next 4
   // what lies behind K is read inside the row and not used
   const auto load_w = [&](int s) {
@@ -119,11 +138,13 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
 #pragma unroll
     for (int t = 0; t < NT; t++) w[t] = *(const u32x4 *)(w_base + s * 64 + (row[t] * (K / 2) + at));
   };
-  const auto load_x = [&](int s, int d) {  // d: of 4 / XD
+  const auto load_x = [&](int s, int d) {  // d: of 4 / XD, then of the next step
+    s += d / (4 / XD), d %= 4 / XD;
+    s = s < s1 ? s : s1 - 1;
     const int c = (s * 128 + 32 * XD * d) * ES + lane % C * 16, last = K * ES - 16;
     const uint32_t at = G128 || c < last ? c : last;
 #pragma unroll
-    for (int j = 0; j < XL; j++) x[d][j] = *(const u32x4 *)(x_base + (x_off[j] + at));
+    for (int j = 0; j < XL; j++) x[d % XS][j] = *(const u32x4 *)(x_base + (x_off[j] + at));
   };
   const auto load_scales = [&](int quad, uint32_t (&sv)[NT], uint32_t (&zv)[NT]) {
     const int g = 4 * quad + (lane & 3);
@@ -165,18 +186,17 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
     load_scales(g / 4, sr[0], zr[0]);
     load_w(s0);
 #pragma unroll
-    for (int d = 0; d < 4 / XD; d++) load_x(s0, d);
+    for (int d = 0; d < XS; d++) load_x(s0, d);
     load_scales(g / 4 + 1, sr[1], zr[1]);
     pick();
   }
   for (int s = s0; s < s1; s++) {
-    const int next = s + 1 < s1 ? s + 1 : s;
     u32x4 q[NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) w_swap[64 * t + w_put] = w[t];
 #pragma unroll
     for (int t = 0; t < NT; t++) q[t] = w_swap[64 * t + w_get];
-    load_w(next);
+    load_w(s + 1 < s1 ? s + 1 : s);
 #pragma unroll
     for (int t = 0; t < NT; t++) {
       const auto s02 = __builtin_amdgcn_permlane32_swap(q[t][0], q[t][2], false, false);
@@ -191,8 +211,8 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
       if (!G128 && c >= end) break;
       if (d % XD == 0) {
 #pragma unroll
-        for (int j = 0; j < XL; j++) x_swap[x_place(R * j + lane / C, lane % C)] = x[d / XD][j];
-        load_x(next, d / XD);
+        for (int j = 0; j < XL; j++) x_swap[x_place(R * j + lane / C, lane % C)] = x[d / XD % XS][j];
+        load_x(s, d / XD + XS);
       }
       // the activations in the order of the weights' pairs: coordinates j and j + 4
       bf16x8 xf[MT][NQ];
@@ -300,18 +320,16 @@ hipError_t launch_rtn4_group_prepare(const void *W, int dtype, int64_t rows, int
 }
 
 hipError_t launch_rtn4_group_linear(const Rtn4GroupArgs &a) {
-  const bool narrow = a.N <= 16 * 1024;
-  if (a.M <= 4) {
-    if (narrow) launch_linear<1, 1, 4>(a);
-    else launch_linear<1, 2, 4>(a);
-  } else if (a.M <= 16) {
-    if (narrow) launch_linear<1, 1, 16>(a);
-    else launch_linear<1, 2, 16>(a);
-  } else if (a.dtype == 0) {
-    launch_linear<2, 2, 16>(a);
-  } else {
-    launch_linear<2, 4, 16>(a);
-  }
+  // Four tiles of columns share what a tile of x costs, two make twice the workgroups:
+  // four win from 128 of them on (64 rows of 5120 x 5120, 160: 15.2 against 19.0 us;
+  // 29 x 13824, 216: 16.7 against 20.0 us), two below (32 rows of 5120 x 13824, 80:
+  // 28.4 against 42.2 us).  Up to 16 rows two win over one and four (5120 x 5120: 7.9
+  // against 8.3 and 11.3 us; 2 x 30720 x 5120: 21.3 against 22.9 and 24.4 us).
+  const bool wide = ((a.N + 63) / 64) * ((a.M + 31) / 32) >= 128;
+  if (a.M <= 4) launch_linear<1, 2, 4>(a);
+  else if (a.M <= 16) launch_linear<1, 2, 16>(a);
+  else if (wide) launch_linear<2, 4, 16>(a);
+  else launch_linear<2, 2, 16>(a);
   return hipGetLastError();
 }
 
