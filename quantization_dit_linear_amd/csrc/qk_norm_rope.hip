@@ -8,7 +8,12 @@
 //
 // Memory bound: each head is read once, kept in registers between the sum of
 // squares and the turn, and written once, 16 bytes a lane.  G neighbouring lanes
-// share a head, so its sum is log2 G lane exchanges.
+// share a head, so its sum is log2 G lane exchanges.  The weights lie in LDS: held in
+// registers they are a chain of loads at every workgroup's start and a choice between
+// the two sides for every element.  Measured: 32760 tokens x (40 + 40) heads x 128 bf16
+// 272 us (4.9 TB/s; weights in registers 300 us); 5003 tokens x (16 + 4) heads x 96
+// fp32, half-split, 17.4 us (25.7 us); one token 4.1 us (6.0 us).  Two passes' loads at
+// once against one, three and four: 272, 277, 278, 307 us.
 #include <hip/hip_runtime.h>
 
 #include "mx_codec.h"
@@ -18,16 +23,20 @@
 namespace oq {
 namespace {
 
+constexpr int kMaxHeadDim = 512;
 constexpr int kPairs = 1024;  // LDS table: pairs of the tokens that a workgroup takes
 
-template <class T>
-__device__ __forceinline__ void load_weight(const void *w, int dtype, int at, float *v) {
-  constexpr int E = 16 / sizeof(T);
+__device__ __forceinline__ void widen(u32x4 r, float (&v)[8]) {
 #pragma unroll
-  for (int e = 0; e < E; e++)
-    v[e] = !w ? 1.f
-           : dtype == 1 ? __builtin_bit_cast(float, (uint32_t)((const uint16_t *)w)[at + e] << 16)
-                        : ((const float *)w)[at + e];
+  for (int e = 0; e < 4; e++) {
+    v[2 * e] = __builtin_bit_cast(float, r[e] << 16);
+    v[2 * e + 1] = __builtin_bit_cast(float, r[e] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void widen(u32x4 r, float (&v)[4]) {
+  const f32x4 f = __builtin_bit_cast(f32x4, r);
+#pragma unroll
+  for (int e = 0; e < 4; e++) v[e] = f[e];
 }
 
 // the sum over the G lanes of a head
@@ -53,7 +62,8 @@ __device__ __forceinline__ float head_sum(float v) {
 template <class T, bool HALF, int G, int NI>
 __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRopeArgs a, int tok_group, int hs) {
   __shared__ __attribute__((aligned(16))) f32x2 table[kPairs + 8];
-  constexpr int E = 16 / sizeof(T), R = 256 / G;  // heads a pass
+  __shared__ __attribute__((aligned(16))) float weight[2][kMaxHeadDim];
+  constexpr int E = 16 / sizeof(T), R = 256 / G, U = 2;  // heads a pass, passes loaded at once
   const int tid = threadIdx.x, half = a.turned / 2, lane = tid % G;
   const int h0 = blockIdx.y * hs, heads = a.side[0].heads + a.side[1].heads;
   const int nh = heads - h0 < hs ? heads - h0 : hs;
@@ -62,19 +72,18 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRopeArgs a, int
   const float inv_d = 1.0f / (float)a.head_dim;
   const int dh = R % nh, dt = R / nh;
 
-  float wu[2][NI][E], wv[2][NI][HALF ? E : 1];
   int at[NI];
 #pragma unroll
   for (int i = 0; i < NI; i++) {
     const int c = lane + G * i;
     at[i] = c >= per ? -1 : !HALF || c < turned_items ? E * c : a.turned + E * (c - turned_items);
-    if (at[i] < 0) continue;
-#pragma unroll
-    for (int s = 0; s < 2; s++) {
-      load_weight<T>(a.side[s].weight, a.param_dtype, at[i], wu[s][i]);
-      if constexpr (HALF)
-        if (c < turned_items) load_weight<T>(a.side[s].weight, a.param_dtype, at[i] + half, wv[s][i]);
-    }
+  }
+  for (int i = tid; i < 2 * a.head_dim; i += 256) {
+    const int s = i >= a.head_dim, e = i - (s ? a.head_dim : 0);
+    const void *const w = a.side[s].weight;
+    weight[s][e] = !w ? 1.f
+                   : a.param_dtype == 1 ? __builtin_bit_cast(float, (uint32_t)((const uint16_t *)w)[e] << 16)
+                                        : ((const float *)w)[e];
   }
 
   for (int64_t t0 = (int64_t)blockIdx.x * tok_group; t0 < a.tokens;
@@ -90,82 +99,115 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRopeArgs a, int
 
     int h = tid / G, t = h / nh;
     h -= t * nh;
+    // U heads at a time, all loads first; what is behind the last reads the first
     while (t < nt) {
-      const int s = h0 + h >= a.side[0].heads;
-      const QkNormRopeArgs::Side &sd = a.side[s];
-      const int64_t hh = h0 + h - (s ? a.side[0].heads : 0);
-      const T *px = (const T *)sd.x + (t0 + t) * sd.x_token + hh * sd.x_head;
-      T *py = (T *)sd.y + (t0 + t) * sd.y_token + hh * sd.y_head;
-      float u[NI][E], v[NI][HALF ? E : 1];
-      float ss = 0.f;
+      u32x4 ru[U][NI], rv[U][HALF ? NI : 1];
+      int it[U], is[U];
+      T *py[U];
 #pragma unroll
-      for (int i = 0; i < NI; i++) {
-        if (at[i] < 0) continue;
-        load16(px + at[i], u[i]);
-        if constexpr (HALF)
-          if (lane + G * i < turned_items) load16(px + at[i] + half, v[i]);
-      }
-      auto squares = [&](float unit) {
-        float q = 0.f;
+      for (int k = 0; k < U; k++) {
+        it[k] = t;
+        const int tc = t < nt ? t : 0, hc = t < nt ? h0 + h : h0;
+        const int s = is[k] = hc >= a.side[0].heads;
+        const QkNormRopeArgs::Side &sd = a.side[s];
+        const int64_t hh = hc - (s ? a.side[0].heads : 0);
+        const T *px = (const T *)sd.x + (t0 + tc) * sd.x_token + hh * sd.x_head;
+        py[k] = (T *)sd.y + (t0 + tc) * sd.y_token + hh * sd.y_head;
 #pragma unroll
         for (int i = 0; i < NI; i++) {
-          if (at[i] < 0) continue;
-#pragma unroll
-          for (int e = 0; e < E; e++) {
-            const float x = u[i][e] * unit;
-            q = fmaf(x, x, q);
-          }
-          if constexpr (HALF)
-            if (lane + G * i < turned_items)
-#pragma unroll
-              for (int e = 0; e < E; e++) {
-                const float x = v[i][e] * unit;
-                q = fmaf(x, x, q);
-              }
+          const T *src = px + (at[i] < 0 ? 0 : at[i]);
+          ru[k][i] = *(const u32x4 *)src;
+          if constexpr (HALF) rv[k][i] = *(const u32x4 *)(lane + G * i < turned_items ? src + half : src);
         }
-        return head_sum<G>(q);
-      };
-      ss = squares(1.f);
-      const float ms = fmaf(ss, inv_d, a.eps);
-      float rs = rsqrtf(ms), back = 1.f;
-      if (__any(!(ms < __builtin_huge_valf()))) {
-        // a mean overflowed: once more at 2^-72, where the squares of 512 values
-        // below 2^128 sum to 2^121 at most.  The factor's 2^-72 is applied behind
-        // the product, exactly.  (A head with a NaN or an infinity stays one.)
-        const float m2 = fmaf(squares(0x1p-72f), inv_d, a.eps * 0x1p-144f);
-        if (!(ms < __builtin_huge_valf())) rs = rsqrtf(m2), back = 0x1p-72f;
+        h += dh, t += dt;
+        if (h >= nh) h -= nh, t++;
       }
 #pragma unroll
-      for (int i = 0; i < NI; i++) {
-        const int c = lane + G * i;
-        if (at[i] < 0) continue;
+      for (int k = 0; k < U; k++) {
+        if (it[k] >= nt) break;
+        const int s = is[k];
+        float u[NI][E], v[NI][HALF ? E : 1];
+        float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; e++) u[i][e] = u[i][e] * rs * back * (s ? wu[1][i][e] : wu[0][i][e]);
-        if (c < turned_items) {
-          const f32x2 *z = table + t * half + (HALF ? E : E / 2) * c;
-          if constexpr (HALF) {
+        for (int i = 0; i < NI; i++) {
+          widen(ru[k][i], u[i]);
+          if constexpr (HALF) widen(rv[k][i], v[i]);
+        }
+        auto squares = [&](float unit) {
+          float q = 0.f;
+#pragma unroll
+          for (int i = 0; i < NI; i++) {
+            if (at[i] < 0) continue;
 #pragma unroll
             for (int e = 0; e < E; e++) {
-              const float x = u[i][e], y = v[i][e] * rs * back * (s ? wv[1][i][e] : wv[0][i][e]);
-              u[i][e] = x * z[e][0] - y * z[e][1];
-              v[i][e] = x * z[e][1] + y * z[e][0];
+              const float x = u[i][e] * unit;
+              q = fmaf(x, x, q);
             }
-            store16_nt(py + at[i] + half, v[i]);
-          } else {
-            const int left = half - E / 2 * c;  // the last item may hold elements behind the turned ones
+            if constexpr (HALF)
+              if (lane + G * i < turned_items)
 #pragma unroll
-            for (int e = 0; e < E / 2; e++) {
-              if (e >= left) break;
-              const float x = u[i][2 * e], y = u[i][2 * e + 1];
-              u[i][2 * e] = x * z[e][0] - y * z[e][1];
-              u[i][2 * e + 1] = x * z[e][1] + y * z[e][0];
+                for (int e = 0; e < E; e++) {
+                  const float x = v[i][e] * unit;
+                  q = fmaf(x, x, q);
+                }
+          }
+          return head_sum<G>(q);
+        };
+        ss = squares(1.f);
+        const float ms = fmaf(ss, inv_d, a.eps);
+        float rs = rsqrtf(ms), back = 1.f;
+        const bool rare = __any(!(ms < __builtin_huge_valf()));
+        if (rare) {
+          // a mean overflowed: once more at 2^-72, where the squares of 512 values
+          // below 2^128 sum to 2^121 at most.  The factor's 2^-72 is applied behind
+          // the product, exactly.  (A head with a NaN or an infinity stays one.)
+          const float m2 = fmaf(squares(0x1p-72f), inv_d, a.eps * 0x1p-144f);
+          if (!(ms < __builtin_huge_valf())) rs = rsqrtf(m2), back = 0x1p-72f;
+        }
+        const auto normed = [&](float (&x)[E], int at) {
+#pragma unroll
+          for (int e = 0; e < E; e++) x[e] *= rs;
+          if (rare)
+#pragma unroll
+            for (int e = 0; e < E; e++) x[e] *= back;
+#pragma unroll
+          for (int e = 0; e < E; e += 4) {
+            const f32x4 w = *(const f32x4 *)(weight[s] + at + e);
+#pragma unroll
+            for (int j = 0; j < 4; j++) x[e + j] *= w[j];
+          }
+        };
+#pragma unroll
+        for (int i = 0; i < NI; i++) {
+          const int c = lane + G * i;
+          if (at[i] < 0) continue;
+          normed(u[i], at[i]);
+          if (c < turned_items) {
+            const f32x2 *z = table + it[k] * half + (HALF ? E : E / 2) * c;
+            if constexpr (HALF) {
+              normed(v[i], at[i] + half);
+#pragma unroll
+              for (int e = 0; e < E; e++) {
+                const float x = u[i][e], y = v[i][e];
+                u[i][e] = x * z[e][0] - y * z[e][1];
+                v[i][e] = x * z[e][1] + y * z[e][0];
+              }
+              store16_nt(py[k] + at[i] + half, v[i]);
+            } else {
+              const int left = half - E / 2 * c;  // the last item may hold elements behind the turned ones
+#pragma unroll
+              for (int e = 0; e < E / 2; e++) {
+                const f32x2 r = e < left ? z[e] : f32x2{1.f, 0.f};
+                const float x = u[i][2 * e], y = u[i][2 * e + 1];
+                const float p = x * r[0] - y * r[1], q = x * r[1] + y * r[0];
+                u[i][2 * e] = e < left ? p : x;
+                u[i][2 * e + 1] = e < left ? q : y;
+              }
             }
           }
+          store16_nt(py[k] + at[i], u[i]);
         }
-        store16_nt(py + at[i], u[i]);
       }
-      h += dh, t += dt;
-      if (h >= nh) h -= nh, t++;
     }
   }
 }
