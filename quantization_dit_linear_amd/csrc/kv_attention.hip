@@ -129,9 +129,17 @@ __global__ __launch_bounds__(256) void kv_join_wide_kernel(KvLaunch p) {
   if (a.lse && d == 0) a.lse[tok * a.q_heads + head] = lse_of(top, sum);
 }
 
-#ifndef KV_WIDE
-#define KV_WIDE 32
-#endif
+// Rows of a sequence, on average, from which on the tiles kernel takes a call, rows
+// against tiles kernel: 64 sequences of 2048 tokens, 8 heads of 4 queries, 64 rows 81
+// against 137 us, 128 rows 142 against 142; 8 of 4096 tokens 46 against 49 and 65
+// against 53 us; one of 32760 tokens 47 against 67 and 71 against 70 us; 6 of 2040
+// tokens with heads of 64 in fp32 54 against 27 us and 32 against 30.
+constexpr int kWide = 64;
+
+// Groups (a tile of rows and a head) up to which their many parts are joined by the
+// waves of a workgroup together and their steps taken by teams of waves (fewer parts):
+// 48 groups 37 against 57 us with a wave a row, 128 groups 70 against 41 us.
+constexpr int kFew = 64;
 
 // The launch that the sizes decide.
 struct Plan {
@@ -146,7 +154,7 @@ struct Plan {
 Plan plan(int dtype, int64_t q_tokens, int q_heads, int kv_heads, int head_dim, int64_t batch, int64_t capacity) {
   const int64_t share = q_heads / kv_heads, per = q_tokens * share / batch;  // rows of a sequence, on average
   Plan r;
-  r.wide = per > KV_WIDE;
+  r.wide = per > kWide;
   r.rows = r.wide ? kv_tiles_rows(dtype, head_dim) : 16;
   r.step = r.wide ? kKvTilesStep : kv_rows_step(head_dim);
   // every sequence may end inside a tile
@@ -157,7 +165,7 @@ Plan plan(int dtype, int64_t q_tokens, int q_heads, int kv_heads, int head_dim, 
   // against 26 us).
   const int64_t units = r.tiles * kv_heads * (capacity / r.step + 8);
   r.workers = r.tiles <= 1024 && units < (int64_t)1 << 30 ? 2048 : 0;
-  r.team = r.workers && r.tiles * kv_heads <= 128;
+  r.team = r.workers && r.tiles * kv_heads <= kFew;
   if (r.team) r.workers /= 4;
   if (r.wide) r.team = false, r.workers = r.workers && r.tiles * kv_heads <= 1024 ? 256 : 0;
   return r;
@@ -196,7 +204,7 @@ hipError_t launch_kv_attention(const KvAttentionArgs &a) {
     return hipGetLastError();
   }
   // a workgroup a row where the groups are few
-  const bool few = tiles * a.cache.heads <= 128;
+  const bool few = tiles * a.cache.heads <= kFew;
   const dim3 grid((unsigned)tiles, (unsigned)a.cache.heads, few ? r.rows : 1);
   if (a.dtype == 0) {
     if (few) hipLaunchKernelGGL((kv_join_kernel<float, true>), grid, dim3(1024), 0, a.stream, p);
