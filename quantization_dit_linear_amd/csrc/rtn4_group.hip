@@ -170,15 +170,24 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
 #pragma unroll
   for (int e = 0; e < 8; e++) ones[e] = (__bf16)1.f;
 
+  // in registers, so that and and or are one instruction (which takes no two literals)
+  uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+  asm("" : "+s"(mask), "+v"(sixteen));
+
   int g = 0, left = 0;  // the group, and the coordinates that it still holds
   float scale[NT], off[NT];
+  const int up = s32 ? 0 : 16;
   const auto pick = [&] {
     const int from = 4 * (4 * col + (g & 3));
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-      const uint32_t sv = __builtin_amdgcn_ds_bpermute(from, sr[0][t]), zv = __builtin_amdgcn_ds_bpermute(from, zr[0][t]);
-      scale[t] = __builtin_bit_cast(float, s32 ? sv : sv << 16);
-      off[t] = -16.f - (symmetric ? 8.f : __builtin_bit_cast(float, s32 ? zv : zv << 16));
+      const uint32_t sv = __builtin_amdgcn_ds_bpermute(from, sr[0][t]);
+      scale[t] = __builtin_bit_cast(float, sv << up);
+      off[t] = -24.f;
+      if (!symmetric) {
+        const uint32_t zv = __builtin_amdgcn_ds_bpermute(from, zr[0][t]);
+        off[t] = -16.f - __builtin_bit_cast(float, zv << up);
+      }
     }
   };
   if (s0 < s1) {
@@ -243,8 +252,7 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
 #pragma unroll
       for (int t = 0; t < NT; t++) {
         const uint32_t v = q[t][d];
-        const u32x4 p = {(v << 3 & 0x00780078u) | 0x41804180u, (v >> 1 & 0x00780078u) | 0x41804180u,
-                         (v >> 5 & 0x00780078u) | 0x41804180u, (v >> 9 & 0x00780078u) | 0x41804180u};
+        const u32x4 p = {(v << 3 & mask) | sixteen, (v >> 1 & mask) | sixteen, (v >> 5 & mask) | sixteen, (v >> 9 & mask) | sixteen};
         const bf16x8 wf = __builtin_bit_cast(bf16x8, p);
 #pragma unroll
         for (int i = 0; i < MT; i++)
