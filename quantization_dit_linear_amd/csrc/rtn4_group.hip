@@ -84,12 +84,14 @@ constexpr int kWaves = 8;
 // own) the same kernel is held by address processing: 2 x 30720 x 5120 with zeros in 45
 // instead of 30 us, 16 rows of 30720 x 5120 in 45 instead of 24 us.
 //
-// 1 x 5120 x 5120: 7.8 us; 1 x 32768 x 16384: 58 us (4.6 TB/s); 2 x 30720 x 5120,
-// groups of 64 with zeros: 30 us; 29 fp32 rows x 13824 x 5120, groups of 32: 39 us.
+// 1 x 5120 x 5120: 7.1 us; 1 x 32768 x 16384: 57 us (4.7 TB/s); 2 x 30720 x 5120,
+// groups of 64 with zeros: 30 us; 29 fp32 rows x 13824 x 5120, groups of 32: 35 us,
+// 60 % of it vector instructions (the parts, the nibbles, the groups' ends).
 //
-// G128: groups are whole steps.  XR: the rows of x that there can be in a tile, 4 or
+// GK: the group where it is 32, 64 or 128 (its products are known then, and the first
+// starts from zero: 34.8 against 38.5 us for the 29 rows, 7.1 against 7.6 for one), else 0.  XR: the rows of x that there can be in a tile, 4 or
 // 16; 4 are repeated, which saves three of four loads.
-template <int MT, int NT, int XR, bool G128, bool F32>
+template <int MT, int NT, int XR, int GK, bool F32>
 __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4GroupArgs a, FastDiv per_group) {
   constexpr int NQ = F32 ? 3 : 1, ES = F32 ? 4 : 2, XV = ES / 2;  // XV: 16-byte parts of 8 activations
   constexpr int C = XR == 4 ? 16 : 4 * XV, R = 64 / C;            // a load of x: rows and parts of a row
@@ -134,7 +136,7 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
   // what lies behind K is read inside the row and not used
   const auto load_w = [&](int s) {
     const int last = (K - s * 128) / 2 - 16;
-    const uint32_t at = G128 || 16 * (lane & 3) < last ? 16 * (lane & 3) : last;
+    const uint32_t at = GK == 128 || 16 * (lane & 3) < last ? 16 * (lane & 3) : last;
 #pragma unroll
     for (int t = 0; t < NT; t++) w[t] = *(const u32x4 *)(w_base + s * 64 + (row[t] * (K / 2) + at));
   };
@@ -142,7 +144,7 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
     s += d / (4 / XD), d %= 4 / XD;
     s = s < s1 ? s : s1 - 1;
     const int c = (s * 128 + 32 * XD * d) * ES + lane % C * 16, last = K * ES - 16;
-    const uint32_t at = G128 || c < last ? c : last;
+    const uint32_t at = GK == 128 || c < last ? c : last;
 #pragma unroll
     for (int j = 0; j < XL; j++) x[d % XS][j] = *(const u32x4 *)(x_base + (x_off[j] + at));
   };
@@ -217,12 +219,14 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
 #pragma unroll
     for (int d = 0; d < 4; d++) {
       const int c = s * 128 + 32 * d;
-      if (!G128 && c >= end) break;
+      if (GK != 128 && c >= end) break;
       if (d % XD == 0) {
 #pragma unroll
         for (int j = 0; j < XL; j++) x_swap[x_place(R * j + lane / C, lane % C)] = x[d / XD % XS][j];
         load_x(s, d / XD + XS);
       }
+      const bool fresh = GK && 32 * d % (GK ? GK : 1) == 0;
+      const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
       // the activations in the order of the weights' pairs: coordinates j and j + 4
       bf16x8 xf[MT][NQ];
 #pragma unroll
@@ -247,7 +251,7 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
         }
 #pragma unroll
         for (int k = NQ - 1; k >= 0; k--)  // small parts first
-          sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i][k], ones, sum[i], 0, 0, 0);
+          sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i][k], ones, fresh && k == NQ - 1 ? zero : sum[i], 0, 0, 0);
       }
 #pragma unroll
       for (int t = 0; t < NT; t++) {
@@ -258,21 +262,20 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
         for (int i = 0; i < MT; i++)
 #pragma unroll
           for (int k = NQ - 1; k >= 0; k--)
-            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i][k], wf, acc[t][i], 0, 0, 0);
+            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i][k], wf, fresh && k == NQ - 1 ? zero : acc[t][i], 0, 0, 0);
       }
-      if constexpr (G128)
-        if (d < 3) continue;
-      left -= G128 ? 128 : 32;
-      if (left == 0 || c + 32 == end) {  // the group's end, or the wave's
+      if (GK && (32 * d + 32) % (GK ? GK : 1)) continue;
+      left -= 32;
+      if (GK || left == 0 || c + 32 == end) {  // the group's end, or the wave's
 #pragma unroll
         for (int i = 0; i < MT; i++) {
 #pragma unroll
           for (int t = 0; t < NT; t++) {
 #pragma unroll
             for (int e = 0; e < 4; e++) total[t][i][e] = fmaf(scale[t], fmaf(off[t], sum[i][e], acc[t][i][e]), total[t][i][e]);
-            acc[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (!GK) acc[t][i] = zero;
           }
-          sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (!GK) sum[i] = zero;
         }
         g++, left = group;
         if (g % 4 == 0) {
@@ -309,11 +312,16 @@ template <int MT, int NT, int XR>
 void launch_linear(const Rtn4GroupArgs &a) {
   const dim3 grid((unsigned)((a.N + 16 * NT - 1) / (16 * NT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT))), block(64 * kWaves);
   const FastDiv per_group((uint32_t)(a.group / 32));
-  const bool f = a.dtype == 0, g = a.group % 128 == 0;
-  if (g && f) hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, true, true>), grid, block, 0, a.stream, a, per_group);
-  else if (g) hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, true, false>), grid, block, 0, a.stream, a, per_group);
-  else if (f) hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, false, true>), grid, block, 0, a.stream, a, per_group);
-  else hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, false, false>), grid, block, 0, a.stream, a, per_group);
+#define OQ_CASE(GK)                                                                                                     \
+  {                                                                                                                     \
+    if (a.dtype == 0) hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, GK, true>), grid, block, 0, a.stream, a, per_group); \
+    else hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, GK, false>), grid, block, 0, a.stream, a, per_group); \
+  }
+  if (a.group == 128) OQ_CASE(128)
+  else if (a.group == 64) OQ_CASE(64)
+  else if (a.group == 32) OQ_CASE(32)
+  else OQ_CASE(0)
+#undef OQ_CASE
 }
 
 }  // namespace
