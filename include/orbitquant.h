@@ -411,7 +411,9 @@ int oq_rtn4_group_prepare_weights(const void *W, int dtype, int64_t n_out, int d
  * zero = 8 where zeros is NULL; fp32 accumulation, one bf16 rounding, no bias.
  *   x: device fp32 or bf16 [M][K] (16-byte aligned); y: bf16 [M][N], apart from
  *   the inputs
- * Sized for few rows.  M = 0 or N = 0 no-op.
+ * Sized for few rows.  Sums hold x_mk (16 + nibble): a row whose |x| sum to 2^122
+ * or more over a group may come out infinite or NaN, as one with an infinity or a
+ * NaN does; no other row is touched by it.  M = 0 or N = 0 no-op.
  * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
 int oq_rtn4_group_linear(const void *x, int dtype, int64_t M, const uint8_t *q4,
                          const void *scales, const void *zeros, int scale_dtype, int group,

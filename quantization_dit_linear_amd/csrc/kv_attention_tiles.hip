@@ -13,7 +13,7 @@
 //
 // Bound by the matrix unit and the instructions beside it: 1560 queries over 32760
 // tokens, 40 heads of 128, bf16, 1.05 TFLOP, 1.12 ms (0.93 PFLOP/s; a large product of
-// the library reaches 1.30).  Four waves of twice 32 rows 1.87 ms; operands read as the
+// the library reaches 1.3 to 1.6).  Four waves of twice 32 rows 1.87 ms; operands read as the
 // compiler orders them 1.21 ms; two groups of waves half a step apart, or the scores
 // of the next step computed beside this one's weights within a wave, no faster (1.23).
 #include <hip/hip_runtime.h>

@@ -86,7 +86,7 @@ constexpr int kWaves = 8;
 //
 // 1 x 5120 x 5120: 7.1 us; 1 x 32768 x 16384: 57 us (4.7 TB/s); 2 x 30720 x 5120,
 // groups of 64 with zeros: 30 us; 29 fp32 rows x 13824 x 5120, groups of 32: 35 us,
-// 60 % of it vector instructions (the parts, the nibbles, the groups' ends).
+// half of it vector instructions (the parts, the nibbles, the groups' ends).
 //
 // GK: the group where it is 32, 64 or 128 (its products are known then, and the first
 // starts from zero: 34.8 against 38.5 us for the 29 rows, 7.1 against 7.6 for one), else 0.  XR: the rows of x that there can be in a tile, 4 or
