@@ -413,7 +413,8 @@ int oq_rtn4_group_prepare_weights(const void *W, int dtype, int64_t n_out, int d
  *   the inputs
  * Sized for few rows.  Sums hold x_mk (16 + nibble): a row whose |x| sum to 2^122
  * or more over a group may come out infinite or NaN, as one with an infinity or a
- * NaN does; no other row is touched by it.  M = 0 or N = 0 no-op.
+ * NaN does; no other row is touched by it.  N up to 2^27, M up to
+ * 2^30.  M = 0 or N = 0 no-op.
  * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
 int oq_rtn4_group_linear(const void *x, int dtype, int64_t M, const uint8_t *q4,
                          const void *scales, const void *zeros, int scale_dtype, int group,
@@ -466,7 +467,9 @@ int64_t oq_mx_kv_attention_workspace(int64_t q_tokens, int q_heads, int kv_heads
  *     and y, apart from each other
  *   batch sequences; q_starts: device int32 [batch + 1], sequence b's queries
  *     are the tokens [q_starts[b], q_starts[b + 1]); the outputs of tokens behind
- *     the last sequence are left as they were.  NULL: the tokens are split
+ *     the last sequence are left as they were.  Starts ascend and are clamped to
+ *     [0, q_tokens]; where they descend, the outputs are unspecified (nothing else
+ *     is touched).  NULL: the tokens are split
  *     evenly (q_tokens a multiple of batch)
  *   lengths: device int32 [batch], tokens in the cache (counting the new ones);
  *     taken as 0 below 0 and as table_pages * page_size above that

@@ -180,14 +180,21 @@ __device__ __forceinline__ KvUnits find_units(const KvLaunch &p, int x) {
 // A worker's units [pos, end), `share` each, and the sequence of the first.
 __device__ __forceinline__ KvUnits first_units(const KvLaunch &p, int worker, int &share, int &pos, int &end) {
   const int lane = threadIdx.x & 63;
-  int total = 0;
+  int total = 0, tiles = 0;
   KvUnits u;
-  int all = 0, sum = 0;
+  int all = 0, sum = 0, tsum = 0;
   for (int b0 = 0; b0 < p.a.batch; b0 += 64) {
     u = units_of(p, b0 + lane);
     all = u.all(p.a.cache.heads);
-    sum = prefix_sum(all);
+    sum = prefix_sum(all), tsum = prefix_sum(u.tiles);
     total += __builtin_amdgcn_readlane(sum, 63);
+    tiles += __builtin_amdgcn_readlane(tsum, 63);
+    // starts that descend name tokens twice and can make more tiles than the sizes
+    // allow, which the workspace has no place for: then no worker does anything
+    if (tiles > p.count) {
+      total = 0;
+      break;
+    }
   }
   share = (total + p.workers - 1) / p.workers;
   if (share < p.least) share = p.least;
@@ -195,7 +202,7 @@ __device__ __forceinline__ KvUnits first_units(const KvLaunch &p, int worker, in
   end = pos + share < total ? pos + share : total;
   if (pos >= end) return u;
   if (p.a.batch > 64) return find_units(p, pos);
-  return pick(u, all, sum, prefix_sum(u.tiles), __ballot(sum > pos));
+  return pick(u, all, sum, tsum, __ballot(sum > pos));
 }
 
 // Eight e2m1 codes of one block as bf16: exact at every scale.

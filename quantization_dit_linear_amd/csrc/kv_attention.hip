@@ -13,6 +13,12 @@
 namespace oq {
 namespace {
 
+// Whether a group has parts to join.  (Starts that descend leave what the workspace
+// held before: nothing beyond it is read.)
+__device__ __forceinline__ bool joins(const KvLaunch &p, int first, int parts) {
+  return parts > 1 && parts <= p.workers + 1 && first >= 0 && first < 2 * p.workers && first - 1 + 2 * (parts - 1) < 2 * p.workers;
+}
+
 // A group's parts, in their order, a wave a row: 64 parts' maxima and sums of
 // weights a time, then their sums, as many side by side as the lanes hold, eight
 // loads a lane.  SPLIT: the waves of a workgroup share a row (parts are many where
@@ -29,7 +35,7 @@ __global__ __launch_bounds__(SPLIT ? 1024 : 256) void kv_join_kernel(KvLaunch p)
   const KvTile t = find_tile(p, blockIdx.x);
   if (t.b < 0) return;
   const int first = which.x, parts = which.y;
-  if (parts == 1) return;
+  if (!joins(p, first, parts)) return;
   // part k: the last of its worker where the group starts there, else the first
   const auto slot = [&](int k) { return (int64_t)(k == 0 ? first : first - 1 + 2 * k) * p.rows; };
   const int rows = t.rows - t.row0 < p.rows ? t.rows - t.row0 : p.rows;
@@ -106,7 +112,7 @@ __global__ __launch_bounds__(256) void kv_join_wide_kernel(KvLaunch p) {
   if (t.b < 0) return;
   const int first = which.x, parts = which.y, hd = a.cache.head_dim, q4 = hd / 4;
   const int e = (int)blockIdx.z * 256 + (int)threadIdx.x, r = e / q4, d = 4 * (e - r * q4);
-  if (parts == 1 || r >= p.rows || t.row0 + r >= t.rows) return;
+  if (!joins(p, first, parts) || r >= p.rows || t.row0 + r >= t.rows) return;
   const auto slot = [&](int k) { return (int64_t)(k == 0 ? first : first - 1 + 2 * k) * p.rows + r; };
   float top = -kInf, sum = 0.f;
   for (int k = 0; k < parts; k++) top = fmaxf(top, p.part_ml[slot(k)][0]);

@@ -1102,7 +1102,7 @@ int oq_rtn4_group_linear(const void *x, int dtype, int64_t M, const uint8_t *q4,
   if (M < 0 || !is_dtype(dtype)) return OQ_EINVAL;
   const int rc = check_group(N, K, group, scale_dtype);
   if (rc != OQ_OK) return rc;
-  if (M > kMaxRows) return OQ_EUNSUPPORTED;
+  if (M > kMaxRows || N > (int64_t)1 << 27) return OQ_EUNSUPPORTED;
   if (M == 0 || N == 0) return OQ_OK;
   if (!x || !q4 || !scales || !y) return OQ_EINVAL;
   if (!aligned(x, 16) || !aligned(q4, 16) || !aligned(scales, 4) || !aligned(zeros, 4) || !aligned(y, 2))

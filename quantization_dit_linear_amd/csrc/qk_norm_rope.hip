@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkNormRopeArgs a, int
   }
   for (int i = tid; i < 2 * a.head_dim; i += 256) {
     const int s = i >= a.head_dim, e = i - (s ? a.head_dim : 0);
-    const void *const w = a.side[s].weight;
+    const void *const w = a.side[s].heads ? a.side[s].weight : nullptr;
     weight[s][e] = !w ? 1.f
                    : a.param_dtype == 1 ? __builtin_bit_cast(float, (uint32_t)((const uint16_t *)w)[e] << 16)
                                         : ((const float *)w)[e];

@@ -89,8 +89,9 @@ constexpr int kWaves = 8;
 // half of it vector instructions (the parts, the nibbles, the groups' ends).
 //
 // GK: the group where it is 32, 64 or 128 (its products are known then, and the first
-// starts from zero: 34.8 against 38.5 us for the 29 rows, 7.1 against 7.6 for one), else 0.  XR: the rows of x that there can be in a tile, 4 or
-// 16; 4 are repeated, which saves three of four loads.
+// starts from zero: 34.8 against 38.5 us for the 29 rows, 7.1 against 7.6 for one), else
+// 0.  XR: the rows of x that there can be in a tile, 4 or 16; 4 are repeated, which
+// saves three of four loads.
 template <int MT, int NT, int XR, int GK, bool F32>
 __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4GroupArgs a, FastDiv per_group) {
   constexpr int NQ = F32 ? 3 : 1, ES = F32 ? 4 : 2, XV = ES / 2;  // XV: 16-byte parts of 8 activations
@@ -335,18 +336,27 @@ hipError_t launch_rtn4_group_prepare(const void *W, int dtype, int64_t rows, int
   return hipGetLastError();
 }
 
-hipError_t launch_rtn4_group_linear(const Rtn4GroupArgs &a) {
+hipError_t launch_rtn4_group_linear(const Rtn4GroupArgs &all) {
   // Four tiles of columns share what a tile of x costs, two make twice the workgroups:
   // four win from 128 of them on (64 rows of 5120 x 5120, 160: 15.2 against 19.0 us;
   // 29 x 13824, 216: 16.7 against 20.0 us), two below (32 rows of 5120 x 13824, 80:
   // 28.4 against 42.2 us).  Up to 16 rows two win over one and four (5120 x 5120: 7.9
   // against 8.3 and 11.3 us; 2 x 30720 x 5120: 21.3 against 22.9 and 24.4 us).
-  const bool wide = ((a.N + 63) / 64) * ((a.M + 31) / 32) >= 128;
-  if (a.M <= 4) launch_linear<1, 2, 4>(a);
-  else if (a.M <= 16) launch_linear<1, 2, 16>(a);
-  else if (wide) launch_linear<2, 4, 16>(a);
-  else launch_linear<2, 2, 16>(a);
-  return hipGetLastError();
+  const bool wide = ((all.N + 63) / 64) * ((all.M + 31) / 32) >= 128;
+  constexpr int64_t kRows = 1 << 20;  // a launch: a grid has no more than 65535 tiles of rows
+  for (int64_t m = 0; m < all.M; m += kRows) {
+    Rtn4GroupArgs a = all;
+    a.x = (const char *)all.x + m * all.K * (all.dtype == 0 ? 4 : 2);
+    a.y = all.y + m * all.N;
+    a.M = all.M - m < kRows ? all.M - m : kRows;
+    if (all.M <= 4) launch_linear<1, 2, 4>(a);
+    else if (all.M <= 16) launch_linear<1, 2, 16>(a);
+    else if (wide) launch_linear<2, 4, 16>(a);
+    else launch_linear<2, 2, 16>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace oq

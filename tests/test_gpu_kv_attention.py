@@ -269,6 +269,26 @@ def test_starts_that_are_not_ascending(q):
     assert torch.isfinite(out.float()).all()
 
 
+@pytest.mark.parametrize("tokens", [100, 2000])
+def test_starts_that_name_tokens_many_times(q, tokens):
+    """More tiles than the sizes allow: the call ends, touches nothing but its
+    outputs and its workspace, and the next call is right."""
+    import torch
+    say("kv attention starts many times", tokens)
+    rng = np.random.default_rng(16)
+    cache, dev = _cache(q, rng, 8, 1, 16, 32)
+    before = [c.clone() for c in dev]
+    qd = _queries(rng, (tokens, 1, 32), True)
+    around = torch.full((tokens + 64, 1, 32), 3.0, dtype=torch.bfloat16, device="cuda")
+    q.mx_kv_attention(qd, dev, torch.full((8,), 16, dtype=torch.int32, device="cuda"),
+                      q_starts=torch.tensor([0, tokens] * 4 + [0], dtype=torch.int32, device="cuda"),
+                      out=around[32:-32])
+    torch.cuda.synchronize()
+    assert (around[:32] == 3.0).all() and (around[-32:] == 3.0).all()
+    assert all(torch.equal(a, b) for a, b in zip(before, dev))
+    _compare(q, qd, cache, dev, [16] * 8, None, [0, 3, 3, 40, 41, 60, 61, tokens - 1, tokens], True, 0)
+
+
 @pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
 def test_same_bits_every_time_and_in_graphs(q, bf16):
     """Twice the same call, two captured graphs replayed by turns with eager work

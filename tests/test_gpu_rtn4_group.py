@@ -70,6 +70,28 @@ def test_linear(q, M, N, K, group, bf16, scale_bf16, zeros):
     _check(_np(y), _np(xd), q4, s, z, group)
 
 
+@pytest.mark.parametrize("zeros,scale_bf16", [(False, True), (True, False)], ids=["sym", "zeros"])
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("M,N,K,group", [(29, 8200, 320, 32), (33, 4161, 480, 96), (64, 4097, 256, 64),
+                                         (17, 8191, 384, 128), (70, 2753, 1056, 352)])
+def test_wide_tiles(q, M, N, K, group, bf16, scale_bf16, zeros):
+    """Columns and rows enough for the tiles of 64 columns."""
+    test_linear(q, M, N, K, group, bf16, scale_bf16, zeros)
+
+
+def test_many_rows(q):
+    """More rows than one grid has tiles for."""
+    import torch
+    say("rtn4 group many rows")
+    rng, M, N, K = np.random.default_rng(2), (1 << 20) + 37, 3, 32
+    x = rng.standard_normal((M, K)).astype(np.float32)
+    q4, s, _ = _weights(rng, N, K, 32, False, True)
+    xd = _dev(x, True)
+    y = q.rtn4_group_linear(xd, to_device(q4), s)
+    rows = np.r_[0:70, (1 << 20) - 70:M]
+    _check(_np(y[rows]), _np(xd[rows]), q4, s, None, 32)
+
+
 @pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
 @pytest.mark.parametrize("M", [1, 12, 40])
 def test_wide_ranges(q, M, bf16):

@@ -46,7 +46,8 @@ def test_group_linear():
                     dict(s=C + 2), dict(z=D + 2), dict(y=E + 1), dict(dt=5), dict(sdt=2), dict(m=-1), dict(n=-1),
                     dict(k=0), dict(group=0), dict(group=100), dict(group=3), dict(y=A), dict(y=A + 2046),
                     dict(y=B), dict(y=C + 126), dict(y=D - 62)),
-             (dict(group=16), dict(k=16416, group=32), dict(m=(1 << 30) + 1), dict(n=(1 << 30) + 1)))
+             (dict(group=16), dict(k=16416, group=32), dict(m=(1 << 30) + 1), dict(n=(1 << 30) + 1),
+              dict(n=(1 << 27) + 1)))
     for kw in (dict(m=0), dict(n=0), dict(m=0, x=None, y=None)):
         assert call(**kw) == q.OQ_OK
 
