@@ -85,7 +85,7 @@ constexpr int kWaves = 8;
 // instead of 30 us, 16 rows of 30720 x 5120 in 45 instead of 24 us.
 //
 // 1 x 5120 x 5120: 7.1 us; 1 x 32768 x 16384: 57 us (4.7 TB/s); 2 x 30720 x 5120,
-// groups of 64 with zeros: 30 us; 29 fp32 rows x 13824 x 5120, groups of 32: 35 us,
+// groups of 64 with zeros in fp32: 27 us; 29 fp32 rows x 13824 x 5120, groups of 32: 35 us,
 // half of it vector instructions (the parts, the nibbles, the groups' ends).
 //
 // GK: the group where it is 32, 64 or 128 (its products are known then, and the first
@@ -99,6 +99,10 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
   constexpr int XD = XR == 4 ? 4 / XV : 1;                        // and the products that it serves
   constexpr int XL = MT * XR / R;                                 // loads of XD products
   constexpr int XS = MT > 1 && F32 ? 2 : 4 / XD;                  // such sets of loads in flight
+  // No branch for a step's tail within it, so that one group's end overlaps the next
+  // one's products: 2 x 30720 x 5120 in groups of 64 22.3 against 24.3 us.  Groups of 32
+  // (29.3 to 35.7 us) and tiles of 64 columns lose their registers to it.
+  constexpr bool STRAIGHT = GK == 64 && NT == 2;
   constexpr int kSwap = 64 * (NT + XL), kPart = 4 * MT * (16 * NT + 4), kRegion = kSwap > kPart ? kSwap : kPart;
   __shared__ u32x4 region[kWaves][kRegion];
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, kg = lane >> 4;
@@ -220,7 +224,7 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
 #pragma unroll
     for (int d = 0; d < 4; d++) {
       const int c = s * 128 + 32 * d;
-      if (GK != 128 && c >= end) break;
+      if (!STRAIGHT && GK != 128 && c >= end) break;
       if (d % XD == 0) {
 #pragma unroll
         for (int j = 0; j < XL; j++) x_swap[x_place(R * j + lane / C, lane % C)] = x[d / XD % XS][j];
@@ -268,18 +272,22 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
       if (GK && (32 * d + 32) % (GK ? GK : 1)) continue;
       left -= 32;
       if (GK || left == 0 || c + 32 == end) {  // the group's end, or the wave's
+        // (STRAIGHT: a group behind K counts nothing)
+        float by[NT];
+#pragma unroll
+        for (int t = 0; t < NT; t++) by[t] = !STRAIGHT || c < end ? scale[t] : 0.f;
 #pragma unroll
         for (int i = 0; i < MT; i++) {
 #pragma unroll
           for (int t = 0; t < NT; t++) {
 #pragma unroll
-            for (int e = 0; e < 4; e++) total[t][i][e] = fmaf(scale[t], fmaf(off[t], sum[i][e], acc[t][i][e]), total[t][i][e]);
+            for (int e = 0; e < 4; e++) total[t][i][e] = fmaf(by[t], fmaf(off[t], sum[i][e], acc[t][i][e]), total[t][i][e]);
             if (!GK) acc[t][i] = zero;
           }
           if (!GK) sum[i] = zero;
         }
         g++, left = group;
-        if (g % 4 == 0) {
+        if ((!STRAIGHT || d == 3) && g % 4 == 0) {
 #pragma unroll
           for (int t = 0; t < NT; t++) sr[0][t] = sr[1][t], zr[0][t] = zr[1][t];
           load_scales(g / 4 + 1, sr[1], zr[1]);
