@@ -79,6 +79,15 @@ def test_wide_tiles(q, M, N, K, group, bf16, scale_bf16, zeros):
     test_linear(q, M, N, K, group, bf16, scale_bf16, zeros)
 
 
+@pytest.mark.parametrize("zeros,scale_bf16", [(False, False), (True, True)], ids=["sym", "zeros"])
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("M,N,K,group", [(3, 40, 1088, 64), (12, 70, 1600, 64), (40, 70, 1344, 64), (40, 33, 1312, 32),
+                                         (4, 5, 1952, 32), (2, 37, 3232, 3232), (20, 35, 2592, 288)])
+def test_half_steps(q, M, N, K, group, bf16, scale_bf16, zeros):
+    """K that ends within 128 coordinates, where some of the groups do."""
+    test_linear(q, M, N, K, group, bf16, scale_bf16, zeros)
+
+
 def test_many_rows(q):
     """More rows than one grid has tiles for."""
     import torch
