@@ -64,11 +64,9 @@ __global__ __launch_bounds__(256) void rtn4_group_prepare_kernel(const void *__r
   }
 }
 
-constexpr int kWaves = 8;
-
 // A few rows read every weight once: bound by memory up to some 16 rows, beyond that
 // by the products and what prepares them.  A workgroup makes 16 NT columns of y for 16
-// MT rows of x, its eight waves share K, and LDS joins their sums in a fixed order: one
+// MT rows of x, its waves share K, and LDS joins their sums in a fixed order: one
 // launch, 160 workgroups even where N is 5120.  A step is 128 coordinates.
 //
 // A nibble becomes the bf16 16 + nibble by one shift and one mask-or for two (its
@@ -92,8 +90,8 @@ constexpr int kWaves = 8;
 // starts from zero: 34.8 against 38.5 us for the 29 rows, 7.1 against 7.6 for one), else
 // 0.  XR: the rows of x that there can be in a tile, 4 or 16; 4 are repeated, which
 // saves three of four loads.
-template <int MT, int NT, int XR, int GK, bool F32>
-__global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4GroupArgs a, FastDiv per_group) {
+template <int MT, int NT, int XR, int WAVES, int GK, bool F32>
+__global__ __launch_bounds__(64 * WAVES) void rtn4_group_linear_kernel(Rtn4GroupArgs a, FastDiv per_group) {
   constexpr int NQ = F32 ? 3 : 1, ES = F32 ? 4 : 2, XV = ES / 2;  // XV: 16-byte parts of 8 activations
   constexpr int C = XR == 4 ? 16 : 4 * XV, R = 64 / C;            // a load of x: rows and parts of a row
   constexpr int XD = XR == 4 ? 4 / XV : 1;                        // and the products that it serves
@@ -102,14 +100,14 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
   // No branch for a step's tail within it, so that one group's end overlaps the next
   // one's products: 2 x 30720 x 5120 in groups of 64 22.3 against 24.3 us.  Groups of 32
   // (29.3 to 35.7 us) and tiles of 64 columns lose their registers to it.
-  constexpr bool STRAIGHT = GK == 64 && NT == 2;
+  constexpr bool STRAIGHT = GK == 64 && NT <= 2;
   constexpr int kSwap = 64 * (NT + XL), kPart = 4 * MT * (16 * NT + 4), kRegion = kSwap > kPart ? kSwap : kPart;
-  __shared__ u32x4 region[kWaves][kRegion];
+  __shared__ u32x4 region[WAVES][kRegion];
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, kg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t n0 = (int64_t)blockIdx.x * 16 * NT, m0 = (int64_t)blockIdx.y * 16 * MT;
   const int K = a.K, group = a.group, groups = K / group;
-  const int steps = (K + 127) / 128, per = (steps + kWaves - 1) / kWaves;
+  const int steps = (K + 127) / 128, per = (steps + WAVES - 1) / WAVES;
   const int s0 = wave * per, s1 = s0 + per < steps ? s0 + per : steps;
   const int end = s1 * 128 < K ? s1 * 128 : K;
 
@@ -308,23 +306,23 @@ __global__ __launch_bounds__(64 * kWaves) void rtn4_group_linear_kernel(Rtn4Grou
       for (int e = 0; e < 4; e++) part[at(wave, 16 * i + 4 * kg + e, 16 * t + col)] = total[t][i][e];
   __syncthreads();
   const int rows_here = a.M - m0 < 16 * MT ? (int)(a.M - m0) : 16 * MT;
-  for (int e = tid; e < rows_here * 16 * NT; e += 64 * kWaves) {
+  for (int e = tid; e < rows_here * 16 * NT; e += 64 * WAVES) {
     const int m = e / (16 * NT), n = e % (16 * NT);
     float y = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; w++) y += part[at(w, m, n)];
+    for (int w = 0; w < WAVES; w++) y += part[at(w, m, n)];
     if (n0 + n < a.N) a.y[(m0 + m) * a.N + n0 + n] = __builtin_bit_cast(uint16_t, (__bf16)y);
   }
 }
 
-template <int MT, int NT, int XR>
+template <int MT, int NT, int XR, int WAVES = 8>
 void launch_linear(const Rtn4GroupArgs &a) {
-  const dim3 grid((unsigned)((a.N + 16 * NT - 1) / (16 * NT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT))), block(64 * kWaves);
+  const dim3 grid((unsigned)((a.N + 16 * NT - 1) / (16 * NT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT))), block(64 * WAVES);
   const FastDiv per_group((uint32_t)(a.group / 32));
 #define OQ_CASE(GK)                                                                                                     \
   {                                                                                                                     \
-    if (a.dtype == 0) hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, GK, true>), grid, block, 0, a.stream, a, per_group); \
-    else hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, GK, false>), grid, block, 0, a.stream, a, per_group); \
+    if (a.dtype == 0) hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, WAVES, GK, true>), grid, block, 0, a.stream, a, per_group); \
+    else hipLaunchKernelGGL((rtn4_group_linear_kernel<MT, NT, XR, WAVES, GK, false>), grid, block, 0, a.stream, a, per_group); \
   }
   if (a.group == 128) OQ_CASE(128)
   else if (a.group == 64) OQ_CASE(64)
@@ -351,13 +349,20 @@ hipError_t launch_rtn4_group_linear(const Rtn4GroupArgs &all) {
   // 28.4 against 42.2 us).  Up to 16 rows two win over one and four (5120 x 5120: 7.9
   // against 8.3 and 11.3 us; 2 x 30720 x 5120: 21.3 against 22.9 and 24.4 us).
   const bool wide = ((all.N + 63) / 64) * ((all.M + 31) / 32) >= 128;
+  // Where even tiles of 16 columns are a workgroup a CU at most: these, with sixteen
+  // waves up to 16 rows (1 x 1024 x 16384, groups of 64: 10.4 us, eight waves 14.4, two
+  // tiles 17.7; of K 4096 5.1, 5.0 and 6.1 us; 40 rows, eight waves: 19.4 against 26.7).
+  const bool few = ((all.N + 15) / 16) * ((all.M + 31) / 32) <= 256;
   constexpr int64_t kRows = 1 << 20;  // a launch: a grid has no more than 65535 tiles of rows
   for (int64_t m = 0; m < all.M; m += kRows) {
     Rtn4GroupArgs a = all;
     a.x = (const char *)all.x + m * all.K * (all.dtype == 0 ? 4 : 2);
     a.y = all.y + m * all.N;
     a.M = all.M - m < kRows ? all.M - m : kRows;
-    if (all.M <= 4) launch_linear<1, 2, 4>(a);
+    if (few && all.M <= 4) launch_linear<1, 1, 4, 16>(a);
+    else if (few && all.M <= 16) launch_linear<1, 1, 16, 16>(a);
+    else if (few) launch_linear<2, 1, 16>(a);
+    else if (all.M <= 4) launch_linear<1, 2, 4>(a);
     else if (all.M <= 16) launch_linear<1, 2, 16>(a);
     else if (wide) launch_linear<2, 4, 16>(a);
     else launch_linear<2, 2, 16>(a);

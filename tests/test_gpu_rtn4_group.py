@@ -81,6 +81,16 @@ def test_wide_tiles(q, M, N, K, group, bf16, scale_bf16, zeros):
 
 @pytest.mark.parametrize("zeros,scale_bf16", [(False, False), (True, True)], ids=["sym", "zeros"])
 @pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("M,N,K,group", [(1, 4130, 640, 128), (3, 4097, 320, 64), (4, 4111, 352, 32), (2, 4099, 672, 96),
+                                         (5, 4105, 256, 128), (16, 4129, 448, 64), (12, 4098, 288, 32), (9, 4150, 320, 160),
+                                         (17, 4100, 384, 128), (32, 5001, 704, 64), (20, 4321, 224, 32), (31, 8100, 480, 480)])
+def test_pairs_of_tiles(q, M, N, K, group, bf16, scale_bf16, zeros):
+    """Columns enough for two tiles a workgroup, too few for four."""
+    test_linear(q, M, N, K, group, bf16, scale_bf16, zeros)
+
+
+@pytest.mark.parametrize("zeros,scale_bf16", [(False, False), (True, True)], ids=["sym", "zeros"])
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
 @pytest.mark.parametrize("M,N,K,group", [(3, 40, 1088, 64), (12, 70, 1600, 64), (40, 70, 1344, 64), (40, 33, 1312, 32),
                                          (4, 5, 1952, 32), (2, 37, 3232, 3232), (20, 35, 2592, 288)])
 def test_half_steps(q, M, N, K, group, bf16, scale_bf16, zeros):
