@@ -270,16 +270,18 @@ __global__ __launch_bounds__(64 * WAVES) void rtn4_group_linear_kernel(Rtn4Group
       if (GK && (32 * d + 32) % (GK ? GK : 1)) continue;
       left -= 32;
       if (GK || left == 0 || c + 32 == end) {  // the group's end, or the wave's
-        // (STRAIGHT: a group behind K counts nothing)
-        float by[NT];
-#pragma unroll
-        for (int t = 0; t < NT; t++) by[t] = !STRAIGHT || c < end ? scale[t] : 0.f;
 #pragma unroll
         for (int i = 0; i < MT; i++) {
 #pragma unroll
           for (int t = 0; t < NT; t++) {
 #pragma unroll
-            for (int e = 0; e < 4; e++) total[t][i][e] = fmaf(by[t], fmaf(off[t], sum[i][e], acc[t][i][e]), total[t][i][e]);
+            for (int e = 0; e < 4; e++) {
+              const float with = fmaf(scale[t], fmaf(off[t], sum[i][e], acc[t][i][e]), total[t][i][e]);
+              // STRAIGHT: a step's second group may lie behind K.  It is made of the row's
+              // last values, over and over, whose sums may pass the fp32 range where no
+              // group's do: the total without it, not with 0 times it.
+              total[t][i][e] = !STRAIGHT || d == 1 || c < end ? with : total[t][i][e];
+            }
             if (!GK) acc[t][i] = zero;
           }
           if (!GK) sum[i] = zero;

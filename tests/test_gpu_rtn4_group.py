@@ -128,6 +128,35 @@ def test_wide_ranges(q, M, bf16):
     _check(_np(y), _np(xd), q4, s, None, 32)
 
 
+@pytest.mark.parametrize("zeros,scale_bf16", [(False, False), (True, True)], ids=["sym", "zeros"])
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("M,N,group", [(1, 70, 64), (3, 4130, 64), (12, 70, 64), (12, 4130, 64), (40, 70, 64),
+                                       (40, 2100, 64), (3, 70, 32), (12, 4130, 128), (40, 70, 96), (3, 4130, 96)])
+def test_large_numbers_at_the_end(q, M, N, group, bf16, scale_bf16, zeros):
+    """The last 16 bytes of a row up to the stated range (a group's |x| below 2^122),
+    where K ends within a step of 128: what the step reads behind K counts nothing.
+    Sums hold x (16 + nibble) and x (16 + z), as the header says, so each order of
+    summing them is off by at most K u of |s| |x| (16 + nibble + 16 + z), where a
+    column's weights at the end may all be 0; the rest as at the top."""
+    say("rtn4 group large end", M, N, group, bf16, scale_bf16, zeros)
+    for K in (group * 3, group * 17):
+        rng = np.random.default_rng([M, K])
+        x = rng.standard_normal((M, K)).astype(np.float32)
+        last = 8 if bf16 else 4
+        x[:, -last:] = 2.0 ** 121 / last
+        q4, _, z = _weights(rng, N, K, group, zeros, scale_bf16)
+        s = _dev(np.full((N, K // group), 2.0 ** -40, np.float32), scale_bf16)
+        xd = _dev(x, bf16)
+        y = q.rtn4_group_linear(xd, to_device(q4), s, z)
+        x = _np(xd)
+        w, _ = ref.group_weights(q4, _np(s), None if z is None else _np(z), group)
+        n = np.stack((q4 & 15, q4 >> 4), -1).reshape(N, K)
+        mag = 2.0 ** -40 * (32.0 + n + (8.0 if z is None else np.repeat(_np(z), group, 1)))
+        want, e = x @ w.T, (np.abs(x) @ mag.T) * (K + 8) * ref.U
+        err, tol = np.abs(_np(y) - want), e + 2.0 ** -8 * (np.abs(want) + e)
+        assert np.all(err <= tol), float(np.max(err / tol))
+
+
 @pytest.mark.parametrize("M", [1, 3, 20])
 def test_not_finite(q, M):
     """A row with a NaN or an infinity does not reach the others."""
