@@ -133,6 +133,13 @@ __global__ __launch_bounds__(64 * WAVES) void rtn4_group_linear_kernel(Rtn4Group
     return r * C + (XR == 4 ? c ^ 4 * r : F32 ? c ^ 2 * (r / 2 & 3) : c ^ (r / 4 & 3));
   };
   const int x_row = XR == 4 ? col & 3 : col;
+  // Between one lane's writes and another's reads of the wave's LDS, both ways: the
+  // hardware keeps a wave's LDS operations in their order, this keeps the compiler to it
+  // (no instruction of its own).
+  const auto turn = [] {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
 
   u32x4 w[NT], x[XS][XL];
   uint32_t sr[2][NT], zr[2][NT];  // scales and zeros of 16 rows x 4 groups, and of the next 4
@@ -208,6 +215,7 @@ __global__ __launch_bounds__(64 * WAVES) void rtn4_group_linear_kernel(Rtn4Group
     u32x4 q[NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) w_swap[64 * t + w_put] = w[t];
+    turn();
 #pragma unroll
     for (int t = 0; t < NT; t++) q[t] = w_swap[64 * t + w_get];
     load_w(s + 1 < s1 ? s + 1 : s);
@@ -224,8 +232,10 @@ __global__ __launch_bounds__(64 * WAVES) void rtn4_group_linear_kernel(Rtn4Group
       const int c = s * 128 + 32 * d;
       if (!STRAIGHT && GK != 128 && c >= end) break;
       if (d % XD == 0) {
+        turn();
 #pragma unroll
         for (int j = 0; j < XL; j++) x_swap[x_place(R * j + lane / C, lane % C)] = x[d / XD % XS][j];
+        turn();
         load_x(s, d / XD + XS);
       }
       const bool fresh = GK && 32 * d % (GK ? GK : 1) == 0;
