@@ -72,12 +72,17 @@ __global__ __launch_bounds__(SPLIT ? 1024 : 256) void kv_join_kernel(KvLaunch p)
         for (int e = 0; e < 8; e++) v += x[e];
       }
     }
-    if (SPLIT) __syncthreads();  // the row before is read
+    // lanes exchange their sums, without SPLIT within the wave: the hardware keeps its LDS
+    // operations in their order, the fence keeps the compiler to it
+    const auto turn = [] {
+      if (SPLIT) __syncthreads();
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    };
+    turn();  // the row before is read
     *(f32x4 *)&sums[wave][4 * lane] = v;
     if (lane == 0) waves[wave] = f32x2{top, sum};
-    if (SPLIT) __syncthreads();
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    turn();
     if (SPLIT && wave != 0) continue;
     if (lane < q4) {
       v = f32x4{0.f, 0.f, 0.f, 0.f};

@@ -258,7 +258,11 @@ __global__ __launch_bounds__(256, 2) void kv_rows_kernel(KvLaunch p) {
         for (int j = 0; j < NL; j++)
           if (kv_nan(cur.ks[i][j]) || (cur.missing >> (16 * i + col) & 1)) cur.ks[i][j] = 255;
     }
-    // values into the wave's LDS rows
+    // values into the wave's LDS rows: behind the reads of the step before, as these are
+    // of other lanes' writes (the hardware keeps a wave's LDS operations in their order,
+    // the fences keep the compiler to it)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < NV; i++) {
       const int x = lane + 64 * i, tok = x / NB, blk = x % NB;
@@ -267,7 +271,7 @@ __global__ __launch_bounds__(256, 2) void kv_rows_kernel(KvLaunch p) {
         for (int c = 0; c < 4; c++)
           *(bf16x8 *)(rows + tok * ROWB + 64 * blk + 16 * (c ^ (tok & 3))) = fp4x8(cur.v[i][c], kv_scale(cur.vs[i]));
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 
     f32x4 s[2 * TS];
