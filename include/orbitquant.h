@@ -481,7 +481,7 @@ int64_t oq_mx_kv_attention_workspace(int64_t q_tokens, int q_heads, int kv_heads
  *     window > 0 (which needs OQ_ATTN_CAUSAL) of these the last `window`.  A
  *     query that sees none gets zeros (and lse -infinity)
  *   lse: device fp32 [q_tokens][q_heads], ln sum_j p_j; may be NULL
- *   scale: finite
+ *   scale: |scale| <= 2^127
  *   workspace: device, 16-byte aligned, at least oq_mx_kv_attention_workspace
  *     bytes, not shared with other work in flight; its contents before and after
  *     do not matter

@@ -1248,7 +1248,8 @@ int oq_mx_kv_attention(const void *q, int dtype, int64_t q_tokens, int q_heads, 
                        int64_t table_pages, float scale, uint32_t flags, int window, void *out,
                        int64_t out_token, int64_t out_head, float *lse, void *workspace,
                        int64_t workspace_bytes, void *stream) {
-  if (!is_dtype(dtype) || (flags & ~OQ_ATTN_CAUSAL) || !std::isfinite(scale)) return OQ_EINVAL;
+  if (!is_dtype(dtype) || (flags & ~OQ_ATTN_CAUSAL)) return OQ_EINVAL;
+  if (!(std::fabs(scale) <= 0x1p127f)) return OQ_EINVAL;  // times log2 e it has to stay finite
   const bool causal = (flags & OQ_ATTN_CAUSAL) != 0;
   if (window < 0 || (window > 0 && !causal)) return OQ_EINVAL;
   int rc = check_attention_shape(q_tokens, q_heads, kv_heads, head_dim, batch, page_size, table_pages);

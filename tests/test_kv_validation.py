@@ -117,6 +117,18 @@ def test_kv_attention():
         assert call(**kw) == q.OQ_OK
 
 
+@pytest.mark.parametrize("scale", [2.0 ** 127 * 1.5, -3.4e38])
+def test_kv_attention_scale(scale):
+    """A scale that passes the fp32 range in base 2 (times log2 e) is refused: it would make a score of
+    0 a NaN."""
+    call = _caller("oq_mx_kv_attention", dict(
+        q=A, dt=1, tokens=4, qh=4, qt=256, qs=64, kc=B, ksc=B + 0x1000000, vc=C, vsc=C + 0x1000000, pages=8, kh=2,
+        page=16, hd=64, batch=4, lengths=D, starts=None, table=E, width=2, scale=0.125, flags=1, window=0, out=F,
+        ot=256, os=64, lse=G, ws=H, wsb=1 << 28, stream=None))
+    assert call(scale=scale) == q.OQ_EINVAL
+    assert call(scale=scale, tokens=0) == q.OQ_EINVAL
+
+
 def test_kv_attention_workspace():
     size = q.lib().oq_mx_kv_attention_workspace
     for args in ((1, 4, 3, 64, 1, 16, 1), (1, 4, 2, 48, 1, 16, 1), (-1, 4, 2, 64, 1, 16, 1), (1, 4, 2, 64, 1, 0, 1),
