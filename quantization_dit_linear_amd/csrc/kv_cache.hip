@@ -18,7 +18,7 @@ namespace {
 // is 8 elements: chunk i % chunks of head i / chunks % heads of a token.
 template <class T>
 __global__ __launch_bounds__(256) void kv_write_kernel(KvWriteArgs a, int group, FastDiv chunks,
-                                                       FastDiv row_chunks, FastDiv page) {
+                                                       FastDiv row_chunks) {
   const bool second = blockIdx.y != 0;
   const T *x = (const T *)(second ? a.v : a.k);
   const int64_t x_token = second ? a.v_token : a.k_token, x_head = second ? a.v_head : a.k_head;
@@ -35,6 +35,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvWriteArgs a, int group,
       if (slot < 0 || slot >= slots) continue;  // the four lanes of a block agree
       float v[8];
       load8(x + (t0 + t) * x_token + h * x_head + 8 * c, v);
+      // (in 64 bits: a cache may have more slots than 2^32)
       const int64_t p = slot / a.cache.page, r = slot - p * a.cache.page;
       mx_store8<0>(v, ((p * a.cache.heads + h) * a.cache.page + r) * chunks.d + c, codes, scales);
     }
@@ -50,11 +51,11 @@ hipError_t launch_kv_write(const KvWriteArgs &a) {
   if (group < 1 || a.tokens < 1024 * group) group = 1;
   const int64_t gx = (a.tokens + group - 1) / group;
   const dim3 grid((unsigned)(gx < (1 << 20) ? gx : 1 << 20), 2);
-  const FastDiv c((uint32_t)chunks), r((uint32_t)row), p((uint32_t)a.cache.page);
+  const FastDiv c((uint32_t)chunks), r((uint32_t)row);
   if (a.dtype == 0)
-    hipLaunchKernelGGL((kv_write_kernel<float>), grid, dim3(256), 0, a.stream, a, (int)group, c, r, p);
+    hipLaunchKernelGGL((kv_write_kernel<float>), grid, dim3(256), 0, a.stream, a, (int)group, c, r);
   else
-    hipLaunchKernelGGL((kv_write_kernel<uint16_t>), grid, dim3(256), 0, a.stream, a, (int)group, c, r, p);
+    hipLaunchKernelGGL((kv_write_kernel<uint16_t>), grid, dim3(256), 0, a.stream, a, (int)group, c, r);
   return hipGetLastError();
 }
 
