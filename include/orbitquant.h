@@ -486,11 +486,16 @@ int64_t oq_mx_kv_attention_workspace(int64_t q_tokens, int q_heads, int kv_heads
  *     bytes, not shared with other work in flight; its contents before and after
  *     do not matter
  * fp32 statistics and sums.  bf16 queries: the products' operands are the bf16
- * values (the cache's are exact in bf16) and weights p rounded to bf16; fp32
- * queries keep fp32 accuracy.  Scores must be finite in fp32; a row with a NaN
- * among its query or the keys or values it sees is NaN, tokens that it does not
- * see do not reach it.  Scale bytes 253 to 255 read as NaN here (the writer
- * makes none but 255), and values below 2^-126 may count as 0.
+ * values (the cache's are exact in bf16) and weights p rounded to bf16 (by 2^-8 of
+ * each at most; their sum is of the fp32 ones); fp32 queries keep fp32 accuracy.
+ * Scores q k_j, the sums that make them and scale q k_j log2 e must be finite in
+ * fp32, and so must the sums of p_j |v_j|, in which p_j may be up to 2^8: values
+ * below 2^119 / (tokens that a row sees) always are.  A row with a NaN in its query
+ * or in a key that it sees is NaN, its lse too.  A block of 32 values with a NaN
+ * makes these 32 elements NaN in the rows that see its token; their lse stays as it
+ * is.  Tokens that a row does not see do not reach it.  Scale bytes 253 to 255 read
+ * as NaN here (the writer makes none but 255), and values below 2^-126 may count as
+ * 0.
  * A call gives the same bits every time; the order of a row's sums is chosen by
  * the sizes.  q_tokens * q_heads / kv_heads up to 2^27, batch up to 2^20,
  * table_pages * page_size up to 2^30.  q_tokens = 0 or batch = 0 no-op.

@@ -116,3 +116,28 @@ def test_one_long_sequence_among_many_short_ones(q, starts, hd, page, bf16):  # 
     if starts:
         counts[39], counts[41] = 0, 2
     _check(q, 5, lengths, counts, 2, 1, hd, page, True, 0, bf16, True, starts)
+
+
+@pytest.mark.parametrize("bf16", [False, True], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("n", [1, 9, 130])
+def test_large_values(q, n, bf16):  # noqa: F811
+    """Values up to the stated range, 2^119 over the tokens that a row sees: here 64 of them,
+    6 times 2^110 at most, all of one sign where the sums are largest.  And tiny ones, 2^-100."""
+    import torch
+    say("kv sizes large values", n, bf16)
+    rng = np.random.default_rng([20, n])
+    for codes, s in ((None, 127 + 110), (0x77, 127 + 110), (None, 127 - 100)):
+        cache, _ = _cache(q, rng, 4, 2, 16, 64)
+        cache[3][:] = s
+        if codes is not None:
+            cache[2][:] = codes  # 6 times the scale everywhere
+        dev = q.KVCache(*(torch.from_numpy(t).cuda() for t in cache))
+        table = np.array([[2, 0, 3, 1]], np.int32)
+        qd = _queries(rng, (n, 4, 64), bf16)
+        out = q.mx_kv_attention(qd, dev, torch.tensor([64], dtype=torch.int32, device="cuda"),
+                                table=torch.from_numpy(table).cuda())
+        k, v = ref.cache_values(*cache[:2]), ref.cache_values(*cache[2:])
+        want, tol, _, _ = ref.attention(_np(qd), ref.rows_of(k, table, 0, 64), ref.rows_of(v, table, 0, 64),
+                                        np.float64(np.float32(64 ** -0.5)), False, 0, bf16)
+        err, tol = np.abs(_np(out) - want), tol + ref.half_step(bf16) * (np.abs(want) + tol)
+        assert np.all(err <= tol), float(np.max(err / np.maximum(tol, 1e-300)))
