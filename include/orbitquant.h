@@ -394,7 +394,9 @@ int oq_rope(const void *x, int dtype, int64_t tokens, int heads, int head_dim, i
  *   zeros:      scale = hi / 15 - lo / 15 with hi = max(w, 0), lo = min(w, 0),
  *               zero = rint(-lo / scale), nibble = rint(w / scale) + zero in [0, 15]
  * in fp32 (IEEE division, ties to even), with the scale already rounded to
- * scale_dtype; a scale of 0 gives the nibble that stands for 0 (8, or zero = 0).
+ * scale_dtype; nibbles past 0 or 15 (by the scale's rounding) are 0 or 15; a scale
+ * of 0 gives the nibble that stands for 0 (8, or zero = 0).  A NaN or an infinity
+ * gives its group unspecified nibbles, scale and zero, and no error.
  *   W: device, fp32 or bf16 [n_out][d_in] (4-byte aligned)
  *   q4: device [n_out][d_in / 2] (16-byte aligned), the even coordinate in the
  *       low nibble; scales, zeros: device, scale_dtype [n_out][d_in / group]
@@ -497,7 +499,9 @@ int64_t oq_mx_kv_attention_workspace(int64_t q_tokens, int q_heads, int kv_heads
  * as NaN here (the writer makes none but 255), and values below 2^-126 may count as
  * 0.
  * A call gives the same bits every time; the order of a row's sums is chosen by
- * the sizes.  q_tokens * q_heads / kv_heads up to 2^27, batch up to 2^20,
+ * the sizes, as is the kernel that takes the call: by a sequence's rows on average
+ * (queries times heads of a key head), so that single tokens beside a long prompt
+ * are faster in a call of their own.  q_tokens * q_heads / kv_heads up to 2^27, batch up to 2^20,
  * table_pages * page_size up to 2^30.  q_tokens = 0 or batch = 0 no-op.
  * Errors: OQ_EINVAL, OQ_EUNSUPPORTED, OQ_EDEVICE. */
 int oq_mx_kv_attention(const void *q, int dtype, int64_t q_tokens, int q_heads, int64_t q_token,
