@@ -145,6 +145,8 @@ __global__ __launch_bounds__(256) void kv_join_wide_kernel(KvLaunch p) {
 // against 137 us, 128 rows 142 against 142; 8 of 4096 tokens 46 against 49 and 65
 // against 53 us; one of 32760 tokens 47 against 67 and 71 against 70 us; 6 of 2040
 // tokens with heads of 64 in fp32 54 against 27 us and 32 against 30.
+// One kernel takes the whole call: 63 single tokens (over up to 8192) beside a prompt of
+// 4096, 32 query and 8 key heads, 555 us, as two calls 56 and 254 us.
 constexpr int kWide = 64;
 
 // Groups (a tile of rows and a head) up to which their many parts are joined by the
@@ -173,11 +175,20 @@ Plan plan(int dtype, int64_t q_tokens, int q_heads, int kv_heads, int head_dim, 
   // Even shares of the steps while the tiles are few enough to be counted by every
   // wave: eight waves a CU, or two workgroups of them where the groups are so few that
   // each is cut into many parts (fewer parts to join: one token over 32760 24.3
-  // against 26 us).
+  // against 26 us).  Beyond 1024 tiles a wave takes a group.  One token of each of n
+  // sequences, 8 query heads a key head, shared out against a wave a group: n = 256 up to
+  // 4096 tokens, one key head, 36 against 92 us, up to 512 tokens 24 against 18; n = 1100
+  // 52 against 23 us (up to 512) and 104 against 121 us (up to 4096), with 8 key heads 170
+  // against 96 and 570 against 531; n = 4000 197 against 43 and 399 against 262 us.  What
+  // it does not even out: one of 32768 among 1099 of up to 512 tokens, 90 against 652 us.
   const int64_t units = r.tiles * kv_heads * (capacity / r.step + 8);
   r.workers = r.tiles <= 1024 && units < (int64_t)1 << 30 ? 2048 : 0;
   r.team = r.workers && r.tiles * kv_heads <= kFew;
   if (r.team) r.workers /= 4;
+  // The tiles kernel up to 1024 groups, four a CU: 1560 x 32760, 40 heads (280) 1150
+  // against 1950 us; a causal prompt of 2048 tokens, 8 key heads of 4 (264) 80 against 73,
+  // of 4096 (520) 255 against 247, of 8192 (1032) 948 against 728 us, all tokens seen 1057
+  // against 1046.
   if (r.wide) r.team = false, r.workers = r.workers && r.tiles * kv_heads <= 1024 ? 256 : 0;
   return r;
 }

@@ -16,8 +16,12 @@
 // 16-byte pieces are swizzled by the token so that neither side conflicts.
 //
 // Bound by the cache's bytes where sequences are many: 64 of up to 8192 tokens (32
-// query, 8 key heads of 128, 295 MB) 59 us and 6 us for the join, 5.0 TB/s; by
-// latency where they are few: one of 32760 tokens 17 and 7 us.
+// query, 8 key heads of 128, 295 MB) 54 us and 6 us for the join, 5.4 TB/s; by
+// latency where they are few: one of 32760 tokens 17 and 7 us.  By the parts between
+// both: 8 of 4096 tokens with 16 rows a key head 40 us, three steps a wave, of which each
+// leaves a part of 8 KB.  fp32 heads of 128 (27 registers), 224 (68) and 256 (95) and bf16
+// heads of 224 (10) and 256 (26) spill: the 64 sequences 80 us in fp32, with heads of 256
+// 153 us in bf16 (twice the bytes) and 290 us in fp32.
 #include <hip/hip_runtime.h>
 
 #include "kv_attention.h"
@@ -346,6 +350,8 @@ __global__ __launch_bounds__(256, 2) void kv_rows_kernel(KvLaunch p) {
       v[e] = __builtin_amdgcn_exp2f(fmaf(v[e], p.log2_scale, -base));
       l += v[e];
     }
+    // bf16 queries: weights rounded to bf16 (by 2^-8 of each at most), one product instead
+    // of three; their sum l is of the fp32 ones
     bf16x8 pf[TS][NQ];
 #pragma unroll
     for (int h = 0; h < TS; h++) split8<NQ>(v + 8 * h, pf[h]);

@@ -11,8 +11,9 @@
 // share a head, so its sum is log2 G lane exchanges.  The weights lie in LDS: held in
 // registers they are a chain of loads at every workgroup's start and a choice between
 // the two sides for every element.  Measured: 32760 tokens x (40 + 40) heads x 128 bf16
-// 272 us (4.9 TB/s; weights in registers 300 us); 5003 tokens x (16 + 4) heads x 96
-// fp32, half-split, 17.4 us (25.7 us); one token 4.1 us (6.0 us).  Two passes' loads at
+// 272 us (weights in registers 300 us; in a row of calls 265 us, 5.1 TB/s); 5003 tokens x
+// (16 + 4) heads x 96 fp32, half-split, 17.4 us (25.7 us; traced alone 21 us, in a row of
+// calls 16.7 us); one token 4.1 us (6.0 us).  Two passes' loads at
 // once against one, three and four: 272, 277, 278, 307 us.
 #include <hip/hip_runtime.h>
 

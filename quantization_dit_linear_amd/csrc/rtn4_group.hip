@@ -28,7 +28,9 @@ __device__ __forceinline__ void store_scale(void *p, int dtype, int64_t i, float
   else ((float *)p)[i] = v;
 }
 
-// Eight lanes a group: each holds every eighth 8-element piece of it.
+// Eight lanes a group: each holds every eighth 8-element piece of it, read twice (the
+// second time from cache), one element a load.  Runs once for a weight, so no more was
+// done: 30720 x 5120 in groups of 64, bf16 309 us, fp32 544 us (1.3 TB/s).
 __global__ __launch_bounds__(256) void rtn4_group_prepare_kernel(const void *__restrict__ W, int dtype,
                                                                  int64_t groups, int group,
                                                                  uint32_t *__restrict__ q4,
@@ -82,9 +84,11 @@ __global__ __launch_bounds__(256) void rtn4_group_prepare_kernel(const void *__r
 // own) the same kernel is held by address processing: 2 x 30720 x 5120 with zeros in 45
 // instead of 30 us, 16 rows of 30720 x 5120 in 45 instead of 24 us.
 //
-// 1 x 5120 x 5120: 7.1 us; 1 x 32768 x 16384: 57 us (4.7 TB/s); 2 x 30720 x 5120,
-// groups of 64 with zeros in fp32: 27 us; 29 fp32 rows x 13824 x 5120, groups of 32: 35 us,
-// half of it vector instructions (the parts, the nibbles, the groups' ends).
+// Launches of a graph, groups of 128 in bf16 where not said otherwise: 1 x 5120 x 5120
+// 6.4 us; 1 x 32768 x 16384 55.6 us (5.0 TB/s); 2 x 30720 x 5120, groups of 64 with zeros,
+// 24 us; 29 fp32 rows x 13824 x 5120, groups of 32, 32.5 us, half of it vector instructions
+// (the parts, the nibbles, the groups' ends); 64 rows x 30720 x 5120 59 us and 512 rows
+// 421 us: 32 rows a tile, each of which converts the weights again.
 //
 // GK: the group where it is 32, 64 or 128 (its products are known then, and the first
 // starts from zero: 34.8 against 38.5 us for the 29 rows, 7.1 against 7.6 for one), else
@@ -356,14 +360,15 @@ hipError_t launch_rtn4_group_prepare(const void *W, int dtype, int64_t rows, int
 
 hipError_t launch_rtn4_group_linear(const Rtn4GroupArgs &all) {
   // Four tiles of columns share what a tile of x costs, two make twice the workgroups:
-  // four win from 128 of them on (64 rows of 5120 x 5120, 160: 15.2 against 19.0 us;
-  // 29 x 13824, 216: 16.7 against 20.0 us), two below (32 rows of 5120 x 13824, 80:
-  // 28.4 against 42.2 us).  Up to 16 rows two win over one and four (5120 x 5120: 7.9
+  // four win from 128 of them on (64 rows of 5120 x 5120, 160: 13.2 against 17.2 us;
+  // 29 x 13824, 216: 14.7 against 18.7 us; not yet at 128 itself: 40 rows of 4096 x 16384
+  // 34.8 against 24.7 us), two below (32 rows of 5120 x 13824, 80: 21.8 against 30.4
+  // us).  Up to 16 rows two win over one and four (5120 x 5120: 7.9
   // against 8.3 and 11.3 us; 2 x 30720 x 5120: 21.3 against 22.9 and 24.4 us).
   const bool wide = ((all.N + 63) / 64) * ((all.M + 31) / 32) >= 128;
   // Where even tiles of 16 columns are a workgroup a CU at most: these, with sixteen
-  // waves up to 16 rows (1 x 1024 x 16384, groups of 64: 10.4 us, eight waves 14.4, two
-  // tiles 17.7; of K 4096 5.1, 5.0 and 6.1 us; 40 rows, eight waves: 19.4 against 26.7).
+  // waves up to 16 rows (1 x 1024 x 16384, groups of 64: 9.8 us, eight waves 14.4, two
+  // tiles 17.6; of K 4096 4.7, 5.0 and 6.3 us; 40 rows, eight waves: 19.0 against 26.7).
   const bool few = ((all.N + 15) / 16) * ((all.M + 31) / 32) <= 256;
   constexpr int64_t kRows = 1 << 20;  // a launch: a grid has no more than 65535 tiles of rows
   for (int64_t m = 0; m < all.M; m += kRows) {
